@@ -533,6 +533,131 @@ mla_status_t mla_gather_up_project(const mla_tensor_t* k_out, const mla_tensor_t
                                    const uint32_t* buffer_row_offsets, const uint32_t* cache_offsets,
                                    uint32_t kv_lora_rank, uint32_t* status, mla_stream_t stream);
 
+/*
+ * ---- The serving step around the attention, with 8-bit data ----
+ * (No counterpart on the reference pages, which stop at the prefill.)  A step
+ * for new tokens: mla_rms_norm of the hidden states, mla_matmul_fp8 with the
+ * projections' weights, mla_append_latent of the new latent rows,
+ * mla_decode_latent over the cache.  A prompt over an 8-bit cache: mla_gather_rows,
+ * mla_matmul_fp8 with the up-projection weights (one scale per row: x_scales
+ * with column stride 0), then the prefill calls above.
+ * Outputs must not overlap inputs or each other unless a call says so.
+ */
+
+/*
+ * Root-mean-square norm of the rows of x, with an optional residual and an
+ * 8-bit output:
+ *   h = x + residual (x without one),  residual_out = bf16(h)
+ *   y = h * weight / sqrt(mean over the row of h^2 + eps)
+ *   out = bf16(y);  out_scales[r, g] = max(amax over columns 128 g .. 128 g +
+ *   127 of |y|, 1e-30) / 448,  out_fp8 = e4m3(y / out_scales)
+ * h, its mean square and y are 32-bit: y does not pass through the rounding
+ * of residual_out.  A row with a NaN gives NaN scales and codes.
+ *   x             device bf16 [rows, D], 1 <= D <= 32768
+ *   residual      device bf16 [rows, D] or NULL
+ *   residual_out  device bf16 [rows, D] (written) or NULL; needs residual
+ *   weight        device bf16 or float32 [D]
+ *   out           device bf16 [rows, D] (written) or NULL
+ *   out_fp8       device e4m3 [rows, D] (written) or NULL
+ *   out_scales    device float32 [rows, ceil(D / 128)] (written), with out_fp8
+ *   eps           finite, >= 0
+ * At least one of out and out_fp8.  Rows may have any stride >= D (outputs; an
+ * input's may be less) and any alignment of their type; rows that all start
+ * 16-byte aligned (out_fp8: 8-byte) take wide accesses.  residual_out and out may
+ * each be the same view as x or as residual (in place), but not each other's.
+ * One launch.
+ */
+mla_status_t mla_rms_norm(const mla_tensor_t* out, const mla_tensor_t* out_fp8,
+                          const mla_tensor_t* out_scales, const mla_tensor_t* x,
+                          const mla_tensor_t* residual, const mla_tensor_t* residual_out,
+                          const mla_tensor_t* weight, float eps, mla_stream_t stream);
+
+/*
+ * Matrix product of 8-bit operands with a scale per block of 128:
+ *   out[m, n] = sum over kb of x_scales[m, kb] * w_scales[n / 128, kb] *
+ *               sum over k in [128 kb, 128 kb + 128) of x[m, k] * w[n, k]
+ *   out       device bf16 or float32 [M, N] (written), any row stride >= N
+ *   x         device e4m3 [M, K]; K a multiple of 16
+ *   x_scales  device float32 [M, ceil(K / 128)], any strides >= 0 (column
+ *             stride 0: one scale per row)
+ *   w         device e4m3 [N, K] (nn.Linear layout)
+ *   w_scales  device float32 [ceil(N / 128), ceil(K / 128)], any strides >= 0
+ *   status    device uint32 or NULL: MLA_DEVICE_STATUS_TIMEOUT is ORed in if a
+ *             pipeline wait of the kernel gives up
+ * Rows of x and w start 16-byte aligned.  Every sum is 32-bit; one rounding,
+ * of the output.  The result does not depend on timing (no atomics).
+ */
+mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor_t* x,
+                            const mla_tensor_t* x_scales, const mla_tensor_t* w,
+                            const mla_tensor_t* w_scales, uint32_t* status, mla_stream_t stream);
+
+/*
+ * Append of new latent rows to a paged 8-bit cache.  Row row_offsets[b] + i
+ * of `rows` becomes context token a = cache_lens[b] + i of sequence b:
+ *   scale = max(amax |row|, 1e-30) / 448
+ *   cache[page_table[b, a / P], a % P, :] = e4m3(row / scale)
+ *   cache->scale[page_table[b, a / P] * P + a % P] = scale
+ * (a row with a NaN gets a NaN scale).
+ *   cache        device e4m3 [num_pages, P, W] (written), with per-token scales
+ *                (scale_gran MLA_SCALE_PER_TOKEN, [num_pages * P] floats,
+ *                written although the descriptor's pointer is const); W a
+ *                multiple of 16 up to 1024, strides multiples of 16 bytes
+ *   rows         device bf16 [Tq, W], e.g. [c_kv 512 | k_rope 64]
+ *   page_table   device uint32 [B, max_pages]
+ *   row_offsets  device uint32 [B + 1], non-decreasing; rows outside
+ *                [row_offsets[0], row_offsets[B]) are not read into the cache
+ *   cache_lens   device uint32 [B], tokens cached before this call
+ *   status       device uint32 or NULL: an out-of-range page id or page-table
+ *                column skips that row and ORs MLA_DEVICE_STATUS_BAD_PAGE /
+ *                _BAD_COLUMN into *status
+ * Slots no new token lands on keep their contents.  Two tokens of one call
+ * must not land on the same slot (sequences that share a page they both append
+ * to); which one stays would be undefined.  The rope columns and the scales
+ * are what the fp8 prefill calls take as a paged K_rope.  One launch.
+ */
+mla_status_t mla_append_latent(const mla_tensor_t* cache, const mla_tensor_t* rows,
+                               const mla_tensor_t* page_table, const uint32_t* row_offsets,
+                               const uint32_t* cache_lens, uint32_t* status, mla_stream_t stream);
+
+/* Bytes of device workspace mla_decode_latent needs, whatever its sizes. */
+size_t mla_decode_latent_workspace_size(void);
+
+/*
+ * Attention of new tokens over a paged 8-bit latent cache: MLA in its absorbed
+ * form, where each head's query is already in the latent space and all heads
+ * share the cached rows.  With c_j the dequantised cache row (code * scale) of
+ * context token j of sequence b, for head h of query row_offsets[b] + i:
+ *   x_j = scale * dot(q[row_offsets[b] + i, h, 0:576], c_j)
+ *   out[row_offsets[b] + i, h, :] = sum over j of softmax(x)_j * c_j[0:512]
+ *   lse[row_offsets[b] + i, h]    = ln sum over j of exp(x_j)
+ * over the keys the mask leaves visible (causal: j <= cache_lens[b] + i; null:
+ * j < cache_lens[b] + n_b), n_b = row_offsets[b + 1] - row_offsets[b].  The new
+ * tokens' own rows are in the cache already (mla_append_latent).
+ *   out          device bf16 [Tq, H, 512] (written)
+ *   lse          device float32 [Tq, H] (written) or NULL
+ *   q            device bf16 [Tq, H, 576]; 1 <= H <= 1024
+ *   cache        device e4m3 [num_pages, P, 576], pages contiguous (page
+ *                stride = P x token stride), token stride a multiple of 16
+ *                bytes; scales per token ([num_pages * P] floats) or one for all
+ *   page_table   device uint32 [B, max_pages], B <= 16384
+ *   row_offsets, cache_lens, scale, mask  as in mla_prefill_ragged
+ *   status       device uint32 or NULL: an out-of-range page id or page-table
+ *                column ORs MLA_DEVICE_STATUS_BAD_PAGE / _BAD_COLUMN and its
+ *                keys count as masked; a pipeline wait that gives up ORs
+ *                MLA_DEVICE_STATUS_TIMEOUT
+ *   workspace    device, mla_decode_latent_workspace_size() bytes, 256-byte
+ *                aligned; its contents before the call do not matter.  Calls
+ *                that may overlap on the GPU need distinct workspaces.
+ * Slots past a sequence's context may hold anything.  A query all of whose
+ * keys are masked gets 0 and lse -inf.  Rows outside [row_offsets[0],
+ * row_offsets[B]) are not written.
+ */
+mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                               const mla_tensor_t* cache, const mla_tensor_t* page_table,
+                               const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
+                               mla_mask_t mask, uint32_t* status, void* workspace,
+                               size_t workspace_bytes, mla_stream_t stream);
+
 /* Device status bits written into the workspace's first uint32. */
 #define MLA_DEVICE_STATUS_BAD_PAGE 0x1u    /* page id >= num_pages */
 #define MLA_DEVICE_STATUS_BAD_COLUMN 0x2u  /* context needs more pages than max_pages */

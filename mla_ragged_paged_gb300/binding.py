@@ -28,7 +28,8 @@ EXPORTS = ["mla_prefill_plan", "mla_prefill_plan_max_rows", "mla_prefill_ragged_
            "mla_prefill_ragged_contiguous",
            "mla_prefill_ragged_chunk_contiguous", "mla_gather_rows", "mla_up_project",
            "mla_gather_up_project",
-           "mla_prefill_ragged_split", "mla_test_inject_stall", "mla_test_delay_softmax",
+           "mla_prefill_ragged_split", "mla_rms_norm", "mla_matmul_fp8", "mla_append_latent",
+           "mla_decode_latent_workspace_size", "mla_decode_latent", "mla_test_inject_stall", "mla_test_delay_softmax",
            "mla_read_device_status",
            "mla_last_error_string"]
 
@@ -103,6 +104,17 @@ def load(path=LIB_PATH):
     lib.mla_up_project.restype = ctypes.c_int
     lib.mla_gather_up_project.argtypes = [pt, pt, pt, pt, pt, pt, vp, vp, u32, vp, vp]
     lib.mla_gather_up_project.restype = ctypes.c_int
+    lib.mla_rms_norm.argtypes = [pt, pt, pt, pt, pt, pt, pt, ctypes.c_float, vp]
+    lib.mla_rms_norm.restype = ctypes.c_int
+    lib.mla_matmul_fp8.argtypes = [pt, pt, pt, pt, pt, vp, vp]
+    lib.mla_matmul_fp8.restype = ctypes.c_int
+    lib.mla_append_latent.argtypes = [pt, pt, pt, vp, vp, vp, vp]
+    lib.mla_append_latent.restype = ctypes.c_int
+    lib.mla_decode_latent_workspace_size.argtypes = []
+    lib.mla_decode_latent_workspace_size.restype = ctypes.c_size_t
+    lib.mla_decode_latent.argtypes = [pt, pt, pt, pt, pt, vp, vp, ctypes.c_float, ctypes.c_int, vp, vp,
+                                      ctypes.c_size_t, vp]
+    lib.mla_decode_latent.restype = ctypes.c_int
     lib.mla_read_device_status.argtypes = [vp, ctypes.POINTER(u32), vp]
     lib.mla_read_device_status.restype = ctypes.c_int
     lib.mla_last_error_string.argtypes = []
@@ -471,6 +483,142 @@ def merge(out, partial_out, partial_lse, row_offsets, buffer_row_offsets, stream
     d_pl = describe(partial_lse, MLA_DTYPE_F32)
     _check(load().mla_prefill_merge(ctypes.byref(d_out), ctypes.byref(d_po), ctypes.byref(d_pl),
                                     _ptr(row_offsets), _ptr(buffer_row_offsets), B, _stream(stream)))
+    return out
+
+
+def _ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def _opt(t, dtype):
+    return None if t is None else describe(t, dtype)
+
+
+def _typed(t, what, *dtypes):
+    """Refuse a tensor whose elements the call would read as another type."""
+    if t is not None and t.dtype not in dtypes:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    return t
+
+
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_INDEX = (torch.int32, torch.uint32)
+
+
+def _indices(t, what, numel):
+    """A packed device array of 32-bit indices."""
+    _typed(t, what, *_INDEX)
+    if t.numel() != numel or not t.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must hold {numel} packed elements (got {tuple(t.shape)})")
+    return t
+
+
+def _same_device(*tensors):
+    """Every tensor of a call lives on the device the call launches on."""
+    tensors = [_on_device(t) for t in tensors if t is not None]
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != dev:
+            raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on the current device cuda:{dev} (got {t.device})")
+
+
+def rms_norm(x, weight, eps, residual=None, residual_out=None, out=None, out_fp8=None, out_scales=None,
+             stream=None):
+    """mla_rms_norm: h = x + residual, residual_out = bf16(h), y = h * weight /
+    sqrt(mean(h^2) + eps) as bf16 `out` and / or e4m3 `out_fp8` with one scale
+    per 128 columns of a row in `out_scales`.  Returns the outputs given."""
+    _same_device(x, weight, residual, residual_out, out, out_fp8, out_scales)
+    bf16 = torch.bfloat16
+    for t, what in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (out, "out")):
+        _typed(t, what, bf16)
+    _typed(weight, "weight", bf16, torch.float32)
+    _typed(out_fp8, "out_fp8", *_FP8)
+    _typed(out_scales, "out_scales", torch.float32)
+    _check(load().mla_rms_norm(_ref(_opt(out, MLA_DTYPE_BF16)), _ref(_opt(out_fp8, MLA_DTYPE_FP8_E4M3)),
+                               _ref(_opt(out_scales, MLA_DTYPE_F32)), _ref(_opt(x, MLA_DTYPE_BF16)),
+                               _ref(_opt(residual, MLA_DTYPE_BF16)), _ref(_opt(residual_out, MLA_DTYPE_BF16)),
+                               _ref(describe(weight, _dtype_code(weight))), float(eps), _stream(stream)))
+    return tuple(t for t in (out, out_fp8, out_scales, residual_out) if t is not None)
+
+
+def matmul_fp8(out, x, x_scales, w, w_scales, status=None, stream=None):
+    """mla_matmul_fp8: out [M, N] (bf16 or float32) = x [M, K] x w [N, K]^T, both
+    e4m3 with a scale per row and 128 columns of x ([M, ceil(K / 128)]; an
+    expanded column is one scale a row) and per 128 x 128 block of w."""
+    _same_device(out, x, x_scales, w, w_scales, status)
+    _typed(out, "out", torch.bfloat16, torch.float32)
+    _typed(x, "x", *_FP8)
+    _typed(w, "w", *_FP8)
+    _typed(x_scales, "x_scales", torch.float32)
+    _typed(w_scales, "w_scales", torch.float32)
+    _check(load().mla_matmul_fp8(_ref(describe(out, _dtype_code(out))), _ref(describe(x, MLA_DTYPE_FP8_E4M3)),
+                                 _ref(describe(x_scales, MLA_DTYPE_F32)), _ref(describe(w, MLA_DTYPE_FP8_E4M3)),
+                                 _ref(describe(w_scales, MLA_DTYPE_F32)), _ptr(status), _stream(stream)))
+    return out
+
+
+def _latent_cache(cache, cache_scales, per_tensor):
+    """Descriptor of a paged e4m3 latent cache with its scales: one per slot
+    ([num_pages, P]), or, where allowed, a single float."""
+    _typed(cache, "cache", *_FP8)
+    _typed(cache_scales, "cache_scales", torch.float32)
+    if cache.dim() != 3:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"cache must be [num_pages, P, W] (got {tuple(cache.shape)})")
+    if per_tensor and cache_scales.numel() == 1 and cache.shape[0] * cache.shape[1] != 1:
+        return describe(cache, MLA_DTYPE_FP8_E4M3, cache_scales, MLA_SCALE_PER_TENSOR)
+    if cache_scales.numel() != cache.shape[0] * cache.shape[1] or not cache_scales.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, "cache_scales must be a packed [num_pages, P]")
+    return describe(cache, MLA_DTYPE_FP8_E4M3, cache_scales, MLA_SCALE_PER_TOKEN)
+
+
+def append_latent(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status=None, stream=None):
+    """mla_append_latent: bf16 rows [Tq, W] quantised per token into the paged
+    e4m3 cache [num_pages, P, W] and its scales [num_pages, P], at context
+    positions cache_lens[b] + i."""
+    _same_device(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status)
+    _typed(rows, "rows", torch.bfloat16)
+    _typed(page_table, "page_table", *_INDEX)
+    B = page_table.shape[0]
+    _check(load().mla_append_latent(_ref(_latent_cache(cache, cache_scales, False)),
+                                    _ref(describe(rows, MLA_DTYPE_BF16)),
+                                    _ref(describe(page_table, MLA_DTYPE_U32)),
+                                    _ptr(_indices(row_offsets, "row_offsets", B + 1)),
+                                    _ptr(_indices(cache_lens, "cache_lens", B)), _ptr(status), _stream(stream)))
+    return cache, cache_scales
+
+
+def decode_workspace_size():
+    """Workspace bytes of decode_latent, whatever its sizes."""
+    return int(load().mla_decode_latent_workspace_size())
+
+
+def alloc_decode_workspace(device="cuda"):
+    return torch.empty(decode_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, scale,
+                  mask=MLA_MASK_CAUSAL, workspace=None, lse=None, status=None, stream=None):
+    """mla_decode_latent: attention of new tokens (q [Tq, H, 576], absorbed
+    queries) over the paged e4m3 latent cache [num_pages, P, 576] with its
+    scales ([num_pages, P], or one float); out [Tq, H, 512] stays in the latent
+    space, lse [Tq, H] is optional."""
+    _same_device(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, workspace, lse, status)
+    _typed(out, "out", torch.bfloat16)
+    _typed(q, "q", torch.bfloat16)
+    _typed(lse, "lse", torch.float32)
+    _typed(page_table, "page_table", *_INDEX)
+    if workspace is None:
+        # From the launch stream's pool: its memory is not reused before the call is done.
+        with torch.cuda.stream(stream):
+            workspace = alloc_decode_workspace(q.device)
+    B = page_table.shape[0]
+    _check(load().mla_decode_latent(_ref(describe(out, MLA_DTYPE_BF16)), _ref(_opt(lse, MLA_DTYPE_F32)),
+                                    _ref(describe(q, MLA_DTYPE_BF16)), _ref(_latent_cache(cache, cache_scales, True)),
+                                    _ref(describe(page_table, MLA_DTYPE_U32)),
+                                    _ptr(_indices(row_offsets, "row_offsets", B + 1)),
+                                    _ptr(_indices(cache_lens, "cache_lens", B)), float(scale), int(mask),
+                                    _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
     return out
 
 

@@ -89,9 +89,11 @@ mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int s
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
-mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla_dtype_t dtype) {
+mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla_dtype_t dtype, bool empty_ok) {
   if (!t) return fail(MLA_ERR_INVALID_ARG, "%s descriptor is NULL", name);
-  if (!t->data) return fail(MLA_ERR_INVALID_ARG, "%s data is NULL", name);
+  bool empty = false;
+  for (int i = 0; empty_ok && i < ndim && t->ndim == ndim; ++i) empty |= t->shape[i] == 0;
+  if (!t->data && !empty) return fail(MLA_ERR_INVALID_ARG, "%s data is NULL", name);
   if (t->ndim != ndim) return fail(MLA_ERR_INVALID_ARG, "%s has ndim %d, expected %d", name, t->ndim, ndim);
   if (t->dtype != dtype)
     return fail(MLA_ERR_INVALID_ARG, "%s has dtype %d, expected %d", name, (int)t->dtype, (int)dtype);

@@ -28,8 +28,10 @@ mla_status_t encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t 
 bool aligned16(const void* ptr);
 
 // Descriptor checks: non-NULL data, rank, dtype, shapes in [0, 2^31),
-// non-negative strides, innermost stride 1.
-mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla_dtype_t dtype);
+// non-negative strides, innermost stride 1.  empty_ok: a tensor without
+// elements may have NULL data.
+mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla_dtype_t dtype,
+                          bool empty_ok = false);
 
 // Allow `bytes` of dynamic shared memory for `func` on `device`, cached per
 // (device, slot): each kernel needs a slot of its own, 0..7 (0 plan,
