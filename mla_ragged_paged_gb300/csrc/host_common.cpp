@@ -13,7 +13,8 @@ thread_local char g_error[512] = "no error";
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_num_sms[kMaxDevices];  // 0 = unknown, -1 = unsupported device
-std::atomic<int> g_smem_set[kMaxDevices][8];
+std::atomic<int> g_smem_set[kMaxDevices][kSmemSlots];
+std::atomic<int> g_regs_ok[kMaxDevices][kSmemSlots];
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -84,6 +85,18 @@ mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int s
   if (e != cudaSuccess)
     return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute(%d bytes): %s", bytes, cudaGetErrorString(e));
   cached.store(bytes, std::memory_order_relaxed);
+  return MLA_OK;
+}
+
+mla_status_t check_registers(const void* func, int regs, int device, int slot) {
+  std::atomic<int>& seen = g_regs_ok[device][slot];
+  if (seen.load(std::memory_order_relaxed)) return MLA_OK;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, func);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(e));
+  if (fa.numRegs != regs)
+    return fail(MLA_ERR_UNSUPPORTED, "kernel built with %d registers per thread, expected %d", fa.numRegs, regs);
+  seen.store(1, std::memory_order_relaxed);
   return MLA_OK;
 }
 

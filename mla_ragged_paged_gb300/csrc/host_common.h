@@ -34,8 +34,15 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
                           bool empty_ok = false);
 
 // Allow `bytes` of dynamic shared memory for `func` on `device`, cached per
-// (device, slot): each kernel needs a slot of its own, 0..7 (0 plan,
-// 1 scheduler, 2 / 3 / 4 attention bf16 / fp8 / fp8 with per-token K scales).
+// (device, slot): each kernel needs a slot of its own (0 plan, 1 scheduler,
+// 2 / 3 / 4 attention bf16 / fp8 / fp8 with per-token K scales, 6 / 7 the last
+// two with two-term precision, 5 up-projection, 8 fp8 product, 9 .. 12 its form
+// for few tokens, 13 latent decode).
+constexpr int kSmemSlots = 16;
 mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int slot);
+
+// A kernel that moves registers between its warps (setmaxnreg) may only run as
+// built with exactly `regs` registers per thread; cached per (device, slot).
+mla_status_t check_registers(const void* func, int regs, int device, int slot);
 
 }  // namespace mla

@@ -1,9 +1,29 @@
 // Matrix product of e4m3 operands with a scale per block of 128:
 //   out[m, n] = sum_kb xs[m, kb] * ws[n / 128, kb] * sum_{k in kb} x[m, k] * w[n, k]
 // (x: one scale per row and 128 columns; w: one per 128 x 128 block).
+//
+// The inner sums of one block of 128 columns run on the tensor cores
+// (tcgen05.mma kind::f8f6f4, fp32 accumulation in tensor memory); the block's
+// accumulator is then read back, multiplied by its scales and added in fp32
+// registers while the tensor cores work on the next block in the other half of
+// tensor memory.  No sum ever passes through fewer than 32 bits.
+//
+// Two kernels:
+// * matmul_tile_kernel, for products with enough output tiles to fill the
+//   GPU: persistent CTA pairs, each CTA one 128 x 256 output tile.  Bound by the
+//   tensor cores and the power limit; the pair shares its weight tile by TMA
+//   multicast, because one SM's share of the L2 cannot feed 48 KB per 512
+//   tensor-core cycles.
+// * matmul_thin_kernel, for the others (few tokens): HBM-bound on w.  The
+//   weights are the 128-row operand and the tokens the narrow one, so few rows
+//   waste no tensor time, and K is split over a cluster of up to eight CTAs whose
+//   partial sums meet in distributed shared memory, in rank order.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "host_common.h"
 #include "sm103.cuh"
@@ -11,80 +31,513 @@
 namespace mla {
 namespace {
 
+constexpr uint32_t kKB = 128;                 // columns of one scale block (bytes of one swizzle atom row)
+constexpr uint32_t kTileM = 128, kTileN = 256;
+
 struct MatmulParams {
-  const uint8_t* x;
-  const uint8_t* w;
+  CUtensorMap tm_x, tm_w;
   const float* xs;
   const float* ws;
   void* out;
-  long long x_row, w_row, xs_row, xs_col, ws_row, ws_col, out_row;
-  uint32_t M, N, K;
+  long long xs_row, xs_col, ws_row, ws_col, out_row;
+  uint32_t M, N, kblocks;
   uint32_t out_f32;
+  uint32_t access;              // bytes an output row may be stored in at once: 32, 16, or its element's
+  uint32_t m_tiles, n_tiles;    // tile kernel: m_tiles counts pairs of 128 rows
+  uint32_t* status;
 };
 
-// 64 x 64 outputs per block of 256 threads, 4 x 4 per thread.
-__global__ void __launch_bounds__(256) matmul_kernel(const MatmulParams p) {
-  __shared__ float sx[32][65], sw[32][65];
-  const uint32_t m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int lr = tid >> 2, lk = (tid & 3) * 8;  // loader: row, first of 8 columns
-  float acc[4][4] = {};
-  for (uint32_t k0 = 0; k0 < p.K; k0 += 128) {
-    float part[4][4] = {};
-    for (uint32_t k1 = k0; k1 < min(k0 + 128, p.K); k1 += 32) {
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t r = (half ? n0 : m0) + lr, lim = half ? p.N : p.M;
-        const uint8_t* base = half ? p.w + r * p.w_row : p.x + r * p.x_row;
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        if (r < lim && k1 + lk < p.K) {
-          const uint2 u = *reinterpret_cast<const uint2*>(base + k1 + lk);
-          e4m3x4_to_f32(u.x, f[0], f[1], f[2], f[3]);
-          e4m3x4_to_f32(u.y, f[4], f[5], f[6], f[7]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) (half ? sw : sx)[lk + e][lr] = f[e];
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k) {
-        float a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = sx[k][ty * 4 + i];
-          b[i] = sw[k][tx + 16 * i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(a[i], b[j], part[i][j]);
-      }
-      __syncthreads();
+// ---------------------------------------------------------------- many tiles
+constexpr int kStages = 4;
+constexpr int kTileThreads = 384;
+constexpr int kTileRegs = 168;        // what 65536 / 384 threads allows; split by setmaxnreg below
+constexpr uint32_t kXBytes = kTileM * kKB, kWBytes = kTileN * kKB;
+constexpr uint32_t kBand = 8;         // pairs of row tiles walked together, so their x stays in L2
+
+struct __align__(1024) TileSmem {
+  uint8_t x[kStages][kXBytes];
+  uint8_t w[kStages][kWBytes];
+  float stage[8][32][33];              // per accumulating warp: 32 x 32 outputs on their way to narrow stores
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+static_assert(sizeof(TileSmem) + 1024 <= 232448, "matmul tile shared memory");
+
+// Tile t: bands of kBand row pairs, inside a band the row pairs of one column
+// tile follow each other.
+__device__ __forceinline__ void tile_of(const MatmulParams& p, uint32_t t, uint32_t& m, uint32_t& n) {
+  const uint32_t per_band = kBand * p.n_tiles;
+  const uint32_t band = t / per_band, r = t - band * per_band;
+  const uint32_t rows = min(kBand, p.m_tiles - band * kBand);
+  n = r / rows;
+  m = band * kBand + (r - n * rows);
+}
+
+__device__ void tile_producer(TileSmem& s, const MatmulParams& p, uint32_t rank, volatile uint32_t* abort) {
+  const uint32_t tiles = p.m_tiles * p.n_tiles;
+  uint32_t pos = 0;
+  bool alive = true;
+  for (uint32_t t = blockIdx.x >> 1; t < tiles && alive; t += gridDim.x >> 1) {
+    uint32_t m, n;
+    tile_of(p, t, m, n);
+    const int32_t mr = static_cast<int32_t>((2 * m + rank) * kTileM);
+    const int32_t nr = static_cast<int32_t>(n * kTileN + rank * (kTileN / 2));
+    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
+      const uint32_t st = pos % kStages;
+      if (!(alive = mbar_wait(smem_u32(&s.empty[st]), ((pos / kStages) & 1u) ^ 1u, abort))) break;
+      const uint32_t bar = smem_u32(&s.full[st]);
+      mbar_arrive_expect_tx(bar, kXBytes + kWBytes);
+      const int32_t k = static_cast<int32_t>(kb * kKB);
+      tma_load_2d(smem_u32(s.x[st]), &p.tm_x, bar, k, mr);
+      // Half of the pair's weight tile, into both CTAs.
+      tma_load_2d_multicast(smem_u32(s.w[st]) + rank * (kWBytes / 2), &p.tm_w, bar, k, nr, 3);
     }
-    const uint32_t kb = k0 >> 7;
+  }
+  // Both CTAs' UMMA threads have arrived on every slot before this CTA exits.
+  for (uint32_t i = pos < kStages ? pos : kStages; i >= 1 && !*abort; --i) {
+    const uint32_t q = pos - i;
+    mbar_wait(smem_u32(&s.empty[q % kStages]), (q / kStages) & 1u, abort);
+  }
+  if (*abort) {
+    // Let the copies still in flight land before the CTA exits.
+    const uint32_t n = pos < kStages ? pos : kStages;
+    for (uint32_t i = 1; i <= n; ++i) {
+      const uint32_t q = pos - i;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(&s.full[q % kStages]), (q / kStages) & 1u))
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    }
+  }
+}
+
+__device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, volatile uint32_t* abort) {
+  const uint32_t tiles = p.m_tiles * p.n_tiles;
+  const uint32_t idesc = make_idesc(kTileM, kTileN, 0, false);  // e4m3, both K-major
+  uint32_t pos = 0;
+  bool alive = true;
+  for (uint32_t t = blockIdx.x >> 1; t < tiles && alive; t += gridDim.x >> 1) {
+    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
+      const uint32_t st = pos % kStages, buf = pos & 1u;
+      if (!(alive = mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort))) break;
+      if (!(alive = mbar_wait(smem_u32(&s.full[st]), (pos / kStages) & 1u, abort))) break;
+      tc_fence_after();
+      const uint64_t ad = sw128_desc_at(smem_u32(s.x[st])), bd = sw128_desc_at(smem_u32(s.w[st]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = m0 + ty * 4 + i;
-      const float a = m < p.M ? p.xs[m * p.xs_row + kb * p.xs_col] : 0.f;
+      for (int k = 0; k < 4; ++k) umma_f8_ss(tmem + buf * kTileN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+      umma_commit_multicast(smem_u32(&s.empty[st]), 3);
+      umma_commit(smem_u32(&s.acc_full[buf]));
+    }
+  }
+  // No UMMA may still be in flight when tensor memory is released.
+  umma_commit(smem_u32(&s.drain));
+  const uint64_t tw = global_timer_ns();
+  while (!mbar_try_wait(smem_u32(&s.drain), 0))
+    if (global_timer_ns() - tw > kWaitTimeoutNs) break;
+}
+
+// Stores 128 output columns of row m from fp32 pairs.  Rows that allow wide
+// accesses are stored by their own thread; others go through shared memory,
+// so that a warp stores 32 neighbouring columns of one row at a time.
+template <typename Stage>
+__device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, const uint64_t (&acc)[64], uint32_t m,
+                                          uint32_t n0, int lane) {
+  if (p.access >= 16) {
+    if (m >= p.M) return;
+    if (p.out_f32) {
+      float* dst = static_cast<float*>(p.out) + m * p.out_row + n0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t n = n0 + tx + 16 * j;
-        if (n < p.N) acc[i][j] = fmaf(part[i][j], a * p.ws[(n >> 7) * p.ws_row + kb * p.ws_col], acc[i][j]);
+      for (int c = 0; c < 16; ++c) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[2 * e] = static_cast<uint32_t>(acc[4 * c + e]);
+          w[2 * e + 1] = static_cast<uint32_t>(acc[4 * c + e] >> 32);
+        }
+        if (n0 + 8 * c + 8 <= p.N) {
+          if (p.access == 32) {
+            st_global_v8(dst + 8 * c, w);
+          } else {
+            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + 8 * c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n0 + 8 * c + e < p.N) dst[8 * c + e] = __uint_as_float(w[e]);
+        }
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.out_row + n0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float lo, hi;
+          f2_unpack(acc[8 * c + e], lo, hi);
+          w[e] = pack_bf16x2(lo, hi);
+        }
+        if (n0 + 16 * c + 16 <= p.N) {
+          if (p.access == 32) {
+            st_global_v8(dst + 16 * c, w);
+          } else {
+            *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (n0 + 16 * c + e < p.N) dst[16 * c + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float lo, hi;
+      f2_unpack(acc[16 * c + e], lo, hi);
+      stage[lane][2 * e] = lo;
+      stage[lane][2 * e + 1] = hi;
+    }
+    __syncwarp();
+    const uint32_t n = n0 + 32 * c + lane, m0 = m - lane;
+    if (n < p.N) {
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        if (m0 + r >= p.M) break;
+        if (p.out_f32) static_cast<float*>(p.out)[(m0 + r) * p.out_row + n] = stage[r][lane];
+        else static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(stage[r][lane], 0.f));
       }
     }
   }
+}
+
+// One of two warpgroups: columns [128 * half, 128 * half + 128) of the tile, a
+// row per thread.
+__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, int half, int quarter,
+                                int lane, volatile uint32_t* abort) {
+  const uint32_t tiles = p.m_tiles * p.n_tiles;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+  uint32_t pos = 0;
+  for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
+    uint32_t mt, nt;
+    tile_of(p, t, mt, nt);
+    const uint32_t m = (2 * mt + rank) * kTileM + quarter * 32 + lane;
+    const uint32_t n0 = nt * kTileN + half * 128;
+    const float* xs = p.xs + (m < p.M ? m : 0u) * p.xs_row;
+    const float* ws = p.ws + (n0 < p.N ? n0 >> 7 : 0u) * p.ws_row;
+    uint64_t acc[64];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = m0 + ty * 4 + i;
-    if (m >= p.M) continue;
+    for (int e = 0; e < 64; ++e) acc[e] = 0;
+    float scale = __ldg(xs) * __ldg(ws);
+    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
+      const uint32_t buf = pos & 1u;
+      const uint64_t s2 = f2_pack(scale, scale);
+      if (kb + 1 < p.kblocks) scale = __ldg(xs + (kb + 1) * p.xs_col) * __ldg(ws + (kb + 1) * p.ws_col);
+      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) return;
+      tc_fence_after();
+      const uint32_t col = taddr + buf * kTileN;
+      uint32_t v[2][32];
+      tmem_ld_32x32b_x32(col, v[0]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t n = n0 + tx + 16 * j;
-      if (n >= p.N) continue;
-      if (p.out_f32) static_cast<float*>(p.out)[m * p.out_row + n] = acc[i][j];
-      else static_cast<uint16_t*>(p.out)[m * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(acc[i][j], 0.f));
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait();
+        if (c < 3) {
+          tmem_ld_32x32b_x32(col + 32 * (c + 1), v[(c + 1) & 1]);
+        } else {
+          // The accumulator is in registers: the block after next may use it.
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[16 * c + e] = f2_fma(f2_pack(__uint_as_float(v[c & 1][2 * e]), __uint_as_float(v[c & 1][2 * e + 1])), s2,
+                                   acc[16 * c + e]);
+      }
+    }
+    store_row(p, s.stage[half * 4 + quarter], acc, m, n0, lane);
+  }
+}
+
+__global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
+    matmul_tile_kernel(const __grid_constant__ MatmulParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  TileSmem& s = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  volatile uint32_t* abort = &s.abort_flag;
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 2);   // both CTAs' UMMA threads: a slot is filled for both at once
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.acc_full[i]), 1);
+      mbar_init(smem_u32(&s.acc_empty[i]), 8);  // the eight accumulating warps
+    }
+    mbar_init(smem_u32(&s.drain), 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&p.tm_x);
+    tma_prefetch_desc(&p.tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers are ready before either copies into the other
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) tile_producer(s, p, rank, abort);
+    if (warp == 1 && lane == 0) tile_mma(s, p, tmem, abort);
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");  // 128 x 56 + 256 x 224 = 384 x 168
+    tile_accumulate(s, p, tmem, rank, (warp - 4) >> 2, warp & 3, lane, abort);
+  }
+  tc_fence_before();
+  cluster_sync();   // the other CTA no longer copies into this one or arrives on its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && s.abort_flag && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- few tokens
+constexpr int kThinThreads = 192;
+constexpr uint32_t kThinSmem = 112 * 1024;   // two CTAs per SM
+
+// MT tokens per CTA (the UMMA's N), 128 weight rows (its M).
+template <int MT>
+struct __align__(1024) ThinSmem {
+  static constexpr int kRing = (kThinSmem - 8192 - 2048) / (128 * kKB + MT * kKB);
+  uint8_t w[kRing][128 * kKB];
+  uint8_t x[kRing][MT * kKB];
+  float scale[4][2][MT];       // per accumulating warp: this block's and the next one's scales
+  uint64_t full[kRing], empty[kRing];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __grid_constant__ MatmulParams p,
+                                                                      const uint32_t splits) {
+  using Smem = ThinSmem<MT>;
+  constexpr int kRing = Smem::kRing;
+  constexpr uint32_t kCols = MT < 16 ? 16 : MT;          // tensor-memory columns of one accumulator
+  constexpr uint32_t kAlloc = 2 * kCols < 32 ? 32 : 2 * kCols;
+  static_assert(sizeof(Smem) + 1024 <= kThinSmem, "matmul thin shared memory");
+  static_assert(sizeof(float) * MT * 128 <= kRing * (128 + MT) * kKB, "the partial sums take the ring's place");
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile uint32_t* abort = &s.abort_flag;
+  const uint32_t rank = blockIdx.x % splits, tile = blockIdx.x / splits;
+  const uint32_t nt = tile % p.n_tiles, mt = tile / p.n_tiles;
+  const uint32_t kb0 = static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * rank / splits);
+  const uint32_t kb1 = static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * (rank + 1) / splits);
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.acc_full[i]), 1);
+      mbar_init(smem_u32(&s.acc_empty[i]), 4);
+    }
+    mbar_init(smem_u32(&s.drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s.tmem_base), kAlloc);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  float acc[MT];
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t pos = 0;
+      for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
+        const uint32_t st = pos % kRing;
+        if (!mbar_wait(smem_u32(&s.empty[st]), ((pos / kRing) & 1u) ^ 1u, abort)) break;
+        const uint32_t bar = smem_u32(&s.full[st]);
+        mbar_arrive_expect_tx(bar, (128 + MT) * kKB);
+        tma_load_2d(smem_u32(s.w[st]), &p.tm_w, bar, static_cast<int32_t>(kb * kKB), static_cast<int32_t>(nt * 128));
+        tma_load_2d(smem_u32(s.x[st]), &p.tm_x, bar, static_cast<int32_t>(kb * kKB), static_cast<int32_t>(mt * MT));
+      }
+      if (*abort) {
+        const uint32_t n = pos < kRing ? pos : kRing;
+        for (uint32_t i = 1; i <= n; ++i) {
+          const uint32_t q = pos - i;
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(smem_u32(&s.full[q % kRing]), (q / kRing) & 1u))
+            if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc(128, MT, 0, false);
+      uint32_t pos = 0;
+      for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
+        const uint32_t st = pos % kRing, buf = pos & 1u;
+        if (!mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort)) break;
+        if (!mbar_wait(smem_u32(&s.full[st]), (pos / kRing) & 1u, abort)) break;
+        tc_fence_after();
+        const uint64_t ad = sw128_desc_at(smem_u32(s.w[st])), bd = sw128_desc_at(smem_u32(s.x[st]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f8_ss(tmem + buf * kCols, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+        umma_commit(smem_u32(&s.empty[st]));
+        umma_commit(smem_u32(&s.acc_full[buf]));
+      }
+      umma_commit(smem_u32(&s.drain));
+      const uint64_t tw = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(&s.drain), 0))
+        if (global_timer_ns() - tw > kWaitTimeoutNs) break;
+    }
+    __syncwarp();
+  } else {
+    // Lane = weight row, register = token.
+    const int quarter = warp & 3;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float* ws = p.ws + nt * p.ws_row;
+    constexpr int kPer = (MT + 31) / 32;
+    float next[kPer];
+    auto fetch = [&](uint32_t kb) {
+      const float w = __ldg(ws + kb * p.ws_col);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t m = mt * MT + i * 32 + lane;
+        next[i] = i * 32 + lane < MT && m < p.M ? __ldg(p.xs + m * p.xs_row + kb * p.xs_col) * w : 0.f;
+      }
+    };
+#pragma unroll
+    for (int e = 0; e < MT; ++e) acc[e] = 0.f;
+    if (kb0 < kb1) fetch(kb0);
+    uint32_t pos = 0;
+    for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
+      const uint32_t buf = pos & 1u;
+      float* sc = s.scale[quarter][buf];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i * 32 + lane < MT) sc[i * 32 + lane] = next[i];
+      __syncwarp();
+      if (kb + 1 < kb1) fetch(kb + 1);
+      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < MT / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + buf * kCols + 16 * c, v);
+        tmem_ld_wait();
+        if (c == MT / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sc + 16 * c + e);
+          acc[16 * c + e] = fmaf(__uint_as_float(v[e]), f.x, acc[16 * c + e]);
+          acc[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), f.y, acc[16 * c + e + 1]);
+          acc[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), f.z, acc[16 * c + e + 2]);
+          acc[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), f.w, acc[16 * c + e + 3]);
+        }
+      }
     }
   }
+  const uint32_t n = nt * 128 + (warp & 3) * 32 + lane, m0 = mt * MT;
+  auto store = [&](uint32_t m, float v) {
+    if (p.out_f32) static_cast<float*>(p.out)[m * p.out_row + n] = v;
+    else static_cast<uint16_t*>(p.out)[m * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+  };
+  if (splits == 1) {
+    if (warp >= 2 && n < p.N) {
+#pragma unroll
+      for (int e = 0; e < MT; ++e)
+        if (m0 + e < p.M) store(m0 + e, acc[e]);
+    }
+  } else {
+    // Partial sums into the ring's place (all its copies and UMMAs are done:
+    // every block's accumulator has been read), then each CTA of the cluster
+    // adds the ranks' sums of its share of the tokens, in rank order.
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(s.w);
+    if (warp >= 2) {
+#pragma unroll
+      for (int e = 0; e < MT; ++e) part[e * 128 + (warp & 3) * 32 + lane] = acc[e];
+    }
+    cluster_sync();
+    if (warp >= 2 && n < p.N) {
+      const uint32_t e1 = min(static_cast<uint32_t>(MT), p.M - m0);
+      const uint32_t base = smem_u32(part) + ((warp & 3) * 32 + lane) * 4;
+      for (uint32_t e = rank; e < e1; e += splits) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < splits; ++r) v += ld_shared_cluster(map_shared(base + e * 512, r));
+        store(m0 + e, v);
+      }
+    }
+    cluster_sync();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kAlloc);
+  }
+  if (threadIdx.x == 0 && s.abort_flag && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+}
+
+template <int MT>
+mla_status_t launch_thin(MatmulParams& p, int dev, int sms, int slot, cudaStream_t stream) {
+  auto kernel = matmul_thin_kernel<MT>;
+  mla_status_t st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kThinSmem, dev, slot);
+  if (st != MLA_OK) return st;
+  const uint64_t tiles = static_cast<uint64_t>(p.n_tiles) * p.m_tiles;
+  // Split K until every SM has a CTA, but leave each at least two blocks.
+  uint32_t splits = 1;
+  while (splits < 8 && tiles * splits < static_cast<uint64_t>(sms) && p.kblocks >= 4 * splits) splits *= 2;
+  if (tiles * splits > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<uint32_t>(tiles * splits));
+  cfg.blockDim = dim3(kThinThreads);
+  cfg.dynamicSmemBytes = kThinSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, splits);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
+  return MLA_OK;
+}
+
+mla_status_t encode_codes(CUtensorMap* map, const mla_tensor_t* t, uint32_t box_rows, const char* what) {
+  uint64_t dims[2] = {static_cast<uint64_t>(t->shape[1]), static_cast<uint64_t>(t->shape[0])};
+  uint64_t str[1] = {static_cast<uint64_t>(std::max<int64_t>(t->stride[0], t->shape[1]))};
+  uint32_t box[2] = {kKB, box_rows};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t->data, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
 mla_status_t check_codes(const mla_tensor_t* t, const char* name) {
@@ -138,13 +591,10 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   if (M == 0) return MLA_OK;
   MatmulParams p;
-  p.x = static_cast<const uint8_t*>(x->data);
-  p.w = static_cast<const uint8_t*>(w->data);
+  memset(&p, 0, sizeof(p));
   p.xs = static_cast<const float*>(x_scales->data);
   p.ws = static_cast<const float*>(w_scales->data);
   p.out = out->data;
-  p.x_row = x->stride[0];
-  p.w_row = w->stride[0];
   p.xs_row = x_scales->stride[0];
   p.xs_col = x_scales->stride[1];
   p.ws_row = w_scales->stride[0];
@@ -152,13 +602,40 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   p.out_row = out->stride[0];
   p.M = static_cast<uint32_t>(M);
   p.N = static_cast<uint32_t>(N);
-  p.K = static_cast<uint32_t>(K);
+  p.kblocks = static_cast<uint32_t>(kb);
   p.out_f32 = out->dtype == MLA_DTYPE_F32;
-  (void)status;
-  const dim3 grid((p.N + 63) / 64, (p.M + 63) / 64);
-  if (grid.y > 65535u) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
-  matmul_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
-  return MLA_OK;
+  const uint32_t es = p.out_f32 ? 4 : 2;
+  const uint64_t place = reinterpret_cast<uintptr_t>(out->data) | (M > 1 ? static_cast<uint64_t>(out->stride[0]) * es : 0);
+  p.access = place % 32 == 0 ? 32 : place % 16 == 0 ? 16 : es;
+  p.status = status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
+  const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;
+  // The tile kernel needs a tile for most SMs (2 x pairs x wide of them).
+  if (M > 128 && 2 * pairs * wide >= static_cast<uint64_t>(sms) * 2 / 3) {
+    if (pairs * wide > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
+    if ((st = encode_codes(&p.tm_x, x, kTileM, "x")) != MLA_OK) return st;
+    if ((st = encode_codes(&p.tm_w, w, kTileN / 2, "w")) != MLA_OK) return st;
+    p.m_tiles = static_cast<uint32_t>(pairs);
+    p.n_tiles = static_cast<uint32_t>(wide);
+    const int smem = static_cast<int>(sizeof(TileSmem) + 1024);
+    if ((st = set_max_dynamic_smem(reinterpret_cast<const void*>(matmul_tile_kernel), smem, dev, 8)) != MLA_OK) return st;
+    if ((st = check_registers(reinterpret_cast<const void*>(matmul_tile_kernel), kTileRegs, dev, 8)) != MLA_OK) return st;
+    const uint32_t clusters = static_cast<uint32_t>(std::min<uint64_t>(pairs * wide, static_cast<uint64_t>(sms) / 2));
+    matmul_tile_kernel<<<2 * clusters, kTileThreads, smem, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
+    return MLA_OK;
+  }
+  const uint32_t mt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  if ((st = encode_codes(&p.tm_x, x, mt, "x")) != MLA_OK) return st;
+  if ((st = encode_codes(&p.tm_w, w, 128, "w")) != MLA_OK) return st;
+  p.m_tiles = static_cast<uint32_t>((M + mt - 1) / mt);
+  p.n_tiles = static_cast<uint32_t>((N + 127) / 128);
+  switch (mt) {
+    case 16: return launch_thin<16>(p, dev, sms, 9, s);
+    case 32: return launch_thin<32>(p, dev, sms, 10, s);
+    case 64: return launch_thin<64>(p, dev, sms, 11, s);
+    default: return launch_thin<128>(p, dev, sms, 12, s);
+  }
 }
