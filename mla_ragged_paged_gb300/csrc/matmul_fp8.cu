@@ -49,15 +49,17 @@ struct MatmulParams {
 
 // ---------------------------------------------------------------- many tiles
 constexpr int kStages = 4;
-constexpr int kTileThreads = 384;
-constexpr int kTileRegs = 168;        // what 65536 / 384 threads allows; split by setmaxnreg below
+constexpr int kAccWarps = 16;         // accumulating warps: four warpgroups of 64 columns each
+constexpr int kAccCols = 64;
+constexpr int kTileThreads = 128 + 32 * kAccWarps;
+constexpr int kTileRegs = 96;         // what 65536 / 640 threads allows; split by setmaxnreg below
 constexpr uint32_t kXBytes = kTileM * kKB, kWBytes = kTileN * kKB;
 constexpr uint32_t kBand = 8;         // pairs of row tiles walked together, so their x stays in L2
 
 struct __align__(1024) TileSmem {
   uint8_t x[kStages][kXBytes];
   uint8_t w[kStages][kWBytes];
-  float stage[8][32][33];              // per accumulating warp: 32 x 32 outputs on their way to narrow stores
+  float stage[kAccWarps][16][33];      // per accumulating warp: 16 x 32 outputs on their way to narrow stores
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -138,18 +140,18 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, vola
     if (global_timer_ns() - tw > kWaitTimeoutNs) break;
 }
 
-// Stores 128 output columns of row m from fp32 pairs.  Rows that allow wide
+// Stores kAccCols output columns of row m from fp32 pairs.  Rows that allow wide
 // accesses are stored by their own thread; others go through shared memory,
 // so that a warp stores 32 neighbouring columns of one row at a time.
 template <typename Stage>
-__device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, const uint64_t (&acc)[64], uint32_t m,
+__device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, const uint64_t (&acc)[kAccCols / 2], uint32_t m,
                                           uint32_t n0, int lane) {
   if (p.access >= 16) {
     if (m >= p.M) return;
     if (p.out_f32) {
       float* dst = static_cast<float*>(p.out) + m * p.out_row + n0;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < kAccCols / 8; ++c) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -172,7 +174,7 @@ __device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, c
     } else {
       uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.out_row + n0;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < kAccCols / 16; ++c) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -197,61 +199,68 @@ __device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, c
     return;
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    __syncwarp();
+  for (int c = 0; c < kAccCols / 32; ++c) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float lo, hi;
-      f2_unpack(acc[16 * c + e], lo, hi);
-      stage[lane][2 * e] = lo;
-      stage[lane][2 * e + 1] = hi;
-    }
-    __syncwarp();
-    const uint32_t n = n0 + 32 * c + lane, m0 = m - lane;
-    if (n < p.N) {
+    for (int half = 0; half < 2; ++half) {   // rows 0..15, then 16..31 of the warp
+      __syncwarp();
+      if ((lane >> 4) == half) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float lo, hi;
+          f2_unpack(acc[16 * c + e], lo, hi);
+          stage[lane & 15][2 * e] = lo;
+          stage[lane & 15][2 * e + 1] = hi;
+        }
+      }
+      __syncwarp();
+      const uint32_t n = n0 + 32 * c + lane, m0 = m - lane + 16 * half;
+      if (n < p.N) {
 #pragma unroll 4
-      for (int r = 0; r < 32; ++r) {
-        if (m0 + r >= p.M) break;
-        if (p.out_f32) static_cast<float*>(p.out)[(m0 + r) * p.out_row + n] = stage[r][lane];
-        else static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(stage[r][lane], 0.f));
+        for (int r = 0; r < 16; ++r) {
+          if (m0 + r >= p.M) break;
+          if (p.out_f32) static_cast<float*>(p.out)[(m0 + r) * p.out_row + n] = stage[r][lane];
+          else static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(stage[r][lane], 0.f));
+        }
       }
     }
   }
 }
 
-// One of two warpgroups: columns [128 * half, 128 * half + 128) of the tile, a
+// One of four warpgroups: columns [64 * group, 64 * group + 64) of the tile, a
 // row per thread.
-__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, int half, int quarter,
+__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, int group, int quarter,
                                 int lane, volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
-  const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kAccCols;
   uint32_t pos = 0;
   for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
     uint32_t mt, nt;
     tile_of(p, t, mt, nt);
     const uint32_t m = (2 * mt + rank) * kTileM + quarter * 32 + lane;
-    const uint32_t n0 = nt * kTileN + half * 128;
+    const uint32_t n0 = nt * kTileN + group * kAccCols;
     const float* xs = p.xs + (m < p.M ? m : 0u) * p.xs_row;
     const float* ws = p.ws + (n0 < p.N ? n0 >> 7 : 0u) * p.ws_row;
-    uint64_t acc[64];
+    uint64_t acc[kAccCols / 2];
 #pragma unroll
-    for (int e = 0; e < 64; ++e) acc[e] = 0;
+    for (int e = 0; e < kAccCols / 2; ++e) acc[e] = 0;
     float scale = __ldg(xs) * __ldg(ws);
     for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
       const uint32_t buf = pos & 1u;
       const uint64_t s2 = f2_pack(scale, scale);
-      if (kb + 1 < p.kblocks) scale = __ldg(xs + (kb + 1) * p.xs_col) * __ldg(ws + (kb + 1) * p.ws_col);
+      if (kb + 1 < p.kblocks) {
+        xs += p.xs_col;
+        ws += p.ws_col;
+        scale = __ldg(xs) * __ldg(ws);
+      }
       if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) return;
       tc_fence_after();
       const uint32_t col = taddr + buf * kTileN;
-      uint32_t v[2][32];
-      tmem_ld_32x32b_x32(col, v[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kAccCols / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(col + 32 * c, v);
         tmem_ld_wait();
-        if (c < 3) {
-          tmem_ld_32x32b_x32(col + 32 * (c + 1), v[(c + 1) & 1]);
-        } else {
+        if (c == kAccCols / 32 - 1) {
           // The accumulator is in registers: the block after next may use it.
           tc_fence_before();
           __syncwarp();
@@ -259,11 +268,10 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tme
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          acc[16 * c + e] = f2_fma(f2_pack(__uint_as_float(v[c & 1][2 * e]), __uint_as_float(v[c & 1][2 * e + 1])), s2,
-                                   acc[16 * c + e]);
+          acc[16 * c + e] = f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2, acc[16 * c + e]);
       }
     }
-    store_row(p, s.stage[half * 4 + quarter], acc, m, n0, lane);
+    store_row(p, s.stage[group * 4 + quarter], acc, m, n0, lane);
   }
 }
 
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
-      mbar_init(smem_u32(&s.acc_empty[i]), 8);  // the eight accumulating warps
+      mbar_init(smem_u32(&s.acc_empty[i]), kAccWarps);
     }
     mbar_init(smem_u32(&s.drain), 1);
     fence_barrier_init();
@@ -298,12 +306,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0 && lane == 0) tile_producer(s, p, rank, abort);
     if (warp == 1 && lane == 0) tile_mma(s, p, tmem, abort);
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");  // 128 x 56 + 256 x 224 = 384 x 168
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");  // 128 x 32 + 512 x 112 = 640 x 96
     tile_accumulate(s, p, tmem, rank, (warp - 4) >> 2, warp & 3, lane, abort);
   }
   tc_fence_before();
