@@ -4,10 +4,44 @@
 //   x_j = scale * q . c_j       q [576] = [latent 512 | rope 64]
 //   out = sum_j softmax(x)_j c_j[0:512],  lse = ln sum_j exp(x_j)
 // over the keys the mask leaves visible (causal: j <= cache_lens[b] + i).
+//
+// All heads (and new tokens) of a sequence read the same rows, so a row tile
+// is up to 64 (token, head) queries.  A cached row costs 576 bytes and 2 * 1088
+// flops per query: up to about 60 queries a sequence the kernel is bound by
+// HBM, above that by the tensor cores and their shared-memory operands.
+//
+// Tensor cores.  The cached codes go from HBM to the tensor cores as they are:
+// keys are the 128-row operand of both products, so few queries waste no
+// tensor time and a tile is read once for both:
+//   S^T [128 keys, rows]       = codes [128, 576] . Q^T
+//   O^T [4 x 128 dims, rows] += codes^T (512 dims) . P^T
+// Both products are e4m3, so the other operands are split into two e4m3 terms,
+// a value and what its rounding left: q (scaled by a power of two per row) is
+// reproduced exactly, a bf16 value having eight significant bits and each term
+// four; a softmax weight keeps eight bits, like bf16.  Sums are fp32 in tensor
+// memory.  The terms of q are stacked as 2 x rows columns of one product; those
+// of P too for 32-row tiles, else they are two products into one O.
+//
+// Softmax.  A thread owns one key and half the rows of the tile, so the key's
+// scale is a scalar of the thread: with y = x + log2(s_j) (log2 units) the weight
+// that multiplies the codes is w_j = 2^(y_j - mu + 6) <= 2^8.5 and the one that
+// is summed is w_j / s_j.  e4m3 loses what lies below 2^-10, so the reference mu
+// of a row follows the tiles in both directions: it moves when the tile's
+// maximum leaves [mu - 5, mu + 2.5], and O is then rescaled in tensor memory.
+// A key far above the rest (the first token often is) thus does not cost the
+// others their precision.
+//
+// Work.  The units are (sequence, row tile, 128 keys) in that order; each CTA,
+// one per SM, takes an equal contiguous share, however long the sequences are.
+// What a CTA's share cuts out of a row tile's keys goes to the workspace as
+// (O, mu, l), and decode_join_kernel adds the parts in order.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "host_common.h"
 #include "sm103.cuh"
@@ -16,107 +50,812 @@ namespace mla {
 namespace {
 
 constexpr int kLatent = 512, kRope = 64, kWidth = kLatent + kRope;
-constexpr int kDecWarps = 8;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kKeys = 128;               // keys per tile
+constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent dims
+constexpr uint32_t kRopeBytes = kKeys * 64;
+constexpr int kDecThreads = 384;              // producer, UMMA, two idle warps; two softmax warpgroups
+constexpr int kDecRegs = 168;
+constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
+constexpr uint32_t kMaxRows = 64;
+constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
+constexpr float kShift = 6.f;                 // w = 2^(y - mu + kShift)
+constexpr float kRaise = 2.5f, kLower = 5.f;  // mu moves when the tile's maximum is that far off
+constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
+// The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
+// 1e27 neither end leaves fp32.
+constexpr float kSumShift = 30.f;
+
+// Part of a row tile's result: slot 2 c of CTA c for one that continues an
+// earlier CTA's, 2 c + 1 for one that begins and does not end.
+struct PartHeader {
+  uint32_t valid, b, rt, last_cta;
+};
 
 struct DecodeParams {
+  CUtensorMap tm_latent, tm_rope;  // cache rows [slots, 576]; boxes 128 x 1 and 64 x 1
   uint16_t* out;
   long long o_tok, o_head;
   float* lse;
   long long l_tok, l_head;
   const uint16_t* q;
   long long q_tok, q_head;
-  const uint8_t* cache;
-  long long page_bytes, tok_bytes;
   const float* scales;
-  uint32_t per_token;
   const uint32_t* page_table;
   long long pt_stride;
   const uint32_t* ro;
   const uint32_t* lens;
   uint32_t* status;
-  float sl2;  // scale * log2(e)
-  uint32_t causal, Tq, H, B, P, num_pages, max_pages;
+  PartHeader* headers;             // [2 * kMaxCtas]
+  float* part_ml;                  // [slots][2][kMaxRows]: mu, l
+  float* part_o;                   // [slots][kMaxRows][512]
+  float sl2;                       // scale * log2(e)
+  uint32_t per_token, causal, Tq, H, B, P, num_pages, max_pages, max_keys;
 };
 
-// One block per (token, head), a key per warp at a time; the warps' running
-// softmaxes are joined at the end.
-__global__ void __launch_bounds__(kDecWarps * 32) decode_kernel(const DecodeParams p) {
-  __shared__ float sm[kDecWarps], sl[kDecWarps], so[kDecWarps][kLatent];
+template <int NR>
+struct Rows {
+  static constexpr bool kStacked = NR <= 32;      // both terms of P in one product
+  static constexpr int kCols = NR / 2;            // rows of one softmax warpgroup
+  static constexpr uint32_t kQChunk = 2 * NR * 128;
+  static constexpr uint32_t kPTerm = kKeys * 64;  // one P operand: a 64-byte row per key
+  static constexpr int kPTerms = kStacked ? 1 : 2;
+  static constexpr int kSlots = NR <= 32 ? 10 : 8;
+  static constexpr int kRopeSlots = NR <= 32 ? 2 : 1;
+  static constexpr uint32_t kOCols = 64;          // tensor-memory columns of 128 dims of O^T
+};
+
+template <int NR>
+struct __align__(1024) DecodeSmem {
+  using R = Rows<NR>;
+  uint8_t chunk[R::kSlots][kChunk];
+  uint8_t rope[R::kRopeSlots][kRopeBytes];
+  uint8_t q[4][R::kQChunk];
+  uint8_t q_rope[2 * NR * 64];
+  uint8_t p[R::kPTerms][R::kPTerm];
+  float warp_red[2][4][32];
+  float row_val[2][32];
+  float col_factor[NR];
+  uint64_t full[R::kSlots], empty[R::kSlots];
+  uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
+  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+static_assert(sizeof(DecodeSmem<64>) + 1024 <= 232448, "decode shared memory");
+static_assert(sizeof(DecodeSmem<32>) + 1024 <= 232448, "decode shared memory");
+
+// ------------------------------------------------------------ the work's order
+struct Seq {
+  uint32_t q0, n, prior, keys, row_tiles, key_tiles;
+};
+template <int NR>
+__device__ __forceinline__ Seq sequence(const DecodeParams& p, uint32_t b) {
+  Seq s;
+  const uint32_t lo = p.ro[b], hi = p.ro[b + 1];
+  s.prior = p.lens[b];
+  s.q0 = lo;
+  s.n = lo < hi && hi <= p.Tq ? hi - lo : 0u;
+  const uint64_t keys = static_cast<uint64_t>(s.prior) + s.n;
+  s.keys = static_cast<uint32_t>(min(keys, static_cast<uint64_t>(p.max_keys)));
+  s.row_tiles = static_cast<uint32_t>((static_cast<uint64_t>(s.n) * p.H + NR - 1) / NR);
+  s.key_tiles = (s.keys + kKeys - 1) / kKeys;
+  return s;
+}
+
+// A CTA's share: units [first, first + left) from unit `at` of sequence b.
+struct Share {
+  unsigned long long at, left;
+  uint32_t b;
+};
+struct Segment {
+  Seq s;
+  uint32_t b, rt, kt0, kt1;  // key tiles [kt0, kt1) of row tile rt
+};
+template <int NR>
+__device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, Segment& g) {
+  while (sh.left && sh.b < p.B) {
+    const Seq s = sequence<NR>(p, sh.b);
+    const unsigned long long units = static_cast<unsigned long long>(s.row_tiles) * s.key_tiles;
+    if (sh.at >= units) {
+      sh.at = 0;
+      ++sh.b;
+      continue;
+    }
+    g.s = s;
+    g.b = sh.b;
+    g.rt = static_cast<uint32_t>(sh.at / s.key_tiles);
+    g.kt0 = static_cast<uint32_t>(sh.at - static_cast<unsigned long long>(g.rt) * s.key_tiles);
+    g.kt1 = static_cast<uint32_t>(min(static_cast<unsigned long long>(s.key_tiles), g.kt0 + sh.left));
+    sh.left -= g.kt1 - g.kt0;
+    sh.at += g.kt1 - g.kt0;
+    return true;
+  }
+  return false;
+}
+
+// The slot of key j of sequence b; false (and a status bit) for a bad page.
+__device__ __forceinline__ bool key_slot(const DecodeParams& p, uint32_t b, uint32_t j, uint32_t& slot, uint32_t& bad) {
+  const uint32_t col = j / p.P;
+  if (col >= p.max_pages) {
+    bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
+    return false;
+  }
+  const uint32_t page = __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col);
+  if (page >= p.num_pages) {
+    bad |= MLA_DEVICE_STATUS_BAD_PAGE;
+    return false;
+  }
+  slot = page * p.P + (j - col * p.P);
+  return true;
+}
+
+// ------------------------------------------------------------ producer
+template <int NR>
+__device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
+  using R = Rows<NR>;
+  uint32_t tile = 0, bad = 0;
+  bool alive = true;
+  Segment g;
+  while (alive && next_segment<NR>(p, sh, g)) {
+    for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
+      // Rows 4 lane .. 4 lane + 3 of the tile; a row past the context or with a
+      // bad page is slot 0, whatever it holds (the softmax zeroes it).
+      int32_t rows[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t j = kt * kKeys + 4 * lane + e;
+        uint32_t slot = 0;
+        if (j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
+        rows[e] = static_cast<int32_t>(slot);
+      }
+      for (int c = 0; c < 5 && alive; ++c) {
+        const uint32_t pos = c < 4 ? tile * 4 + c : tile;
+        const uint32_t slots = c < 4 ? R::kSlots : R::kRopeSlots;
+        const uint32_t st = pos % slots;
+        uint64_t* full = c < 4 ? &s.full[st] : &s.rope_full[st];
+        uint64_t* empty = c < 4 ? &s.empty[st] : &s.rope_empty[st];
+        if (!(alive = mbar_wait(smem_u32(empty), ((pos / slots) & 1u) ^ 1u, abort))) break;
+        const uint32_t bar = smem_u32(full);
+        if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
+        __syncwarp();
+        if (c < 4)
+          tma_gather4_2d(smem_u32(s.chunk[st]) + lane * 512u, &p.tm_latent, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
+        else
+          tma_gather4_2d(smem_u32(s.rope[st]) + lane * 256u, &p.tm_rope, bar, kLatent, rows[0], rows[1], rows[2], rows[3]);
+      }
+    }
+  }
+  for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+  if (lane == 0 && bad && p.status) atomicOr(p.status, bad);
+  if (*abort) {
+    // Let the copies still in flight land before the CTA exits.
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; i <= R::kSlots && i <= tile * 4 + 4; ++i) {
+      const uint32_t q = tile * 4 + 4 - i;
+      while (!mbar_try_wait(smem_u32(&s.full[q % R::kSlots]), (q / R::kSlots) & 1u))
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    }
+    for (uint32_t i = 0; i < R::kRopeSlots && i <= tile; ++i) {
+      const uint32_t q = tile - i;
+      while (!mbar_try_wait(smem_u32(&s.rope_full[q % R::kRopeSlots]), (q / R::kRopeSlots) & 1u))
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    }
+  }
+}
+
+// ------------------------------------------------------------ UMMA issuer
+template <int NR>
+__device__ void decode_mma(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
+  using R = Rows<NR>;
+  const uint32_t id_s = make_idesc(128, 2 * NR, 0, false);
+  // P.V: A = codes^T (dims contiguous: MN-major), B = P^T (rows contiguous: MN-major).
+  const uint32_t id_o = make_idesc(128, 64, 0, true) | (1u << 15);
+  uint32_t tile = 0, segs = 0;
+  bool alive = true;
+  auto scores = [&](uint32_t t) {
+    if (!(alive = mbar_wait(smem_u32(&s.s_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, abort))) return;
+    const uint32_t d = tmem + kColS + (t & 1) * (2 * NR);
+    for (uint32_t c = 0; c < 4; ++c) {
+      const uint32_t pos = t * 4 + c, st = pos % R::kSlots;
+      if (!(alive = mbar_wait(smem_u32(&s.full[st]), (pos / R::kSlots) & 1u, abort))) return;
+      tc_fence_after();
+      const uint64_t kd = sw128_desc_at(smem_u32(s.chunk[st])), qd = sw128_desc_at(smem_u32(s.q[c]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, (c | k) != 0);
+    }
+    const uint32_t st = t % R::kRopeSlots;
+    if (!(alive = mbar_wait(smem_u32(&s.rope_full[st]), (t / R::kRopeSlots) & 1u, abort))) return;
+    tc_fence_after();
+    const uint64_t kd = sw64_desc_at(smem_u32(s.rope[st])), qd = sw64_desc_at(smem_u32(s.q_rope));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, 1u);
+    umma_commit(smem_u32(&s.rope_empty[st]));
+    umma_commit(smem_u32(&s.s_full[t & 1]));
+  };
+  Segment g;
+  while (alive && next_segment<NR>(p, sh, g)) {
+    const uint32_t n = g.kt1 - g.kt0;
+    if (!(alive = mbar_wait(smem_u32(&s.q_full), segs & 1u, abort))) break;
+    ++segs;
+    scores(tile);
+    for (uint32_t i = 0; i < n && alive; ++i, ++tile) {
+      if (i + 1 < n) scores(tile + 1);
+      if (!alive) break;
+      if (!(alive = mbar_wait(smem_u32(&s.p_full), tile & 1u, abort))) break;
+      tc_fence_after();
+      for (uint32_t c = 0; c < 4; ++c) {
+        const uint32_t st = (tile * 4 + c) % R::kSlots;
+        const uint64_t vd = sw128_desc_at(smem_u32(s.chunk[st]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int term = 0; term < R::kPTerms; ++term)
+            umma_f8_ss(tmem + c * R::kOCols, vd + k * (32 * 128 >> 4), sw64_desc_at(smem_u32(s.p[term])) + k * (32 * 64 >> 4),
+                       id_o, (i | k | term) != 0);
+        umma_commit(smem_u32(&s.empty[st]));
+      }
+      umma_commit(smem_u32(&s.pv_done));
+    }
+  }
+  // No UMMA may still be in flight when tensor memory is released.
+  umma_commit(smem_u32(&s.drain));
+  const uint64_t tw = global_timer_ns();
+  while (!mbar_try_wait(smem_u32(&s.drain), 0))
+    if (global_timer_ns() - tw > kWaitTimeoutNs) break;
+}
+
+// ------------------------------------------------------------ softmax
+// Reduces N values per lane over the warp's lanes; lane l gets the result for
+// value l mod N.  Each step halves the values by trading the half the partner
+// keeps: N - 1 shuffles instead of 5 N.
+template <int N, typename Op>
+__device__ __forceinline__ float warp_transpose_reduce(const float (&in)[N], int lane, Op op) {
+  float a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = in[i];
+#pragma unroll
+  for (int s = N / 2; s >= 1; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float keep = up ? a[i + s] : a[i], give = up ? a[i] : a[i + s];
+      a[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, s));
+    }
+  }
+#pragma unroll
+  for (int s = N; s < 32; s <<= 1) a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], s));
+  return a[0];
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_ld_32x32b_x32(addr, r);
+  else tmem_ld_32x32b_x16(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_st_32x32b_x32(addr, r);
+  else tmem_st_32x32b_x16(addr, r);
+}
+
+// The queries of a row tile as two e4m3 terms, rows t1 at r and t2 at NR + r of
+// the K-major operand; col_factor[r] takes the row's power of two back.
+template <int NR>
+__device__ void load_queries(DecodeSmem<NR>& s, const DecodeParams& p, const Segment& g, int tid) {
+  constexpr int kPer = 256 / NR;                  // threads per row
+  constexpr int kPieces = (36 + kPer - 1) / kPer;  // of 16 dims
+  const uint32_t r = tid / kPer, part = tid % kPer;
+  const uint64_t row = static_cast<uint64_t>(g.rt) * NR + r;
+  const bool live = row < static_cast<uint64_t>(g.s.n) * p.H;
+  const uint32_t tok = static_cast<uint32_t>(row / p.H), head = static_cast<uint32_t>(row - static_cast<uint64_t>(tok) * p.H);
+  const uint16_t* src = p.q + (g.s.q0 + static_cast<long long>(live ? tok : 0u)) * p.q_tok + (live ? head : 0u) * p.q_head;
+  uint4 v[kPieces][2];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const uint32_t piece = part + i * kPer;
+    v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (live && piece < 36) {
+      v[i][0] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * piece);
+      v[i][1] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * piece + 1);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = max(m, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+    }
+  }
+#pragma unroll
+  for (int o = kPer / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // A power of two that takes the row's largest value into [128, 256); a row
+  // with an infinity or a NaN becomes NaN codes.
+  int k = 134 - static_cast<int>(m >> 23);
+  k = min(max(k, -120), 120);
+  const float mul = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+  if (part == 0) s.col_factor[r] = __uint_as_float(static_cast<uint32_t>(127 - k) << 23) * p.sl2;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const uint32_t piece = part + i * kPer;
+    if (piece >= 36) continue;
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t a0, b0, a1, b1;
+        two_terms_e4m3(pack_f16x2(__uint_as_float(w[2 * e] << 16) * mul, __uint_as_float(w[2 * e] & 0xFFFF0000u) * mul), a0, b0);
+        two_terms_e4m3(pack_f16x2(__uint_as_float(w[2 * e + 1] << 16) * mul, __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * mul),
+                       a1, b1);
+        t1[2 * h + e] = a0 | a1 << 16;
+        t2[2 * h + e] = b0 | b1 << 16;
+      }
+    }
+#pragma unroll
+    for (int term = 0; term < 2; ++term) {
+      const uint32_t row_at = term * NR + r;
+      uint8_t* dst;
+      if (piece < 32)
+        dst = s.q[piece >> 3] + row_at * 128 + (((piece & 7) ^ (row_at & 7)) << 4);
+      else
+        dst = s.q_rope + row_at * 64 + (((piece & 3) ^ ((row_at >> 1) & 3)) << 4);
+      *reinterpret_cast<uint4*>(dst) = term ? make_uint4(t2[0], t2[1], t2[2], t2[3]) : make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    }
+  }
+}
+
+// A softmax warp never leaves its loops early, so that the named barriers always
+// meet; once the CTA gives up its waits end at once and its results mean nothing.
+__device__ __forceinline__ void softmax_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if (mbar_try_wait(bar, parity) || *abort) return;
+  mbar_wait(bar, parity, abort);
+}
+
+template <int NR>
+__device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, unsigned long long units, uint32_t ctas,
+                               uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
+  using R = Rows<NR>;
+  constexpr int N = R::kCols;
+  const int tid = group * 128 + quarter * 32 + lane;     // 0 .. 255
+  const uint32_t key = quarter * 32 + lane;              // this thread's key of a tile
+  const uint32_t lane_at = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t bar = 1 + group;
+  const uint32_t r0 = group * N;                         // first row of the warpgroup
+  const uint32_t my_row = lane & (N - 1);                // row of per-lane row values
+  auto fmax2 = [](float a, float b) { return fmaxf(a, b); };
+  auto add2 = [](float a, float b) { return a + b; };
+  uint32_t tile = 0;
+  uint32_t head_valid = 0, part_b = 0, part_rt = 0, part_last = 0;
+  Segment g;
+  while (next_segment<NR>(p, sh, g)) {
+    // ---- queries.  The previous segment's products with the old ones are
+    // done: this warp has seen its last score tile.
+    load_queries<NR>(s, p, g, tid);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+    asm volatile("bar.sync 3, 256;" ::: "memory");       // col_factor is written by both warpgroups
+    const uint64_t live = static_cast<uint64_t>(g.s.n) * p.H;   // rows of the sequence
+    const uint64_t first_row = static_cast<uint64_t>(g.rt) * NR;
+    const uint32_t tok0 = static_cast<uint32_t>(first_row / p.H);
+    const uint32_t tok1 = static_cast<uint32_t>(min(first_row + NR, live) - 1) / p.H;
+    // Keys below `shared` are visible to every row of the tile, keys from `end` on to none.
+    auto seen_by = [&](uint32_t tok) {
+      return p.causal ? static_cast<uint32_t>(min(static_cast<uint64_t>(g.s.keys), static_cast<uint64_t>(g.s.prior) + tok + 1))
+                      : g.s.keys;
+    };
+    const uint32_t shared = seen_by(tok0), end = seen_by(tok1);
+    float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
+    float l[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = 0.f;
+    auto fetch = [&](uint32_t kt, float& sc) -> bool {
+      const uint32_t j = kt * kKeys + key;
+      uint32_t slot, bad = 0;
+      sc = 1.f;
+      if (j >= end || !key_slot(p, g.b, j, slot, bad)) return false;
+      sc = __ldg(p.scales + (p.per_token ? slot : 0u));
+      return true;
+    };
+    float sc_next;
+    bool ok_next = fetch(g.kt0, sc_next);
+    for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
+      const float sc = sc_next;
+      const bool ok = ok_next;
+      if (kt + 1 < g.kt1) ok_next = fetch(kt + 1, sc_next);
+      const uint32_t j = kt * kKeys + key;
+      const float ls = log2f(fmaxf(sc, 0x1p-120f));      // NaN and 0 give finite factors; the score carries the NaN
+      const float to_sum = ex2_approx(-kShift - kSumShift - ls);
+      // ---- scores
+      softmax_wait(smem_u32(&s.s_full[tile & 1]), (tile >> 1) & 1u, abort);
+      tc_fence_after();
+      float y[N];
+      {
+        uint32_t a[N], b[N];
+        const uint32_t col = tmem + lane_at + kColS + (tile & 1) * (2 * NR) + r0;
+        tmem_load<N>(col, a);
+        tmem_load<N>(col + NR, b);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.s_empty[tile & 1]));
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s.col_factor[r0 + i]);
+          y[i] = fmaf((__uint_as_float(a[i]) + __uint_as_float(b[i])) * f.x, sc, ls);
+          y[i + 1] = fmaf((__uint_as_float(a[i + 1]) + __uint_as_float(b[i + 1])) * f.y, sc, ls);
+          y[i + 2] = fmaf((__uint_as_float(a[i + 2]) + __uint_as_float(b[i + 2])) * f.z, sc, ls);
+          y[i + 3] = fmaf((__uint_as_float(a[i + 3]) + __uint_as_float(b[i + 3])) * f.w, sc, ls);
+        }
+      }
+      const bool partial = ok && j >= shared;            // some rows see this key, some do not
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = -INFINITY;
+      } else if (partial) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (j > g.s.prior + static_cast<uint32_t>((first_row + r0 + i) / p.H)) y[i] = -INFINITY;
+      }
+      // ---- the tile's maximum of every row, and the row's reference
+      const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
+      s.warp_red[group][quarter][lane] = wm;
+      named_bar_sync(bar, 128);
+      const float tm = fmaxf(fmaxf(s.warp_red[group][0][lane], s.warp_red[group][1][lane]),
+                             fmaxf(s.warp_red[group][2][lane], s.warp_red[group][3][lane]));
+      // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
+      float next = mu;
+      if (tm > mu + kRaise || (tm < mu - kLower && tm > -INFINITY)) next = fmaxf(rintf(tm), peak - kDepth);
+      peak = fmaxf(peak, next);
+      const float factor = mu == next ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fmaxf(mu - next, -127.f))) << 23);
+      mu = next;
+      if (quarter == 0 && lane < N) s.row_val[group][lane] = mu == -INFINITY ? -kShift : mu - kShift;
+      const bool rescale = __any_sync(0xffffffffu, factor != 1.f);
+      named_bar_sync(bar, 128);
+      if (rescale) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) l[i] *= __shfl_sync(0xffffffffu, factor, i);
+        if (kt != g.kt0) {
+          // Every product into O so far is done, the next one waits for this tile's P.
+          softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * (R::kStacked ? 2 : 1); ++c) {
+            uint32_t o[N];
+            const uint32_t at = tmem + lane_at + (c & 3) * R::kOCols + (c >> 2) * NR + r0;
+            tmem_load<N>(at, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, factor, i));
+            tmem_store<N>(at, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      // ---- weights: two e4m3 terms per row
+      uint32_t t1[N / 4], t2[N / 4];
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
+        const float w0 = ex2_approx(y[i] - m4.x), w1 = ex2_approx(y[i + 1] - m4.y), w2 = ex2_approx(y[i + 2] - m4.z),
+                    w3 = ex2_approx(y[i + 3] - m4.w);
+        l[i] = fmaf(w0, to_sum, l[i]);
+        l[i + 1] = fmaf(w1, to_sum, l[i + 1]);
+        l[i + 2] = fmaf(w2, to_sum, l[i + 2]);
+        l[i + 3] = fmaf(w3, to_sum, l[i + 3]);
+        uint32_t a0, b0, a1, b1;
+        two_terms_e4m3(pack_f16x2(w0, w1), a0, b0);
+        two_terms_e4m3(pack_f16x2(w2, w3), a1, b1);
+        t1[i / 4] = a0 | a1 << 16;
+        t2[i / 4] = b0 | b1 << 16;
+      }
+      // P is free once the previous tile's products are done.
+      if (tile) softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
+      {
+        const uint32_t swz = (key >> 1) & 3;
+        uint8_t* row = s.p[0] + key * 64;
+        if constexpr (R::kStacked) {
+          *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(row + (((2 + group) ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<uint4*>(row + (((2 * group + h) ^ swz) << 4)) =
+                make_uint4(t1[4 * h], t1[4 * h + 1], t1[4 * h + 2], t1[4 * h + 3]);
+            *reinterpret_cast<uint4*>(row + R::kPTerm + (((2 * group + h) ^ swz) << 4)) =
+                make_uint4(t2[4 * h], t2[4 * h + 1], t2[4 * h + 2], t2[4 * h + 3]);
+          }
+        }
+      }
+      if (group == 0 && (!ok || partial)) {
+        // A weight of 0 times a NaN code would be NaN: a key no row sees, or one
+        // some rows do not see and that holds a NaN, becomes zeros.  (Rows that
+        // see the NaN have NaN weights already: the scores read the same codes.)
+        uint32_t nan = !ok;
+        for (int c = 0; c < 4; ++c)   // (complete long ago: orders this thread after the copies)
+          softmax_wait(smem_u32(&s.full[(tile * 4 + c) % R::kSlots]), ((tile * 4 + c) / R::kSlots) & 1u, abort);
+#pragma unroll 1
+        for (int c = 0; c < 4 && !nan; ++c) {
+          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[(tile * 4 + c) % R::kSlots] + key * 128);
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = row[i];
+            nan |= (((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                    ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+          }
+        }
+        if (nan) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint4* row = reinterpret_cast<uint4*>(s.chunk[(tile * 4 + c) % R::kSlots] + key * 128);
+            for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.p_full));
+    }
+    // ---- the segment's result
+    softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
+    tc_fence_after();
+    const float wl = warp_transpose_reduce<N>(l, lane, add2);
+    s.warp_red[group][quarter][lane] = wl;
+    named_bar_sync(bar, 128);
+    const float total = (s.warp_red[group][0][lane] + s.warp_red[group][1][lane]) +
+                        (s.warp_red[group][2][lane] + s.warp_red[group][3][lane]);
+    const bool begins = g.kt0 == 0, ends = g.kt1 == g.s.key_tiles;
+    const bool whole = begins && ends;
+    const uint32_t slot = 2 * blockIdx.x + (begins ? 1 : 0);
+    const uint64_t row = first_row + r0 + my_row;
+    if (quarter == 0 && lane < N) {
+      // 2^(mu - kShift) and 2^(mu + kSumShift) are the units of O and l.
+      s.row_val[group][lane] = total != 0.f ? 0x1p-36f / total : 0.f;
+      if (!whole) {
+        p.part_ml[(static_cast<size_t>(slot) * 2) * kMaxRows + r0 + lane] = mu;
+        p.part_ml[(static_cast<size_t>(slot) * 2 + 1) * kMaxRows + r0 + lane] = total;
+      } else if (p.lse && row < live) {
+        const uint32_t tok = static_cast<uint32_t>(row / p.H);
+        p.lse[(g.s.q0 + static_cast<long long>(tok)) * p.l_tok + static_cast<long long>(row - static_cast<uint64_t>(tok) * p.H) * p.l_head] =
+            total != 0.f ? (mu + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
+      }
+    }
+    named_bar_sync(bar, 128);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[N];
+      const uint32_t at = tmem + lane_at + c * R::kOCols + r0;
+      tmem_load<N>(at, o);
+      if constexpr (R::kStacked) {
+        uint32_t o2[N];
+        tmem_load<N>(at + NR, o2);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o2[i]));
+      } else {
+        tmem_ld_wait();
+      }
+      const uint32_t dim = c * 128 + key;
+      if (whole) {
+        uint32_t tok = static_cast<uint32_t>((first_row + r0) / p.H);
+        uint32_t head = static_cast<uint32_t>(first_row + r0 - static_cast<uint64_t>(tok) * p.H);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (first_row + r0 + i < live) {
+            const float v = s.row_val[group][i];
+            p.out[(g.s.q0 + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + dim] =
+                static_cast<uint16_t>(pack_bf16x2(v != 0.f ? __uint_as_float(o[i]) * v : 0.f, 0.f));
+          }
+          if (++head == p.H) head = 0, ++tok;
+        }
+      } else {
+        float* dst = p.part_o + (static_cast<size_t>(slot) * kMaxRows + r0) * kLatent + dim;
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i * kLatent] = __uint_as_float(o[i]);
+      }
+    }
+    tc_fence_before();
+    if (begins && !ends) {
+      head_valid = 1;
+      part_b = g.b;
+      part_rt = g.rt;
+      // The CTA that holds the row tile's last key tile.
+      const unsigned long long u1 = units * (blockIdx.x + 1) / ctas, last = u1 + (g.s.key_tiles - g.kt1) - 1;
+      part_last = static_cast<uint32_t>(((last + 1) * ctas - 1) / units);
+    }
+    named_bar_sync(bar, 128);                            // row_val and warp_red are free again
+  }
+  if (tid == 0) {
+    PartHeader h = {head_valid, part_b, part_rt, part_last};
+    p.headers[blockIdx.x] = h;
+  }
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+  using R = Rows<NR>;
+  extern __shared__ uint8_t smem_raw[];
+  DecodeSmem<NR>& s = *reinterpret_cast<DecodeSmem<NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t t = blockIdx.x, h = blockIdx.y;
-  if (t < p.ro[0] || t >= p.ro[p.B]) return;
-  uint32_t lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (p.ro[mid] <= t) lo = mid; else hi = mid;
-  }
-  const uint32_t i = t - p.ro[lo], prior = p.lens[lo];
-  const uint64_t keys = static_cast<uint64_t>(prior) + (p.causal ? i + 1 : p.ro[lo + 1] - p.ro[lo]);
-  // Lane's words of four codes: 32 w + lane for w < 4, and 128 + lane (lanes < 16).
-  float q[20], acc[16];
-#pragma unroll
-  for (int w = 0; w < 5; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = 4 * (32 * w + lane) + e;
-      q[4 * w + e] = d < kWidth ? __uint_as_float(static_cast<uint32_t>(p.q[t * p.q_tok + h * p.q_head + d]) << 16) : 0.f;
+  volatile uint32_t* abort = &s.abort_flag;
+  // Scratch of the prologue, in the place of the queries.
+  struct Prologue {
+    unsigned long long warp_sum[kDecThreads / 32], at;
+    uint32_t b;
+  };
+  Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
+  if (threadIdx.x == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < R::kSlots; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
     }
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < R::kRopeSlots; ++i) {
+      mbar_init(smem_u32(&s.rope_full[i]), 1);
+      mbar_init(smem_u32(&s.rope_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.s_full[i]), 1);
+      mbar_init(smem_u32(&s.s_empty[i]), 8);   // the eight softmax warps
+    }
+    mbar_init(smem_u32(&s.q_full), 8);
+    mbar_init(smem_u32(&s.p_full), 8);
+    mbar_init(smem_u32(&s.pv_done), 1);
+    mbar_init(smem_u32(&s.drain), 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&p.tm_latent);
+    tma_prefetch_desc(&p.tm_rope);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s.tmem_base), 512);
+    tmem_relinquish();
+  }
+  // ---- this CTA's share: prefix sums of the sequences' units
+  const uint32_t per = (p.B + kDecThreads - 1) / kDecThreads;
+  const uint32_t b0 = min(p.B, threadIdx.x * per), b1 = min(p.B, b0 + per);
+  unsigned long long mine = 0;
   uint32_t bad = 0;
-  for (uint64_t j = warp; j < keys; j += kDecWarps) {
-    const uint64_t col = j / p.P;
-    if (col >= p.max_pages) { bad |= MLA_DEVICE_STATUS_BAD_COLUMN; continue; }
-    const uint32_t page = p.page_table[lo * p.pt_stride + col];
-    if (page >= p.num_pages) { bad |= MLA_DEVICE_STATUS_BAD_PAGE; continue; }
-    const uint32_t slot = static_cast<uint32_t>(j - col * p.P);
-    const uint32_t* row = reinterpret_cast<const uint32_t*>(p.cache + page * p.page_bytes + slot * p.tok_bytes);
-    const float sc = p.scales[p.per_token ? static_cast<long long>(page) * p.P + slot : 0];
-    float c[20], x = 0.f;
-#pragma unroll
-    for (int w = 0; w < 5; ++w) {
-      const uint32_t u = w < 4 || lane < 16 ? __ldg(row + 32 * w + lane) : 0u;
-      e4m3x4_to_f32(u, c[4 * w], c[4 * w + 1], c[4 * w + 2], c[4 * w + 3]);
-    }
-#pragma unroll
-    for (int e = 0; e < 20; ++e) x = fmaf(q[e], c[e], x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    x *= sc * p.sl2;
-    const float mn = fmaxf(m, x);
-    const float cr = m == mn ? 1.f : exp2f(m - mn), e2 = exp2f(x - mn);
-    m = mn;
-    l = l * cr + e2;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = acc[e] * cr + e2 * sc * c[e];
+  for (uint32_t b = b0; b < b1; ++b) {
+    const Seq q = sequence<NR>(p, b);
+    mine += static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
+    if (p.ro[b + 1] < p.ro[b] || p.ro[b + 1] > p.Tq) bad |= MLA_DEVICE_STATUS_BAD_OFFSETS;
+    if (q.n && static_cast<uint64_t>(q.prior) + q.n > p.max_keys) bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
   }
-  if (bad && lane == 0 && p.status) atomicOr(p.status, bad);
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+  if (bad && p.status && blockIdx.x == 0) atomicOr(p.status, bad);
+  unsigned long long incl = mine;
 #pragma unroll
-  for (int w = 0; w < 4; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) so[warp][4 * (32 * w + lane) + e] = acc[4 * w + e];
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) pro.warp_sum[warp] = incl;
+  tc_fence_before();
   __syncthreads();
-  float mx = -INFINITY, tot = 0.f;
-  for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, sm[w]);
-  for (int w = 0; w < kDecWarps; ++w)
-    if (sl[w] != 0.f) tot += sl[w] * exp2f(sm[w] - mx);
-  for (int d = threadIdx.x; d < kLatent; d += blockDim.x) {
-    float o = 0.f;
-    for (int w = 0; w < kDecWarps; ++w)
-      if (sl[w] != 0.f) o += so[w][d] * exp2f(sm[w] - mx);
-    p.out[t * p.o_tok + h * p.o_head + d] = static_cast<uint16_t>(pack_bf16x2(tot != 0.f ? o / tot : 0.f, 0.f));
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  unsigned long long before = 0, units = 0;
+  for (int w = 0; w < kDecThreads / 32; ++w) {
+    if (w < warp) before += pro.warp_sum[w];
+    units += pro.warp_sum[w];
   }
-  if (threadIdx.x == 0 && p.lse)
-    p.lse[t * p.l_tok + h * p.l_head] = tot != 0.f ? mx * kLn2 + logf(tot) : -INFINITY;
+  // CTAs with a share: all, or the first of them when there are fewer units.
+  const uint32_t ctas = static_cast<uint32_t>(min(static_cast<unsigned long long>(gridDim.x), units));
+  const unsigned long long u0 = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
+  const unsigned long long u1 = blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
+  unsigned long long start = before + incl - mine;
+  if (u0 < u1 && start <= u0 && u0 < start + mine) {
+    for (uint32_t b = b0; b < b1; ++b) {
+      const Seq q = sequence<NR>(p, b);
+      const unsigned long long here = static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
+      if (u0 < start + here) {
+        pro.b = b;
+        pro.at = u0 - start;
+        break;
+      }
+      start += here;
+    }
+  }
+  __syncthreads();
+  Share sh;
+  sh.b = u0 < u1 ? pro.b : p.B;
+  sh.at = u0 < u1 ? pro.at : 0;
+  sh.left = u1 - u0;
+  __syncthreads();     // the scratch becomes query space
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
+    if (warp == 1 && lane == 0) decode_mma<NR>(s, p, sh, tmem, abort);
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 128 x 88 + 256 x 208 = 384 x 168
+    decode_softmax<NR>(s, p, sh, units, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && s.abort_flag && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+}
+
+// ------------------------------------------------------------ joining parts
+// Row r of the row tile that CTA c begins and others end: out = sum of the
+// parts' O in units of the largest reference, over their l.  Four groups of 128
+// threads take every fourth part, four dims a thread.
+__global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, uint32_t nr) {
+  __shared__ float so[4][kLatent];
+  __shared__ float sl[4];
+  const uint32_t c = blockIdx.x, r = blockIdx.y;
+  const PartHeader h = p.headers[c];
+  if (!h.valid) return;
+  const uint32_t lo = p.ro[h.b], n = p.ro[h.b + 1] - lo;
+  const uint64_t row = static_cast<uint64_t>(h.rt) * nr + r;
+  if (row >= static_cast<uint64_t>(n) * p.H) return;
+  const uint32_t parts = h.last_cta - c + 1;
+  auto slot = [&](uint32_t i) { return 2 * (c + i) + (i == 0 ? 1u : 0u); };
+  const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
+  float m = -INFINITY;
+  for (uint32_t i = t & 31; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(slot(i)) * 2 * kMaxRows + r]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (uint32_t i = group; i < parts; i += 4) {
+    const size_t s = slot(i);
+    const float mi = p.part_ml[s * 2 * kMaxRows + r], li = p.part_ml[(s * 2 + 1) * kMaxRows + r];
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * kMaxRows + r) * kLatent + 4 * t);
+    const float f = li == 0.f ? 0.f : exp2f(mi - m);
+    if (li != 0.f) {
+      l = fmaf(li, f, l);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+  }
+  *reinterpret_cast<float4*>(&so[group][4 * t]) = acc;
+  if (t == 0) sl[group] = l;
+  __syncthreads();
+  const float total = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const uint32_t tok = static_cast<uint32_t>(row / p.H), head = static_cast<uint32_t>(row - static_cast<uint64_t>(tok) * p.H);
+  const int d = threadIdx.x;
+  const float o = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
+  p.out[(lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + d] =
+      static_cast<uint16_t>(pack_bf16x2(total != 0.f ? o * (0x1p-36f / total) : 0.f, 0.f));
+  if (d == 0 && p.lse)
+    p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
+        total != 0.f ? (m + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
+}
+
+constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 256;
+constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 2 * kMaxRows;
+constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * kLatent;
+
+template <int NR>
+mla_status_t launch_decode(const DecodeParams& p, int dev, int sms, int slot, cudaStream_t stream) {
+  const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR>);
+  const int smem = static_cast<int>(sizeof(DecodeSmem<NR>) + 1024);
+  mla_status_t st;
+  if ((st = check_registers(kernel, kDecRegs, dev, slot)) != MLA_OK) return st;
+  if ((st = set_max_dynamic_smem(kernel, smem, dev, slot)) != MLA_OK) return st;
+  const uint32_t ctas = std::min<uint32_t>(static_cast<uint32_t>(sms), kMaxCtas);
+  decode_kernel<NR><<<ctas, kDecThreads, smem, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+  decode_join_kernel<<<dim3(ctas, NR), 512, 0, stream>>>(p, NR);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
+  return MLA_OK;
 }
 
 }  // namespace
 }  // namespace mla
 
-extern "C" size_t mla_decode_latent_workspace_size(void) { return 256; }
+extern "C" size_t mla_decode_latent_workspace_size(void) { return mla::kWorkspace; }
 
 extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
                                           const mla_tensor_t* cache, const mla_tensor_t* page_table,
@@ -166,6 +905,18 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   if (Tq == 0) return MLA_OK;
   DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(kWidth), static_cast<uint64_t>(NP * P)};
+    const uint64_t str[1] = {static_cast<uint64_t>(cache->stride[1])};
+    const uint32_t box[2] = {128, 1}, rope_box[2] = {64, 1};   // row gathers take a one-row box
+    if ((st = encode_tiled(&p.tm_latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B, "cache")) != MLA_OK)
+      return st;
+    if ((st = encode_tiled(&p.tm_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, rope_box,
+                           CU_TENSOR_MAP_SWIZZLE_64B, "cache")) != MLA_OK)
+      return st;
+  }
   p.out = static_cast<uint16_t*>(out->data);
   p.o_tok = out->stride[0];
   p.o_head = out->stride[1];
@@ -175,9 +926,6 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   p.q = static_cast<const uint16_t*>(q->data);
   p.q_tok = q->stride[0];
   p.q_head = q->stride[1];
-  p.cache = static_cast<const uint8_t*>(cache->data);
-  p.page_bytes = cache->stride[0];
-  p.tok_bytes = cache->stride[1];
   p.scales = cache->scale;
   p.per_token = cache->scale_gran == MLA_SCALE_PER_TOKEN;
   p.page_table = static_cast<const uint32_t*>(page_table->data);
@@ -185,6 +933,10 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   p.ro = row_offsets;
   p.lens = cache_lens;
   p.status = status;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.headers = reinterpret_cast<PartHeader*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + kMlBytes);
   p.sl2 = scale * 1.4426950408889634f;
   p.causal = mask == MLA_MASK_CAUSAL;
   p.Tq = static_cast<uint32_t>(Tq);
@@ -193,8 +945,9 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   p.P = static_cast<uint32_t>(P);
   p.num_pages = static_cast<uint32_t>(NP);
   p.max_pages = static_cast<uint32_t>(page_table->shape[1]);
-  decode_kernel<<<dim3(p.Tq, p.H), kDecWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-  return MLA_OK;
+  p.max_keys = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(P) * p.max_pages, 0x7FFFFF00ull));
+  // 32-row tiles where an average sequence's queries fit one.
+  const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return rows <= 32 ? launch_decode<32>(p, dev, sms, 13, s) : launch_decode<64>(p, dev, sms, 14, s);
 }

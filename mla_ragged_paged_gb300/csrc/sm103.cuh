@@ -314,6 +314,13 @@ __device__ __forceinline__ uint64_t sw128_desc_at(uint32_t saddr) {
   return kSw128DescBase | static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
 }
 
+// The same for tiles with 64-byte rows and 64-byte swizzle: 8-row groups are
+// 512 bytes apart.
+constexpr uint64_t kSw64DescBase = (1ull << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+__device__ __forceinline__ uint64_t sw64_desc_at(uint32_t saddr) {
+  return kSw64DescBase | static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+}
+
 // Instruction descriptor: fp32 accumulate, A/B format code `fmt` (kind::f16:
 // 1 = bf16; kind::f8f6f4: 0 = e4m3), A K-major, B K-major or MN-major.
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t M, uint32_t N, uint32_t fmt,
@@ -439,6 +446,23 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// A pair of f16 values as two pairs of e4m3 codes, x = first + second up to
+// the rounding of the second: eight significant bits where |x| >= 2^-2.
+__device__ __forceinline__ void two_terms_e4m3(uint32_t x, uint32_t& first, uint32_t& second) {
+  asm("{\n .reg .b16 a, b;\n .reg .b32 v, r;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 v, a;\n"
+      " sub.rn.f16x2 r, %2, v;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 b, r;\n"
+      " cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}\n"
+      : "=r"(first), "=r"(second)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
