@@ -24,12 +24,15 @@
 //
 // Softmax.  A thread owns one key and half the rows of the tile, so the key's
 // scale is a scalar of the thread: with y = x + log2(s_j) (log2 units) the weight
-// that multiplies the codes is w_j = 2^(y_j - mu + 6) <= 2^8.5 and the one that
+// that multiplies the codes is w_j = 2^(y_j - mu + 7) <= 2^8.5 and the one that
 // is summed is w_j / s_j.  e4m3 loses what lies below 2^-10, so the reference mu
-// of a row follows the tiles in both directions: it moves when the tile's
-// maximum leaves [mu - 5, mu + 2.5], and O is then rescaled in tensor memory.
-// A key far above the rest (the first token often is) thus does not cost the
-// others their precision.
+// of a row follows the tiles in both directions, and the row's O is then
+// rescaled in tensor memory: up at once when a key passes mu + 1.5, down when a
+// tile's maximum is below mu - 8, or below mu - 4 twice.  A key far above the
+// rest (the first token often is) thus does not cost the others their precision.
+// Whether some key passes is one vote of the warpgroup; the maxima themselves
+// (transposed through the warps, about three times the vote's time) are only
+// formed in the first tiles, in every fourth one and after a change.
 //
 // Work.  The units are (sequence, row tile, 128 keys) in that order; each CTA,
 // one per SM, takes an equal contiguous share, however long the sequences are.
@@ -59,12 +62,15 @@ constexpr int kDecRegs = 168;
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
-constexpr float kShift = 6.f;                 // w = 2^(y - mu + kShift)
-constexpr float kRaise = 2.5f, kLower = 5.f;  // mu moves when the tile's maximum is that far off
+constexpr float kShift = 7.f;                 // w = 2^(y - mu + kShift)
+constexpr float kRaise = 1.5f;                // mu rises when a key is that far above it
+constexpr float kLower = 4.f, kDrop = 8.f;    // and falls when two maxima, or one, are that far below
+constexpr uint32_t kLook = 4;                 // the maxima are formed in every kLook-th tile
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
 // The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
 // 1e27 neither end leaves fp32.
 constexpr float kSumShift = 30.f;
+constexpr float kUnit = 0x1p-37f;             // 2^-(kShift + kSumShift): out = O / l in these units
 
 // Part of a row tile's result: slot 2 c of CTA c for one that continues an
 // earlier CTA's, 2 c + 1 for one that begins and does not end.
@@ -73,7 +79,7 @@ struct PartHeader {
 };
 
 struct DecodeParams {
-  CUtensorMap tm_latent, tm_rope;  // cache rows [slots, 576]; boxes 128 x 1 and 64 x 1
+  CUtensorMap tm_latent, tm_rope;  // cache rows [slots, 576]; boxes 128 x box_rows and 64 x box_rows
   uint16_t* out;
   long long o_tok, o_head;
   float* lse;
@@ -90,6 +96,7 @@ struct DecodeParams {
   float* part_ml;                  // [slots][2][kMaxRows]: mu, l
   float* part_o;                   // [slots][kMaxRows][512]
   float sl2;                       // scale * log2(e)
+  uint32_t box_rows;               // power of two that divides P, up to 128; 1: row gathers
   uint32_t per_token, causal, Tq, H, B, P, num_pages, max_pages, max_keys;
 };
 
@@ -194,20 +201,30 @@ __device__ __forceinline__ bool key_slot(const DecodeParams& p, uint32_t b, uint
 template <int NR>
 __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
   using R = Rows<NR>;
+  const bool boxed = p.box_rows > 1;
+  const uint32_t boxes = kKeys / p.box_rows;
   uint32_t tile = 0, bad = 0;
   bool alive = true;
   Segment g;
   while (alive && next_segment<NR>(p, sh, g)) {
     for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
-      // Rows 4 lane .. 4 lane + 3 of the tile; a row past the context or with a
-      // bad page is slot 0, whatever it holds (the softmax zeroes it).
+      // Boxes: lane l < 128 / box_rows takes the rows from box_rows * l; row
+      // gathers: rows 4 lane .. 4 lane + 3.  What lies past the context or on a
+      // bad page is read from slot 0 on, whatever it holds (the softmax zeroes it).
       int32_t rows[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t j = kt * kKeys + 4 * lane + e;
+      if (boxed) {
+        const uint32_t j = kt * kKeys + lane * p.box_rows;
         uint32_t slot = 0;
-        if (j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
-        rows[e] = static_cast<int32_t>(slot);
+        if (lane >= boxes || j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
+        rows[0] = static_cast<int32_t>(slot);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t j = kt * kKeys + 4 * lane + e;
+          uint32_t slot = 0;
+          if (j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
+          rows[e] = static_cast<int32_t>(slot);
+        }
       }
       for (int c = 0; c < 5 && alive; ++c) {
         const uint32_t pos = c < 4 ? tile * 4 + c : tile;
@@ -219,10 +236,13 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
         const uint32_t bar = smem_u32(full);
         if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
         __syncwarp();
-        if (c < 4)
-          tma_gather4_2d(smem_u32(s.chunk[st]) + lane * 512u, &p.tm_latent, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
-        else
-          tma_gather4_2d(smem_u32(s.rope[st]) + lane * 256u, &p.tm_rope, bar, kLatent, rows[0], rows[1], rows[2], rows[3]);
+        const uint32_t dst = c < 4 ? smem_u32(s.chunk[st]) : smem_u32(s.rope[st]);
+        const uint32_t row_bytes = c < 4 ? 128u : 64u;
+        const CUtensorMap* map = c < 4 ? &p.tm_latent : &p.tm_rope;
+        if (!boxed)
+          tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
+        else if (lane < boxes)
+          tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * 128, rows[0]);
       }
     }
   }
@@ -333,12 +353,6 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
   if constexpr (N == 32) tmem_ld_32x32b_x32(addr, r);
   else tmem_ld_32x32b_x16(addr, r);
 }
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_st_32x32b_x32(addr, r);
-  else tmem_st_32x32b_x16(addr, r);
-}
-
 // The queries of a row tile as two e4m3 terms, rows t1 at r and t2 at NR + r of
 // the K-major operand; col_factor[r] takes the row's power of two back.
 template <int NR>
@@ -447,7 +461,8 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
                       : g.s.keys;
     };
     const uint32_t shared = seen_by(tok0), end = seen_by(tok1);
-    float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
+    float mu = -INFINITY, peak = -INFINITY, last = INFINITY;  // of row r0 + my_row
+    uint32_t look = g.kt0 + kLook;                       // form the maxima in all tiles before this one
     float l[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = 0.f;
@@ -499,39 +514,62 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         for (int i = 0; i < N; ++i)
           if (j > g.s.prior + static_cast<uint32_t>((first_row + r0 + i) / p.H)) y[i] = -INFINITY;
       }
-      // ---- the tile's maximum of every row, and the row's reference
-      const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
-      s.warp_red[group][quarter][lane] = wm;
-      named_bar_sync(bar, 128);
-      const float tm = fmaxf(fmaxf(s.warp_red[group][0][lane], s.warp_red[group][1][lane]),
-                             fmaxf(s.warp_red[group][2][lane], s.warp_red[group][3][lane]));
-      // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
-      float next = mu;
-      if (tm > mu + kRaise || (tm < mu - kLower && tm > -INFINITY)) next = fmaxf(rintf(tm), peak - kDepth);
-      peak = fmaxf(peak, next);
-      const float factor = mu == next ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fmaxf(mu - next, -127.f))) << 23);
-      mu = next;
-      if (quarter == 0 && lane < N) s.row_val[group][lane] = mu == -INFINITY ? -kShift : mu - kShift;
-      const bool rescale = __any_sync(0xffffffffu, factor != 1.f);
-      named_bar_sync(bar, 128);
-      if (rescale) {
+      // ---- the rows' references: formed anew, or still good for every key?
+      bool form = kt < look || (kt - g.kt0) % kLook == 0;
+      if (!form) {
+        float over = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < N; ++i) l[i] *= __shfl_sync(0xffffffffu, factor, i);
-        if (kt != g.kt0) {
-          // Every product into O so far is done, the next one waits for this tile's P.
-          softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 4 * (R::kStacked ? 2 : 1); ++c) {
-            uint32_t o[N];
-            const uint32_t at = tmem + lane_at + (c & 3) * R::kOCols + (c >> 2) * NR + r0;
-            tmem_load<N>(at, o);
-            tmem_ld_wait();
+        for (int i = 0; i < N; i += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
+          over = max3(over, y[i] - m4.x, y[i + 1] - m4.y);
+          over = max3(over, y[i + 2] - m4.z, y[i + 3] - m4.w);
+        }
+        form = bar_any(bar, 128, over > kShift + kRaise);
+      }
+      if (form) {
+        const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
+        s.warp_red[group][quarter][lane] = wm;
+        named_bar_sync(bar, 128);
+        const float tm = fmaxf(fmaxf(s.warp_red[group][0][lane], s.warp_red[group][1][lane]),
+                               fmaxf(s.warp_red[group][2][lane], s.warp_red[group][3][lane]));
+        // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
+        float next = mu;
+        if (tm > mu + kRaise) next = fmaxf(rintf(tm), peak - kDepth);
+        else if (tm > -INFINITY && (tm < mu - kDrop || (tm < mu - kLower && last < mu - kLower)))
+          next = fmaxf(rintf(tm < mu - kDrop ? tm : fmaxf(tm, last)), peak - kDepth);
+        last = tm;
+        peak = fmaxf(peak, next);
+        const float factor =
+            mu == next ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fmaxf(mu - next, -127.f))) << 23);
+        const bool first = mu == -INFINITY;
+        mu = next;
+        if (quarter == 0 && lane < N) s.row_val[group][lane] = mu == -INFINITY ? -1e30f : mu - kShift;  // (no key yet: the first one passes)
+        uint32_t moved = __ballot_sync(0xffffffffu, factor != 1.f && !first);
+        if (N < 32) moved &= (1u << (N & 31)) - 1u;
+        named_bar_sync(bar, 128);
+        if (moved) {
+          look = kt + 2;
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, factor, i));
-            tmem_store<N>(at, o);
+          for (int i = 0; i < N; ++i) l[i] *= moved >> i & 1 ? __shfl_sync(0xffffffffu, factor, i) : 1.f;
+          if (kt != g.kt0) {
+            // Every product into O so far is done, the next one waits for this tile's P.
+            softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
+            tc_fence_after();
+            for (uint32_t left = moved; left; left &= left - 1) {
+              const int i = __ffs(left) - 1;
+              const float f = __shfl_sync(0xffffffffu, factor, i);
+              constexpr int kParts = 4 * (R::kStacked ? 2 : 1);
+              uint32_t o[kParts];
+              const uint32_t at = tmem + lane_at + r0 + i;
+#pragma unroll
+              for (int c = 0; c < kParts; ++c) o[c] = tmem_ld_32x32b_x1(at + (c & 3) * R::kOCols + (c >> 2) * NR);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < kParts; ++c)
+                tmem_st_32x32b_x1(at + (c & 3) * R::kOCols + (c >> 2) * NR, __float_as_uint(__uint_as_float(o[c]) * f));
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
         }
       }
       // ---- weights: two e4m3 terms per row
@@ -612,7 +650,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     const uint64_t row = first_row + r0 + my_row;
     if (quarter == 0 && lane < N) {
       // 2^(mu - kShift) and 2^(mu + kSumShift) are the units of O and l.
-      s.row_val[group][lane] = total != 0.f ? 0x1p-36f / total : 0.f;
+      s.row_val[group][lane] = total != 0.f ? kUnit / total : 0.f;
       if (!whole) {
         p.part_ml[(static_cast<size_t>(slot) * 2) * kMaxRows + r0 + lane] = mu;
         p.part_ml[(static_cast<size_t>(slot) * 2 + 1) * kMaxRows + r0 + lane] = total;
@@ -825,7 +863,7 @@ __global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, 
   const int d = threadIdx.x;
   const float o = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
   p.out[(lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + d] =
-      static_cast<uint16_t>(pack_bf16x2(total != 0.f ? o * (0x1p-36f / total) : 0.f, 0.f));
+      static_cast<uint16_t>(pack_bf16x2(total != 0.f ? o * (kUnit / total) : 0.f, 0.f));
   if (d == 0 && p.lse)
     p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
         total != 0.f ? (m + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
@@ -904,12 +942,15 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   if (Tq == 0) return MLA_OK;
+  int64_t box_rows = 1;
+  while (box_rows < kKeys && P % (2 * box_rows) == 0) box_rows *= 2;
+  if (box_rows < 8) box_rows = 1;   // row gathers take a one-row box
   DecodeParams p;
   memset(&p, 0, sizeof(p));
   {
     const uint64_t dims[2] = {static_cast<uint64_t>(kWidth), static_cast<uint64_t>(NP * P)};
     const uint64_t str[1] = {static_cast<uint64_t>(cache->stride[1])};
-    const uint32_t box[2] = {128, 1}, rope_box[2] = {64, 1};   // row gathers take a one-row box
+    const uint32_t rows = static_cast<uint32_t>(box_rows), box[2] = {128, rows}, rope_box[2] = {64, rows};
     if ((st = encode_tiled(&p.tm_latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, box,
                            CU_TENSOR_MAP_SWIZZLE_128B, "cache")) != MLA_OK)
       return st;
@@ -946,6 +987,10 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   p.num_pages = static_cast<uint32_t>(NP);
   p.max_pages = static_cast<uint32_t>(page_table->shape[1]);
   p.max_keys = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(P) * p.max_pages, 0x7FFFFF00ull));
+  // One box of as many rows as divide a page; pages without a multiple of the
+  // swizzle's eight rows take row gathers (measured: a 128-row tile in gathers
+  // of four costs the producer twice a tile's time).
+  p.box_rows = static_cast<uint32_t>(box_rows);
   // 32-row tiles where an average sequence's queries fit one.
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

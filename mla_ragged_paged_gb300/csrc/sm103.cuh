@@ -197,6 +197,17 @@ __device__ __forceinline__ void bulk_wait_group_all() {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Named barrier that returns whether any of the threads passed true.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t count, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
+}
 // Make this thread's generic-proxy shared-memory writes visible to the async
 // proxy (TMA, UMMA operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -349,6 +360,14 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       "%11, %12, %13, %14, %15}, [%16];"
       : MLA_R8(0), MLA_R8(8)
       : "r"(taddr));
+}
+__device__ __forceinline__ uint32_t tmem_ld_32x32b_x1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
+}
+__device__ __forceinline__ void tmem_st_32x32b_x1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
