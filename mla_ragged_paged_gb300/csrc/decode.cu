@@ -15,24 +15,27 @@
 // tensor time and a tile is read once for both:
 //   S^T [128 keys, rows]       = codes [128, 576] . Q^T
 //   O^T [4 x 128 dims, rows] += codes^T (512 dims) . P^T
-// Both products are e4m3, so the other operands are split into two e4m3 terms,
-// a value and what its rounding left: q (scaled by a power of two per row) is
-// reproduced exactly, a bf16 value having eight significant bits and each term
-// four; a softmax weight keeps eight bits, like bf16.  Sums are fp32 in tensor
-// memory.  The terms of q are stacked as 2 x rows columns of one product; those
-// of P too for 32-row tiles, else they are two products into one O.
+// Both products are of 8-bit operands, so q and the softmax weights are split
+// into two terms, a value and what its rounding left.  q, scaled by a power of
+// two per row, is reproduced exactly: a bf16 value has eight significant bits,
+// each e4m3 term four; its terms are stacked as 2 x rows columns of one product.
+// A weight is e4m3 + e5m2 (seven significant bits, down to 2^-17), two products
+// into one O, and the sum that divides O is of the weights as the products see
+// them, so that a row which hangs on one key is exact.  (lse takes the unrounded
+// sum.)  Sums are fp32, in tensor memory.
 //
 // Softmax.  A thread owns one key and half the rows of the tile, so the key's
 // scale is a scalar of the thread: with y = x + log2(s_j) (log2 units) the weight
 // that multiplies the codes is w_j = 2^(y_j - mu + 7) <= 2^8.5 and the one that
-// is summed is w_j / s_j.  e4m3 loses what lies below 2^-10, so the reference mu
-// of a row follows the tiles in both directions, and the row's O is then
-// rescaled in tensor memory: up at once when a key passes mu + 1.5, down when a
-// tile's maximum is below mu - 8, or below mu - 4 twice.  A key far above the
-// rest (the first token often is) thus does not cost the others their precision.
-// Whether some key passes is one vote of the warpgroup; the maxima themselves
-// (transposed through the warps, about three times the vote's time) are only
-// formed in the first tiles, in every fourth one and after a change.
+// is summed is w_j / s_j.  The reference mu of a row rises when a key passes
+// mu + 1.5, to 2 above the tile's maximum, so that random maxima seldom pass
+// again; O is then rescaled in tensor memory.  A weight's error is at most
+// 2^-17, which is 2^-22 of the largest weight or less: 131 072 keys of that size
+// together move a row by less than a part in 32, and when all keys of a tile
+// are below mu - 12 (behind a first token far above the rest, say) mu falls to
+// them.  Whether some key passes is one vote of the warpgroup; the maxima
+// themselves (transposed through the warps) are only formed in the first two
+// tiles, in every eighth one and after a change.
 //
 // Work.  The units are (sequence, row tile, 128 keys) in that order; each CTA,
 // one per SM, takes an equal contiguous share, however long the sequences are.
@@ -57,15 +60,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kKeys = 128;               // keys per tile
 constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent dims
 constexpr uint32_t kRopeBytes = kKeys * 64;
-constexpr int kDecThreads = 384;              // producer, UMMA, two idle warps; two softmax warpgroups
+constexpr int kDecThreads = 384;              // producer, three UMMA issuers; two softmax warpgroups
 constexpr int kDecRegs = 168;
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
 constexpr float kShift = 7.f;                 // w = 2^(y - mu + kShift)
-constexpr float kRaise = 1.5f;                // mu rises when a key is that far above it
-constexpr float kLower = 4.f, kDrop = 8.f;    // and falls when two maxima, or one, are that far below
-constexpr uint32_t kLook = 4;                 // the maxima are formed in every kLook-th tile
+constexpr float kRaise = 1.5f;                // mu rises when a key is that far above it,
+constexpr float kDrop = 12.f;                 // and falls when a tile's maximum is that far below it,
+constexpr float kMargin = 2.f;                // in both cases to that far above the maximum
+constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
+constexpr uint32_t kAhead = 3;                // tiles the producer prefetches into L2
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
 // The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
 // 1e27 neither end leaves fp32.
@@ -93,7 +98,7 @@ struct DecodeParams {
   const uint32_t* lens;
   uint32_t* status;
   PartHeader* headers;             // [2 * kMaxCtas]
-  float* part_ml;                  // [slots][2][kMaxRows]: mu, l
+  float* part_ml;                  // [slots][3][kMaxRows]: mu, the sum of the weights, and as the products see them
   float* part_o;                   // [slots][kMaxRows][512]
   float sl2;                       // scale * log2(e)
   uint32_t box_rows;               // power of two that divides P, up to 128; 1: row gathers
@@ -102,30 +107,29 @@ struct DecodeParams {
 
 template <int NR>
 struct Rows {
-  static constexpr bool kStacked = NR <= 32;      // both terms of P in one product
   static constexpr int kCols = NR / 2;            // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
-  static constexpr uint32_t kPTerm = kKeys * 64;  // one P operand: a 64-byte row per key
-  static constexpr int kPTerms = kStacked ? 1 : 2;
-  static constexpr int kSlots = NR <= 32 ? 10 : 8;
-  static constexpr int kRopeSlots = NR <= 32 ? 2 : 1;
-  static constexpr uint32_t kOCols = 64;          // tensor-memory columns of 128 dims of O^T
+  // P: a row of codes per key.  64 rows: an array of 64-byte rows per term; 32
+  // rows: both terms side by side in one.
+  static constexpr uint32_t kPBytes = kKeys * 2 * NR;
+  static constexpr uint32_t kPTerm = NR == 64 ? kKeys * 64 : 32;  // bytes from the first term to the second
+  static constexpr int kRopeSlots = NR <= 32 ? 2 : 1;   // (what fits beside two tiles of latent chunks)
 };
 
 template <int NR>
 struct __align__(1024) DecodeSmem {
   using R = Rows<NR>;
-  uint8_t chunk[R::kSlots][kChunk];
+  uint8_t chunk[2][4][kChunk];
   uint8_t rope[R::kRopeSlots][kRopeBytes];
   uint8_t q[4][R::kQChunk];
   uint8_t q_rope[2 * NR * 64];
-  uint8_t p[R::kPTerms][R::kPTerm];
+  uint8_t p[R::kPBytes];
   float warp_red[2][4][32];
   float row_val[2][32];
   float col_factor[NR];
-  uint64_t full[R::kSlots], empty[R::kSlots];
+  uint64_t full[2][4], empty[2][4];
   uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
-  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain;
+  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain[3];
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
@@ -181,20 +185,17 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, S
   return false;
 }
 
-// The slot of key j of sequence b; false (and a status bit) for a bad page.
-__device__ __forceinline__ bool key_slot(const DecodeParams& p, uint32_t b, uint32_t j, uint32_t& slot, uint32_t& bad) {
+// A key's place in the cache, in two steps so that the page-table read is not
+// waited for where it is issued: the page id (kNoPage past the table or past
+// the keys), and then the slot.
+constexpr uint32_t kNoPage = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t page_of(const DecodeParams& p, uint32_t b, uint32_t j, uint32_t keys) {
   const uint32_t col = j / p.P;
-  if (col >= p.max_pages) {
-    bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
-    return false;
-  }
-  const uint32_t page = __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col);
-  if (page >= p.num_pages) {
-    bad |= MLA_DEVICE_STATUS_BAD_PAGE;
-    return false;
-  }
-  slot = page * p.P + (j - col * p.P);
-  return true;
+  return j < keys && col < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col) : kNoPage;
+}
+__device__ __forceinline__ bool slot_of(const DecodeParams& p, uint32_t page, uint32_t j, uint32_t& slot) {
+  slot = page < p.num_pages ? page * p.P + j % p.P : 0u;
+  return page < p.num_pages;
 }
 
 // ------------------------------------------------------------ producer
@@ -207,36 +208,63 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   bool alive = true;
   Segment g;
   while (alive && next_segment<NR>(p, sh, g)) {
+    // Boxes: lane l < 128 / box_rows takes the rows from box_rows * l; row
+    // gathers: rows 4 lane .. 4 lane + 3.  What lies past the context or on a
+    // bad page is read from slot 0 on, whatever it holds (the softmax zeroes it).
+    const uint32_t first = boxed ? lane * p.box_rows : 4 * lane;
+    const bool mine = !boxed || lane < boxes;
+    auto look_up = [&](uint32_t kt, int e) {
+      return mine && kt < g.kt1 ? page_of(p, g.b, kt * kKeys + first + e, g.s.keys) : kNoPage;
+    };
+    // Boxes: page[i] is that of tile kt + i, the reads running one tile ahead of
+    // the L2 prefetch, which runs kAhead tiles ahead of the loads: the two
+    // tiles of shared memory alone do not cover the latency of HBM.  Row
+    // gathers: page[e] is that of row e of the next tile.
+    uint32_t page[kAhead + 2];
+    auto prefetch = [&](uint32_t kt, uint32_t pg) {
+      uint32_t slot;
+      if (!slot_of(p, pg, kt * kKeys + first, slot)) return;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, static_cast<int32_t>(slot));
+      tma_prefetch_2d(&p.tm_rope, kLatent, static_cast<int32_t>(slot));
+    };
+    if (boxed) {
+#pragma unroll
+      for (uint32_t i = 0; i < kAhead + 1; ++i) page[i] = look_up(g.kt0 + i, 0);
+#pragma unroll
+      for (uint32_t i = 1; i < kAhead; ++i) prefetch(g.kt0 + i, page[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) page[e] = look_up(g.kt0, e);
+    }
     for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
-      // Boxes: lane l < 128 / box_rows takes the rows from box_rows * l; row
-      // gathers: rows 4 lane .. 4 lane + 3.  What lies past the context or on a
-      // bad page is read from slot 0 on, whatever it holds (the softmax zeroes it).
       int32_t rows[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t slot;
+        const uint32_t j = kt * kKeys + first + e;
+        if (!slot_of(p, page[e], j, slot) && mine && j < g.s.keys && (e == 0 || !boxed)) bad |= MLA_DEVICE_STATUS_BAD_PAGE;
+        rows[e] = static_cast<int32_t>(slot);
+      }
       if (boxed) {
-        const uint32_t j = kt * kKeys + lane * p.box_rows;
-        uint32_t slot = 0;
-        if (lane >= boxes || j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
-        rows[0] = static_cast<int32_t>(slot);
+        page[kAhead + 1] = look_up(kt + kAhead + 1, 0);
+        prefetch(kt + kAhead, page[kAhead]);
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead + 1; ++i) page[i] = page[i + 1];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t j = kt * kKeys + 4 * lane + e;
-          uint32_t slot = 0;
-          if (j >= g.s.keys || !key_slot(p, g.b, j, slot, bad)) slot = 0;
-          rows[e] = static_cast<int32_t>(slot);
-        }
+        for (int e = 0; e < 4; ++e) page[e] = look_up(kt + 1, e);
       }
       for (int c = 0; c < 5 && alive; ++c) {
-        const uint32_t pos = c < 4 ? tile * 4 + c : tile;
-        const uint32_t slots = c < 4 ? R::kSlots : R::kRopeSlots;
-        const uint32_t st = pos % slots;
-        uint64_t* full = c < 4 ? &s.full[st] : &s.rope_full[st];
-        uint64_t* empty = c < 4 ? &s.empty[st] : &s.rope_empty[st];
-        if (!(alive = mbar_wait(smem_u32(empty), ((pos / slots) & 1u) ^ 1u, abort))) break;
+        const uint32_t buf = tile & 1, rs = tile % R::kRopeSlots;
+        uint64_t* full = c < 4 ? &s.full[buf][c] : &s.rope_full[rs];
+        uint64_t* empty = c < 4 ? &s.empty[buf][c] : &s.rope_empty[rs];
+        const uint32_t phase = c < 4 ? tile >> 1 : tile / R::kRopeSlots;
+        if (!(alive = mbar_wait(smem_u32(empty), (phase & 1u) ^ 1u, abort))) break;
         const uint32_t bar = smem_u32(full);
         if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
         __syncwarp();
-        const uint32_t dst = c < 4 ? smem_u32(s.chunk[st]) : smem_u32(s.rope[st]);
+        const uint32_t dst = c < 4 ? smem_u32(s.chunk[buf][c]) : smem_u32(s.rope[rs]);
         const uint32_t row_bytes = c < 4 ? 128u : 64u;
         const CUtensorMap* map = c < 4 ? &p.tm_latent : &p.tm_rope;
         if (!boxed)
@@ -251,10 +279,11 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   if (*abort) {
     // Let the copies still in flight land before the CTA exits.
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1; i <= R::kSlots && i <= tile * 4 + 4; ++i) {
-      const uint32_t q = tile * 4 + 4 - i;
-      while (!mbar_try_wait(smem_u32(&s.full[q % R::kSlots]), (q / R::kSlots) & 1u))
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
+    for (uint32_t i = 0; i < 2 && i <= tile; ++i) {
+      const uint32_t q = tile - i;
+      for (int c = 0; c < 4; ++c)
+        while (!mbar_try_wait(smem_u32(&s.full[q & 1][c]), (q >> 1) & 1u))
+          if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
     }
     for (uint32_t i = 0; i < R::kRopeSlots && i <= tile; ++i) {
       const uint32_t q = tile - i;
@@ -264,64 +293,84 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   }
 }
 
-// ------------------------------------------------------------ UMMA issuer
+// ------------------------------------------------------------ UMMA issuers
+// Three threads in three warps: the scores, and two for halves of the output's
+// dims.  One UMMA takes its thread about 50 cycles to issue, and twice that
+// beside two softmax warps on the same scheduler, against 48 to 64 cycles of
+// tensor time: one thread could keep the tensor cores half busy.
 template <int NR>
-__device__ void decode_mma(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
+__device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
   using R = Rows<NR>;
   const uint32_t id_s = make_idesc(128, 2 * NR, 0, false);
-  // P.V: A = codes^T (dims contiguous: MN-major), B = P^T (rows contiguous: MN-major).
-  const uint32_t id_o = make_idesc(128, 64, 0, true) | (1u << 15);
+  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0][0])), q_desc = sw128_desc_at(smem_u32(s.q[0]));
   uint32_t tile = 0, segs = 0;
-  bool alive = true;
-  auto scores = [&](uint32_t t) {
-    if (!(alive = mbar_wait(smem_u32(&s.s_empty[t & 1]), ((t >> 1) & 1u) ^ 1u, abort))) return;
-    const uint32_t d = tmem + kColS + (t & 1) * (2 * NR);
-    for (uint32_t c = 0; c < 4; ++c) {
-      const uint32_t pos = t * 4 + c, st = pos % R::kSlots;
-      if (!(alive = mbar_wait(smem_u32(&s.full[st]), (pos / R::kSlots) & 1u, abort))) return;
-      tc_fence_after();
-      const uint64_t kd = sw128_desc_at(smem_u32(s.chunk[st])), qd = sw128_desc_at(smem_u32(s.q[c]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, (c | k) != 0);
-    }
-    const uint32_t st = t % R::kRopeSlots;
-    if (!(alive = mbar_wait(smem_u32(&s.rope_full[st]), (t / R::kRopeSlots) & 1u, abort))) return;
-    tc_fence_after();
-    const uint64_t kd = sw64_desc_at(smem_u32(s.rope[st])), qd = sw64_desc_at(smem_u32(s.q_rope));
-#pragma unroll
-    for (int k = 0; k < 2; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, 1u);
-    umma_commit(smem_u32(&s.rope_empty[st]));
-    umma_commit(smem_u32(&s.s_full[t & 1]));
-  };
   Segment g;
-  while (alive && next_segment<NR>(p, sh, g)) {
-    const uint32_t n = g.kt1 - g.kt0;
-    if (!(alive = mbar_wait(smem_u32(&s.q_full), segs & 1u, abort))) break;
+  while (next_segment<NR>(p, sh, g)) {
+    if (!mbar_wait(smem_u32(&s.q_full), segs & 1u, abort)) return;
     ++segs;
-    scores(tile);
-    for (uint32_t i = 0; i < n && alive; ++i, ++tile) {
-      if (i + 1 < n) scores(tile + 1);
-      if (!alive) break;
-      if (!(alive = mbar_wait(smem_u32(&s.p_full), tile & 1u, abort))) break;
-      tc_fence_after();
+    for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
+      const uint32_t par = tile & 1, phase = (tile >> 1) & 1u;
+      if (!mbar_wait(smem_u32(&s.s_empty[par]), phase ^ 1u, abort)) return;
+      const uint32_t d = tmem + kColS + par * (2 * NR);
+      const uint64_t kd0 = chunk_desc + par * (4 * kChunk >> 4);
+#pragma unroll 1
       for (uint32_t c = 0; c < 4; ++c) {
-        const uint32_t st = (tile * 4 + c) % R::kSlots;
-        const uint64_t vd = sw128_desc_at(smem_u32(s.chunk[st]));
+        if (!mbar_wait(smem_u32(&s.full[par][c]), phase, abort)) return;
+        tc_fence_after();
+        const uint64_t kd = kd0 + c * (kChunk >> 4), qd = q_desc + c * (R::kQChunk >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, (c | k) != 0);
+      }
+      const uint32_t st = tile % R::kRopeSlots;
+      if (!mbar_wait(smem_u32(&s.rope_full[st]), (tile / R::kRopeSlots) & 1u, abort)) return;
+      tc_fence_after();
+      const uint64_t kd = sw64_desc_at(smem_u32(s.rope[st])), qd = sw64_desc_at(smem_u32(s.q_rope));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, 1u);
+      umma_commit(smem_u32(&s.rope_empty[st]));
+      umma_commit(smem_u32(&s.s_full[par]));
+    }
+  }
+}
+
+// Chunks [c0, c0 + 2) of the output: A = codes^T (dims contiguous: MN-major), B =
+// P^T (rows contiguous: MN-major); the weights' second term is e5m2 (format 1 of B).
+template <int NR>
+__device__ void issue_output(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, uint32_t c0,
+                             volatile uint32_t* abort) {
+  using R = Rows<NR>;
+  const uint32_t id_o = make_idesc(128, NR, 0, true) | (1u << 15);
+  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0][c0])), p_desc = sw64_desc_at(smem_u32(s.p));
+  uint32_t tile = 0;
+  Segment g;
+  while (next_segment<NR>(p, sh, g)) {
+    for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
+      const uint32_t par = tile & 1;
+      if (!mbar_wait(smem_u32(&s.p_full), tile & 1u, abort)) return;
+      tc_fence_after();
+      const uint32_t more = kt != g.kt0;
+#pragma unroll 1
+      for (uint32_t c = 0; c < 2; ++c) {
+        const uint64_t vd = chunk_desc + par * (4 * kChunk >> 4) + c * (kChunk >> 4);
+        const uint32_t d = tmem + (c0 + c) * NR;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int term = 0; term < R::kPTerms; ++term)
-            umma_f8_ss(tmem + c * R::kOCols, vd + k * (32 * 128 >> 4), sw64_desc_at(smem_u32(s.p[term])) + k * (32 * 64 >> 4),
-                       id_o, (i | k | term) != 0);
-        umma_commit(smem_u32(&s.empty[st]));
+          for (int term = 0; term < 2; ++term)
+            umma_f8_ss(d, vd + k * (32 * 128 >> 4), p_desc + term * (R::kPTerm >> 4) + k * (32 * 64 >> 4),
+                       term ? id_o | 1u << 10 : id_o, term || k ? 1u : more);
+        umma_commit(smem_u32(&s.empty[par][c0 + c]));
       }
       umma_commit(smem_u32(&s.pv_done));
     }
   }
-  // No UMMA may still be in flight when tensor memory is released.
-  umma_commit(smem_u32(&s.drain));
+}
+
+// No UMMA of this thread may still be in flight when tensor memory is released.
+__device__ __forceinline__ void drain_umma(uint64_t* drain) {
+  umma_commit(smem_u32(drain));
   const uint64_t tw = global_timer_ns();
-  while (!mbar_try_wait(smem_u32(&s.drain), 0))
+  while (!mbar_try_wait(smem_u32(drain), 0))
     if (global_timer_ns() - tw > kWaitTimeoutNs) break;
 }
 
@@ -427,6 +476,22 @@ __device__ __forceinline__ void softmax_wait(uint32_t bar, uint32_t parity, vola
   mbar_wait(bar, parity, abort);
 }
 
+// Two neighbouring rows' weights as their two terms (codes in the low halves)
+// and as the products see them.
+__device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& first, uint32_t& second, float& q0, float& q1) {
+  const uint32_t w = pack_f16x2(w0, w1);
+  uint32_t seen;
+  asm("{\n .reg .b16 a, b;\n .reg .b32 v, r, u;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n cvt.rn.f16x2.e4m3x2 v, a;\n sub.rn.f16x2 r, %3, v;\n"
+      " cvt.rn.satfinite.e5m2x2.f16x2 b, r;\n cvt.rn.f16x2.e5m2x2 u, b;\n"
+      " add.rn.f16x2 %2, u, v;\n cvt.u32.u16 %0, a;\n cvt.u32.u16 %1, b;\n}\n"
+      : "=r"(first), "=r"(second), "=r"(seen)
+      : "r"(w));
+  asm("{\n .reg .f16 h0, h1;\n mov.b32 {h0, h1}, %2;\n cvt.f32.f16 %0, h0;\n cvt.f32.f16 %1, h1;\n}\n"
+      : "=f"(q0), "=f"(q1)
+      : "r"(seen));
+}
+
 template <int NR>
 __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, unsigned long long units, uint32_t ctas,
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
@@ -461,25 +526,29 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
                       : g.s.keys;
     };
     const uint32_t shared = seen_by(tok0), end = seen_by(tok1);
-    float mu = -INFINITY, peak = -INFINITY, last = INFINITY;  // of row r0 + my_row
-    uint32_t look = g.kt0 + kLook;                       // form the maxima in all tiles before this one
-    float l[N];
+    float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
+    uint32_t look = g.kt0 + 2;                           // form the maxima in all tiles before this one
+    float l[N], lq[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = 0.f;
-    auto fetch = [&](uint32_t kt, float& sc) -> bool {
-      const uint32_t j = kt * kKeys + key;
-      uint32_t slot, bad = 0;
-      sc = 1.f;
-      if (j >= end || !key_slot(p, g.b, j, slot, bad)) return false;
-      sc = __ldg(p.scales + (p.per_token ? slot : 0u));
-      return true;
+    for (int i = 0; i < N; ++i) l[i] = lq[i] = 0.f;
+    // The key's scale is two dependent reads away (page table, scale): the page
+    // is read two tiles ahead and the scale one tile ahead, so that neither is
+    // waited for.
+    auto look_up = [&](uint32_t kt) { return kt < g.kt1 ? page_of(p, g.b, kt * kKeys + key, end) : kNoPage; };
+    auto scale_of = [&](uint32_t kt, uint32_t page, float& sc) {
+      uint32_t slot;
+      const bool ok = slot_of(p, page, kt * kKeys + key, slot);
+      sc = ok ? __ldg(p.scales + (p.per_token ? slot : 0u)) : 1.f;
+      return ok;
     };
     float sc_next;
-    bool ok_next = fetch(g.kt0, sc_next);
+    bool ok_next = scale_of(g.kt0, look_up(g.kt0), sc_next);
+    uint32_t page_after = look_up(g.kt0 + 1);
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
       const float sc = sc_next;
       const bool ok = ok_next;
-      if (kt + 1 < g.kt1) ok_next = fetch(kt + 1, sc_next);
+      ok_next = scale_of(kt + 1, page_after, sc_next);
+      page_after = look_up(kt + 2);
       const uint32_t j = kt * kKeys + key;
       const float ls = log2f(fmaxf(sc, 0x1p-120f));      // NaN and 0 give finite factors; the score carries the NaN
       const float to_sum = ex2_approx(-kShift - kSumShift - ls);
@@ -526,6 +595,8 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         }
         form = bar_any(bar, 128, over > kShift + kRaise);
       }
+      uint32_t moved = 0;
+      float factor = 1.f;
       if (form) {
         const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
         s.warp_red[group][quarter][lane] = wm;
@@ -534,45 +605,26 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
                                fmaxf(s.warp_red[group][2][lane], s.warp_red[group][3][lane]));
         // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
         float next = mu;
-        if (tm > mu + kRaise) next = fmaxf(rintf(tm), peak - kDepth);
-        else if (tm > -INFINITY && (tm < mu - kDrop || (tm < mu - kLower && last < mu - kLower)))
-          next = fmaxf(rintf(tm < mu - kDrop ? tm : fmaxf(tm, last)), peak - kDepth);
-        last = tm;
+        if (tm > mu + kRaise || (tm < mu - kDrop && tm > -INFINITY)) next = fmaxf(rintf(tm) + kMargin, peak - kDepth);
         peak = fmaxf(peak, next);
-        const float factor =
+        factor =
             mu == next ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fmaxf(mu - next, -127.f))) << 23);
         const bool first = mu == -INFINITY;
         mu = next;
         if (quarter == 0 && lane < N) s.row_val[group][lane] = mu == -INFINITY ? -1e30f : mu - kShift;  // (no key yet: the first one passes)
-        uint32_t moved = __ballot_sync(0xffffffffu, factor != 1.f && !first);
+        moved = __ballot_sync(0xffffffffu, factor != 1.f && !first);
         if (N < 32) moved &= (1u << (N & 31)) - 1u;
         named_bar_sync(bar, 128);
         if (moved) {
           look = kt + 2;
 #pragma unroll
-          for (int i = 0; i < N; ++i) l[i] *= moved >> i & 1 ? __shfl_sync(0xffffffffu, factor, i) : 1.f;
-          if (kt != g.kt0) {
-            // Every product into O so far is done, the next one waits for this tile's P.
-            softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
-            tc_fence_after();
-            for (uint32_t left = moved; left; left &= left - 1) {
-              const int i = __ffs(left) - 1;
-              const float f = __shfl_sync(0xffffffffu, factor, i);
-              constexpr int kParts = 4 * (R::kStacked ? 2 : 1);
-              uint32_t o[kParts];
-              const uint32_t at = tmem + lane_at + r0 + i;
-#pragma unroll
-              for (int c = 0; c < kParts; ++c) o[c] = tmem_ld_32x32b_x1(at + (c & 3) * R::kOCols + (c >> 2) * NR);
-              tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < kParts; ++c)
-                tmem_st_32x32b_x1(at + (c & 3) * R::kOCols + (c >> 2) * NR, __float_as_uint(__uint_as_float(o[c]) * f));
-            }
-            tmem_st_wait();
+          for (int i = 0; i < N; ++i) {
+            const float f = __shfl_sync(0xffffffffu, factor, i);
+            if (moved >> i & 1) l[i] *= f, lq[i] *= f;
           }
         }
       }
-      // ---- weights: two e4m3 terms per row
+      // ---- weights: two terms per row
       uint32_t t1[N / 4], t2[N / 4];
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
@@ -584,17 +636,38 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         l[i + 2] = fmaf(w2, to_sum, l[i + 2]);
         l[i + 3] = fmaf(w3, to_sum, l[i + 3]);
         uint32_t a0, b0, a1, b1;
-        two_terms_e4m3(pack_f16x2(w0, w1), a0, b0);
-        two_terms_e4m3(pack_f16x2(w2, w3), a1, b1);
+        float q0, q1, q2, q3;
+        weight_terms(w0, w1, a0, b0, q0, q1);
+        weight_terms(w2, w3, a1, b1, q2, q3);
+        lq[i] = fmaf(q0, to_sum, lq[i]);
+        lq[i + 1] = fmaf(q1, to_sum, lq[i + 1]);
+        lq[i + 2] = fmaf(q2, to_sum, lq[i + 2]);
+        lq[i + 3] = fmaf(q3, to_sum, lq[i + 3]);
         t1[i / 4] = a0 | a1 << 16;
         t2[i / 4] = b0 | b1 << 16;
       }
-      // P is free once the previous tile's products are done.
+      // P and O are free once the previous tile's products are done.
       if (tile) softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
+      if (moved && kt != g.kt0) {
+        tc_fence_after();
+#pragma unroll 1
+        for (uint32_t left = moved; left; left &= left - 1) {
+          const int i = __ffs(left) - 1;
+          const float f = __shfl_sync(0xffffffffu, factor, i);
+          uint32_t o[4];
+          const uint32_t at = tmem + lane_at + r0 + i;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = tmem_ld_32x32b_x1(at + c * NR);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st_32x32b_x1(at + c * NR, __float_as_uint(__uint_as_float(o[c]) * f));
+        }
+        tmem_st_wait();
+      }
       {
         const uint32_t swz = (key >> 1) & 3;
-        uint8_t* row = s.p[0] + key * 64;
-        if constexpr (R::kStacked) {
+        uint8_t* row = s.p + key * 64;
+        if constexpr (NR == 32) {
           *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
           *reinterpret_cast<uint4*>(row + (((2 + group) ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
         } else {
@@ -613,10 +686,10 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         // see the NaN have NaN weights already: the scores read the same codes.)
         uint32_t nan = !ok;
         for (int c = 0; c < 4; ++c)   // (complete long ago: orders this thread after the copies)
-          softmax_wait(smem_u32(&s.full[(tile * 4 + c) % R::kSlots]), ((tile * 4 + c) / R::kSlots) & 1u, abort);
+          softmax_wait(smem_u32(&s.full[tile & 1][c]), (tile >> 1) & 1u, abort);
 #pragma unroll 1
         for (int c = 0; c < 4 && !nan; ++c) {
-          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[(tile * 4 + c) % R::kSlots] + key * 128);
+          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[tile & 1][c] + key * 128);
           for (int i = 0; i < 8; ++i) {
             const uint4 v = row[i];
             nan |= (((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -626,7 +699,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         if (nan) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint4* row = reinterpret_cast<uint4*>(s.chunk[(tile * 4 + c) % R::kSlots] + key * 128);
+            uint4* row = reinterpret_cast<uint4*>(s.chunk[tile & 1][c] + key * 128);
             for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -639,21 +712,27 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     // ---- the segment's result
     softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
     tc_fence_after();
-    const float wl = warp_transpose_reduce<N>(l, lane, add2);
-    s.warp_red[group][quarter][lane] = wl;
-    named_bar_sync(bar, 128);
-    const float total = (s.warp_red[group][0][lane] + s.warp_red[group][1][lane]) +
+    auto row_sum = [&](const float (&v)[N]) {
+      s.warp_red[group][quarter][lane] = warp_transpose_reduce<N>(v, lane, add2);
+      named_bar_sync(bar, 128);
+      const float sum = (s.warp_red[group][0][lane] + s.warp_red[group][1][lane]) +
                         (s.warp_red[group][2][lane] + s.warp_red[group][3][lane]);
+      named_bar_sync(bar, 128);
+      return sum;
+    };
+    const float total = row_sum(l), seen = row_sum(lq);
     const bool begins = g.kt0 == 0, ends = g.kt1 == g.s.key_tiles;
     const bool whole = begins && ends;
     const uint32_t slot = 2 * blockIdx.x + (begins ? 1 : 0);
     const uint64_t row = first_row + r0 + my_row;
     if (quarter == 0 && lane < N) {
       // 2^(mu - kShift) and 2^(mu + kSumShift) are the units of O and l.
-      s.row_val[group][lane] = total != 0.f ? kUnit / total : 0.f;
+      s.row_val[group][lane] = seen != 0.f ? kUnit / seen : 0.f;
       if (!whole) {
-        p.part_ml[(static_cast<size_t>(slot) * 2) * kMaxRows + r0 + lane] = mu;
-        p.part_ml[(static_cast<size_t>(slot) * 2 + 1) * kMaxRows + r0 + lane] = total;
+        float* ml = p.part_ml + static_cast<size_t>(slot) * 3 * kMaxRows + r0 + lane;
+        ml[0] = mu;
+        ml[kMaxRows] = total;
+        ml[2 * kMaxRows] = seen;
       } else if (p.lse && row < live) {
         const uint32_t tok = static_cast<uint32_t>(row / p.H);
         p.lse[(g.s.q0 + static_cast<long long>(tok)) * p.l_tok + static_cast<long long>(row - static_cast<uint64_t>(tok) * p.H) * p.l_head] =
@@ -664,17 +743,9 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[N];
-      const uint32_t at = tmem + lane_at + c * R::kOCols + r0;
+      const uint32_t at = tmem + lane_at + c * NR + r0;
       tmem_load<N>(at, o);
-      if constexpr (R::kStacked) {
-        uint32_t o2[N];
-        tmem_load<N>(at + NR, o2);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o2[i]));
-      } else {
-        tmem_ld_wait();
-      }
+      tmem_ld_wait();
       const uint32_t dim = c * 128 + key;
       if (whole) {
         uint32_t tok = static_cast<uint32_t>((first_row + r0) / p.H);
@@ -726,9 +797,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < R::kSlots; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&s.full[i >> 2][i & 3]), 1);
+      mbar_init(smem_u32(&s.empty[i >> 2][i & 3]), 1);
     }
     for (int i = 0; i < R::kRopeSlots; ++i) {
       mbar_init(smem_u32(&s.rope_full[i]), 1);
@@ -740,8 +811,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
     }
     mbar_init(smem_u32(&s.q_full), 8);
     mbar_init(smem_u32(&s.p_full), 8);
-    mbar_init(smem_u32(&s.pv_done), 1);
-    mbar_init(smem_u32(&s.drain), 1);
+    mbar_init(smem_u32(&s.pv_done), 2);        // both output issuers
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_latent);
     tma_prefetch_desc(&p.tm_rope);
@@ -804,7 +875,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
-    if (warp == 1 && lane == 0) decode_mma<NR>(s, p, sh, tmem, abort);
+    if (warp > 0 && lane == 0) {
+      if (warp == 1) issue_scores<NR>(s, p, sh, tmem, abort);
+      else issue_output<NR>(s, p, sh, tmem, 2 * (warp - 2), abort);
+      drain_umma(&s.drain[warp - 1]);
+    }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 128 x 88 + 256 x 208 = 384 x 168
@@ -825,7 +900,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
 // threads take every fourth part, four dims a thread.
 __global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, uint32_t nr) {
   __shared__ float so[4][kLatent];
-  __shared__ float sl[4];
+  __shared__ float sl[4], sq[4];
   const uint32_t c = blockIdx.x, r = blockIdx.y;
   const PartHeader h = p.headers[c];
   if (!h.valid) return;
@@ -836,19 +911,21 @@ __global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, 
   auto slot = [&](uint32_t i) { return 2 * (c + i) + (i == 0 ? 1u : 0u); };
   const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
   float m = -INFINITY;
-  for (uint32_t i = t & 31; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(slot(i)) * 2 * kMaxRows + r]);
+  for (uint32_t i = t & 31; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(slot(i)) * 3 * kMaxRows + r]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  float l = 0.f, lq = 0.f;
 #pragma unroll 4
   for (uint32_t i = group; i < parts; i += 4) {
     const size_t s = slot(i);
-    const float mi = p.part_ml[s * 2 * kMaxRows + r], li = p.part_ml[(s * 2 + 1) * kMaxRows + r];
+    const float* ml = p.part_ml + s * 3 * kMaxRows + r;
+    const float mi = ml[0], li = ml[kMaxRows], qi = ml[2 * kMaxRows];
     const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * kMaxRows + r) * kLatent + 4 * t);
-    const float f = li == 0.f ? 0.f : exp2f(mi - m);
     if (li != 0.f) {
+      const float f = exp2f(mi - m);
       l = fmaf(li, f, l);
+      lq = fmaf(qi, f, lq);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
@@ -856,21 +933,21 @@ __global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, 
     }
   }
   *reinterpret_cast<float4*>(&so[group][4 * t]) = acc;
-  if (t == 0) sl[group] = l;
+  if (t == 0) sl[group] = l, sq[group] = lq;
   __syncthreads();
-  const float total = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+  const float total = (sl[0] + sl[1]) + (sl[2] + sl[3]), seen = (sq[0] + sq[1]) + (sq[2] + sq[3]);
   const uint32_t tok = static_cast<uint32_t>(row / p.H), head = static_cast<uint32_t>(row - static_cast<uint64_t>(tok) * p.H);
   const int d = threadIdx.x;
   const float o = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
   p.out[(lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + d] =
-      static_cast<uint16_t>(pack_bf16x2(total != 0.f ? o * (kUnit / total) : 0.f, 0.f));
+      static_cast<uint16_t>(pack_bf16x2(seen != 0.f ? o * (kUnit / seen) : 0.f, 0.f));
   if (d == 0 && p.lse)
     p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
         total != 0.f ? (m + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
 }
 
 constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 256;
-constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 2 * kMaxRows;
+constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 3 * kMaxRows;
 constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * kLatent;
 
 template <int NR>
