@@ -7,6 +7,7 @@ missing or the device is unsupported the call raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -104,15 +105,16 @@ def load(path=LIB_PATH):
     lib.mla_up_project.restype = ctypes.c_int
     lib.mla_gather_up_project.argtypes = [pt, pt, pt, pt, pt, pt, vp, vp, u32, vp, vp]
     lib.mla_gather_up_project.restype = ctypes.c_int
-    lib.mla_rms_norm.argtypes = [pt, pt, pt, pt, pt, pt, pt, ctypes.c_float, vp]
+    # Descriptors of these calls are packed bytes (_pack), passed by address.
+    lib.mla_rms_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp]
     lib.mla_rms_norm.restype = ctypes.c_int
-    lib.mla_matmul_fp8.argtypes = [pt, pt, pt, pt, pt, vp, vp]
+    lib.mla_matmul_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     lib.mla_matmul_fp8.restype = ctypes.c_int
-    lib.mla_append_latent.argtypes = [pt, pt, pt, vp, vp, vp, vp]
+    lib.mla_append_latent.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     lib.mla_append_latent.restype = ctypes.c_int
     lib.mla_decode_latent_workspace_size.argtypes = []
     lib.mla_decode_latent_workspace_size.restype = ctypes.c_size_t
-    lib.mla_decode_latent.argtypes = [pt, pt, pt, pt, pt, vp, vp, ctypes.c_float, ctypes.c_int, vp, vp,
+    lib.mla_decode_latent.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, ctypes.c_int, vp, vp,
                                       ctypes.c_size_t, vp]
     lib.mla_decode_latent.restype = ctypes.c_int
     lib.mla_read_device_status.argtypes = [vp, ctypes.POINTER(u32), vp]
@@ -486,19 +488,36 @@ def merge(out, partial_out, partial_lse, row_offsets, buffer_row_offsets, stream
     return out
 
 
-def _ref(d):
-    return None if d is None else ctypes.byref(d)
+# The serving-step calls are a few microseconds of GPU work for one token, so
+# their marshalling is kept short: descriptors are packed as bytes in the layout
+# of MlaTensor (whose size the tests compare), devices and streams are read as
+# plain integers.
+_LAYOUT = {n: struct.Struct(f"=Qii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}xQi4x") for n in range(1, 5)}
 
 
-def _opt(t, dtype):
-    return None if t is None else describe(t, dtype)
+def _pack(t, dtype, scale=0, scale_gran=MLA_SCALE_NONE):
+    """An MlaTensor of CUDA tensor t (None: no descriptor) as bytes."""
+    if t is None:
+        return None
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors have 1 to 4 dimensions (got {tuple(shape)})")
+    return _LAYOUT[n].pack(t.data_ptr(), dtype, n, *shape, *t.stride(), scale, scale_gran)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _typed(t, what, *dtypes):
     """Refuse a tensor whose elements the call would read as another type."""
     if t is not None and t.dtype not in dtypes:
         raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-    return t
 
 
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
@@ -506,20 +525,36 @@ _INDEX = (torch.int32, torch.uint32)
 
 
 def _indices(t, what, numel):
-    """A packed device array of 32-bit indices."""
+    """The address of a packed device array of 32-bit indices."""
     _typed(t, what, *_INDEX)
     if t.numel() != numel or not t.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must hold {numel} packed elements (got {tuple(t.shape)})")
-    return t
+    return t.data_ptr()
 
 
-def _same_device(*tensors):
-    """Every tensor of a call lives on the device the call launches on."""
-    tensors = [_on_device(t) for t in tensors if t is not None]
-    dev = torch.cuda.current_device()
+def _status_word(t):
+    if t is not None and (t.numel() < 1 or t.element_size() < 4):
+        raise MlaError(MLA_ERR_INVALID_ARG, "status must hold a 32-bit word")
+    return _address(t)
+
+
+def _device_of(*tensors):
+    """The device index all given tensors share, which must be the current one:
+    the call launches there."""
+    dev = -1
     for t in tensors:
-        if t.device.index != dev:
-            raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on the current device cuda:{dev} (got {t.device})")
+        if t is None:
+            continue
+        at = t.get_device()
+        if at < 0:
+            _on_device(t)
+        if dev < 0:
+            dev = at
+            if dev != torch.cuda.current_device():
+                raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on the current device (got {t.device})")
+        elif at != dev:
+            raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on one device (got cuda:{dev} and {t.device})")
+    return dev
 
 
 def rms_norm(x, weight, eps, residual=None, residual_out=None, out=None, out_fp8=None, out_scales=None,
@@ -527,17 +562,19 @@ def rms_norm(x, weight, eps, residual=None, residual_out=None, out=None, out_fp8
     """mla_rms_norm: h = x + residual, residual_out = bf16(h), y = h * weight /
     sqrt(mean(h^2) + eps) as bf16 `out` and / or e4m3 `out_fp8` with one scale
     per 128 columns of a row in `out_scales`.  Returns the outputs given."""
-    _same_device(x, weight, residual, residual_out, out, out_fp8, out_scales)
+    dev = _device_of(x, weight, residual, residual_out, out, out_fp8, out_scales)
     bf16 = torch.bfloat16
-    for t, what in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (out, "out")):
-        _typed(t, what, bf16)
+    _typed(x, "x", bf16)
+    _typed(residual, "residual", bf16)
+    _typed(residual_out, "residual_out", bf16)
+    _typed(out, "out", bf16)
     _typed(weight, "weight", bf16, torch.float32)
     _typed(out_fp8, "out_fp8", *_FP8)
     _typed(out_scales, "out_scales", torch.float32)
-    _check(load().mla_rms_norm(_ref(_opt(out, MLA_DTYPE_BF16)), _ref(_opt(out_fp8, MLA_DTYPE_FP8_E4M3)),
-                               _ref(_opt(out_scales, MLA_DTYPE_F32)), _ref(_opt(x, MLA_DTYPE_BF16)),
-                               _ref(_opt(residual, MLA_DTYPE_BF16)), _ref(_opt(residual_out, MLA_DTYPE_BF16)),
-                               _ref(describe(weight, _dtype_code(weight))), float(eps), _stream(stream)))
+    _check(load().mla_rms_norm(_pack(out, MLA_DTYPE_BF16), _pack(out_fp8, MLA_DTYPE_FP8_E4M3),
+                               _pack(out_scales, MLA_DTYPE_F32), _pack(x, MLA_DTYPE_BF16),
+                               _pack(residual, MLA_DTYPE_BF16), _pack(residual_out, MLA_DTYPE_BF16),
+                               _pack(weight, _dtype_code(weight)), eps, _raw_stream(stream, dev)))
     return tuple(t for t in (out, out_fp8, out_scales, residual_out) if t is not None)
 
 
@@ -545,15 +582,15 @@ def matmul_fp8(out, x, x_scales, w, w_scales, status=None, stream=None):
     """mla_matmul_fp8: out [M, N] (bf16 or float32) = x [M, K] x w [N, K]^T, both
     e4m3 with a scale per row and 128 columns of x ([M, ceil(K / 128)]; an
     expanded column is one scale a row) and per 128 x 128 block of w."""
-    _same_device(out, x, x_scales, w, w_scales, status)
+    dev = _device_of(out, x, x_scales, w, w_scales, status)
     _typed(out, "out", torch.bfloat16, torch.float32)
     _typed(x, "x", *_FP8)
     _typed(w, "w", *_FP8)
     _typed(x_scales, "x_scales", torch.float32)
     _typed(w_scales, "w_scales", torch.float32)
-    _check(load().mla_matmul_fp8(_ref(describe(out, _dtype_code(out))), _ref(describe(x, MLA_DTYPE_FP8_E4M3)),
-                                 _ref(describe(x_scales, MLA_DTYPE_F32)), _ref(describe(w, MLA_DTYPE_FP8_E4M3)),
-                                 _ref(describe(w_scales, MLA_DTYPE_F32)), _ptr(status), _stream(stream)))
+    _check(load().mla_matmul_fp8(_pack(out, _dtype_code(out)), _pack(x, MLA_DTYPE_FP8_E4M3),
+                                 _pack(x_scales, MLA_DTYPE_F32), _pack(w, MLA_DTYPE_FP8_E4M3),
+                                 _pack(w_scales, MLA_DTYPE_F32), _status_word(status), _raw_stream(stream, dev)))
     return out
 
 
@@ -564,26 +601,26 @@ def _latent_cache(cache, cache_scales, per_tensor):
     _typed(cache_scales, "cache_scales", torch.float32)
     if cache.dim() != 3:
         raise MlaError(MLA_ERR_INVALID_ARG, f"cache must be [num_pages, P, W] (got {tuple(cache.shape)})")
-    if per_tensor and cache_scales.numel() == 1 and cache.shape[0] * cache.shape[1] != 1:
-        return describe(cache, MLA_DTYPE_FP8_E4M3, cache_scales, MLA_SCALE_PER_TENSOR)
-    if cache_scales.numel() != cache.shape[0] * cache.shape[1] or not cache_scales.is_contiguous():
+    slots = cache.shape[0] * cache.shape[1]
+    if per_tensor and cache_scales.numel() == 1 and slots != 1:
+        return _pack(cache, MLA_DTYPE_FP8_E4M3, cache_scales.data_ptr(), MLA_SCALE_PER_TENSOR)
+    if cache_scales.numel() != slots or not cache_scales.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, "cache_scales must be a packed [num_pages, P]")
-    return describe(cache, MLA_DTYPE_FP8_E4M3, cache_scales, MLA_SCALE_PER_TOKEN)
+    return _pack(cache, MLA_DTYPE_FP8_E4M3, cache_scales.data_ptr(), MLA_SCALE_PER_TOKEN)
 
 
 def append_latent(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status=None, stream=None):
     """mla_append_latent: bf16 rows [Tq, W] quantised per token into the paged
     e4m3 cache [num_pages, P, W] and its scales [num_pages, P], at context
     positions cache_lens[b] + i."""
-    _same_device(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status)
+    dev = _device_of(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status)
     _typed(rows, "rows", torch.bfloat16)
     _typed(page_table, "page_table", *_INDEX)
     B = page_table.shape[0]
-    _check(load().mla_append_latent(_ref(_latent_cache(cache, cache_scales, False)),
-                                    _ref(describe(rows, MLA_DTYPE_BF16)),
-                                    _ref(describe(page_table, MLA_DTYPE_U32)),
-                                    _ptr(_indices(row_offsets, "row_offsets", B + 1)),
-                                    _ptr(_indices(cache_lens, "cache_lens", B)), _ptr(status), _stream(stream)))
+    _check(load().mla_append_latent(_latent_cache(cache, cache_scales, False), _pack(rows, MLA_DTYPE_BF16),
+                                    _pack(page_table, MLA_DTYPE_U32), _indices(row_offsets, "row_offsets", B + 1),
+                                    _indices(cache_lens, "cache_lens", B), _status_word(status),
+                                    _raw_stream(stream, dev)))
     return cache, cache_scales
 
 
@@ -602,7 +639,7 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
     queries) over the paged e4m3 latent cache [num_pages, P, 576] with its
     scales ([num_pages, P], or one float); out [Tq, H, 512] stays in the latent
     space, lse [Tq, H] is optional."""
-    _same_device(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, workspace, lse, status)
+    dev = _device_of(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, workspace, lse, status)
     _typed(out, "out", torch.bfloat16)
     _typed(q, "q", torch.bfloat16)
     _typed(lse, "lse", torch.float32)
@@ -611,14 +648,15 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
         # From the launch stream's pool: its memory is not reused before the call is done.
         with torch.cuda.stream(stream):
             workspace = alloc_decode_workspace(q.device)
+    elif not workspace.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
     B = page_table.shape[0]
-    _check(load().mla_decode_latent(_ref(describe(out, MLA_DTYPE_BF16)), _ref(_opt(lse, MLA_DTYPE_F32)),
-                                    _ref(describe(q, MLA_DTYPE_BF16)), _ref(_latent_cache(cache, cache_scales, True)),
-                                    _ref(describe(page_table, MLA_DTYPE_U32)),
-                                    _ptr(_indices(row_offsets, "row_offsets", B + 1)),
-                                    _ptr(_indices(cache_lens, "cache_lens", B)), float(scale), int(mask),
-                                    _ptr(status), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+    _check(load().mla_decode_latent(_pack(out, MLA_DTYPE_BF16), _pack(lse, MLA_DTYPE_F32), _pack(q, MLA_DTYPE_BF16),
+                                    _latent_cache(cache, cache_scales, True), _pack(page_table, MLA_DTYPE_U32),
+                                    _indices(row_offsets, "row_offsets", B + 1),
+                                    _indices(cache_lens, "cache_lens", B), scale, int(mask), _status_word(status),
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _raw_stream(stream, dev)))
     return out
 
 

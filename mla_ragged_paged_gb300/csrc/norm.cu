@@ -10,11 +10,14 @@
 // the norm factor and y are 32-bit; y comes from the unrounded h, so bf16(h)
 // is rounded only in the copy that is stored.
 //
-// A thread owns chunks of 8 columns, 8 * (c * threads + t) .. + 7, so a
-// 128-column group is 16 neighbouring threads' chunks and its maximum four
-// shuffles.  Rows of up to 1024 columns take one warp each, eight to a block
-// (no barrier); wider rows a block each.
-#include <cuda_bf16.h>
+// Where every row starts 16-byte aligned (codes: 8-byte) a thread owns chunks of
+// 8 neighbouring columns and moves them at once; a 128-column group is then 16
+// neighbouring threads, its maximum four shuffles.  Other rows (odd widths) are
+// moved by single elements: a warp owns 256 columns, lane l those at 32 e + l, so
+// that a warp still reads and writes neighbours, and a group is four of every
+// lane's eight.  Rows of up to 1024 columns take one warp each, eight to a block
+// (no barrier); wider rows a block each, which walks the rows and, where the
+// registers allow, reads the next one while it finishes the current one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,127 +47,166 @@ struct NormParams {
   uint32_t dim;
   float eps;
   uint32_t w_f32;
-  uint32_t vec;  // every row of every operand allows 16-byte (codes: 8-byte) accesses
+  uint32_t vec;  // whole chunks, and every row of every operand allows 16-byte (codes: 8-byte) accesses
 };
 
-__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p, uint32_t n, bool vec) {
-  if (vec && n == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void widen(float (&v)[8], uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+
+// CH: chunks of 8 columns per thread.  THREADS 32: a row per warp, blockDim.y rows
+// a block; otherwise a row per block of at most THREADS threads at a time.
+template <int CH, int THREADS, bool VEC>
+__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS) norm_kernel(const NormParams p) {
+  constexpr bool kWarp = THREADS == 32, kAhead = !kWarp && CH == 1;
+  __shared__ float part[2][32];
+  const uint32_t t = threadIdx.x, threads = blockDim.x, lane = t & 31u;
+  long long row = kWarp ? static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
+  const long long step = kWarp ? p.rows : gridDim.x;
+  if (row >= p.rows) return;
+  // Column of element e of chunk c, and whether it exists.  VEC: dim is a
+  // multiple of 8, so a chunk exists as a whole.
+  auto col_of = [&](int c, int e) {
+    return VEC ? 8 * (c * threads + t) + e : 256 * (c * (threads >> 5) + (t >> 5)) + 32 * e + lane;
+  };
+  auto load = [&](const uint16_t* src, int c) {
+    if constexpr (VEC) return col_of(c, 0) < p.dim ? *reinterpret_cast<const uint4*>(src + col_of(c, 0)) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      const uint32_t lo = col_of(c, 2 * e), hi = col_of(c, 2 * e + 1);
+      w[e] = (lo < p.dim ? src[lo] : 0u) | (hi < p.dim ? static_cast<uint32_t>(src[hi]) << 16 : 0u);
     }
-  } else {
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  auto store = [&](uint16_t* dst, int c, const float (&v)[8]) {
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? __uint_as_float(static_cast<uint32_t>(p[e]) << 16) : 0.f;
-  }
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], uint32_t n, bool vec) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-  if (vec && n == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) p[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-  }
-}
-
-// CH: chunks of 8 columns per thread.  ONE_WARP: a row per warp (blockDim.y
-// rows a block); otherwise a row per block.
-template <int CH, bool ONE_WARP>
-__global__ void __launch_bounds__(ONE_WARP ? 256 : 1024) norm_kernel(const NormParams p) {
-  __shared__ float part[32];
-  const uint32_t t = threadIdx.x, threads = blockDim.x;
-  const long long row = ONE_WARP ? static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
-  if (ONE_WARP && row >= p.rows) return;
-  const bool vec = p.vec != 0;
-  float h[CH][8];
-  float ss = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t col = 8 * (c * threads + t);
-    const uint32_t n = col < p.dim ? min(8u, p.dim - col) : 0u;
-    if (n) {
-      load8(h[c], p.x + row * p.x_row + col, n, vec);
-      if (p.res) {
-        float r[8];
-        load8(r, p.res + row * p.res_row + col, n, vec);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] += r[e];
-      }
+    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    if constexpr (VEC) {
+      if (col_of(c, 0) < p.dim) *reinterpret_cast<uint4*>(dst + col_of(c, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t col = 8 * (c * threads + t);
-    const uint32_t n = col < p.dim ? min(8u, p.dim - col) : 0u;
-    if (n && p.res_out) store8(p.res_out + row * p.res_out_row + col, h[c], n, vec);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (!ONE_WARP) {
-    if ((t & 31u) == 0) part[t >> 5] = ss;
-    __syncthreads();
-    ss = (t & 31u) < (threads >> 5) ? part[t & 31u] : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
-  const float inv = rsqrtf(ss / static_cast<float>(p.dim) + p.eps);
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t col = 8 * (c * threads + t);
-    const uint32_t n = col < p.dim ? min(8u, p.dim - col) : 0u;
-    float w[8];
-    if (p.w_f32) {
-      const float* wp = static_cast<const float*>(p.w) + col;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = e < n ? wp[e] : 0.f;
-    } else {
-      load8(w, static_cast<const uint16_t*>(p.w) + col, n, vec);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[c][e] *= inv * w[e];
-    if (p.y && n) store8(p.y + row * p.y_row + col, h[c], n, vec);
-    if (p.y8) {
-      // The group's amax as the bits of |y|: their integer order is the
-      // numbers' order, with NaN above infinity, so a NaN reaches the scale.
-      uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n) m = max(m, __float_as_uint(h[c][e]) & 0x7FFFFFFFu);
+        if (col_of(c, e) < p.dim) dst[col_of(c, e)] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+  };
+  uint4 rx[CH], rr[CH], rw[CH];
+  auto fetch = [&](long long r) {
 #pragma unroll
-      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = max(m, __float_as_uint(kFp8Tiny));
-      const float scale = __fdiv_rn(__uint_as_float(m), kFp8Max);
-      if (n) {
-        if ((t & 15u) == 0) p.ys[row * p.ys_row + (col >> 7)] = scale;
-        uint32_t q[2];
+    for (int c = 0; c < CH; ++c) {
+      rx[c] = load(p.x + r * p.x_row, c);
+      rr[c] = p.res ? load(p.res + r * p.res_row, c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  fetch(row);
+  if (!p.w_f32) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          q[e] = pack_e4m3x2(__fdiv_rn(h[c][4 * e], scale), __fdiv_rn(h[c][4 * e + 1], scale)) |
-                 pack_e4m3x2(__fdiv_rn(h[c][4 * e + 2], scale), __fdiv_rn(h[c][4 * e + 3], scale)) << 16;
-        uint8_t* yp = p.y8 + row * p.y8_row + col;
-        if (vec && n == 8) {
-          *reinterpret_cast<uint2*>(yp) = make_uint2(q[0], q[1]);
+    for (int c = 0; c < CH; ++c) rw[c] = load(static_cast<const uint16_t*>(p.w), c);
+  }
+  for (int turn = 0;; turn ^= 1) {
+    float h[CH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float r[8];
+      widen(h[c], rx[c]);
+      widen(r, rr[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[c][e] += r[e];
+        ss = fmaf(h[c][e], h[c][e], ss);
+      }
+      if (p.res_out) store(p.res_out + row * p.res_out_row, c, h[c]);
+    }
+    const long long next = row + step;
+    if (kAhead && next < p.rows) fetch(next);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!kWarp) {
+      if (lane == 0) part[turn][t >> 5] = ss;
+      __syncthreads();   // (two turns of partial sums: one barrier a row)
+      ss = lane < (threads >> 5) ? part[turn][lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+    const float inv = rsqrtf(ss / static_cast<float>(p.dim) + p.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[8];
+      if (p.w_f32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = col_of(c, e) < p.dim ? __ldg(static_cast<const float*>(p.w) + col_of(c, e)) : 0.f;
+      } else {
+        widen(w, rw[c]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[c][e] *= inv * w[e];
+      if (p.y) store(p.y + row * p.y_row, c, h[c]);
+      if (p.y8) {
+        // A group's amax as the bits of |y|: their integer order is the
+        // numbers' order, with NaN above infinity, so a NaN reaches the scale.
+        // One division a group: y * (1 / scale) is within 2^-23 of y / scale,
+        // which e4m3's steps of 2^-3 do not see but next to a tie.
+        constexpr int kGroups = VEC ? 1 : 2, kPer = 8 / kGroups;
+        uint8_t* dst = p.y8 + row * p.y8_row;
+        uint32_t q[4];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) m = max(m, __float_as_uint(h[c][g * kPer + e]) & 0x7FFFFFFFu);
+#pragma unroll
+          for (int o = VEC ? 8 : 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = max(m, __float_as_uint(kFp8Tiny));
+          const float scale = __fdiv_rn(__uint_as_float(m), kFp8Max), to = __fdiv_rn(1.f, scale);
+          // (The group's first column is its first lane's first element.)
+          if ((VEC ? (lane & 15u) == 0 : lane == 0) && col_of(c, g * kPer) < p.dim)
+            p.ys[row * p.ys_row + (col_of(c, g * kPer) >> 7)] = scale;
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2)
+            q[(g * kPer + e) / 2] = pack_e4m3x2(h[c][g * kPer + e] * to, h[c][g * kPer + e + 1] * to);
+        }
+        if constexpr (VEC) {
+          if (col_of(c, 0) < p.dim)
+            *reinterpret_cast<uint2*>(dst + col_of(c, 0)) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (e < n) yp[e] = static_cast<uint8_t>(q[e >> 2] >> (8 * (e & 3)));
+            if (col_of(c, e) < p.dim) dst[col_of(c, e)] = static_cast<uint8_t>(q[e >> 1] >> (8 * (e & 1)));
         }
       }
     }
+    if (next >= p.rows) break;
+    row = next;
+    if (!kWarp && !kAhead) fetch(row);
   }
+}
+
+template <bool VEC>
+void launch_norm(const NormParams& p, int sms, cudaStream_t s) {
+  const uint32_t chunks = (p.dim + 255) / 256 * 32;  // whole warps of chunks
+  if (chunks <= 128) {
+    const dim3 block(32, 8);
+    const uint32_t grid = static_cast<uint32_t>((p.rows + 7) / 8);
+    if (chunks <= 32) norm_kernel<1, 32, VEC><<<grid, block, 0, s>>>(p);
+    else if (chunks <= 64) norm_kernel<2, 32, VEC><<<grid, block, 0, s>>>(p);
+    else norm_kernel<4, 32, VEC><<<grid, block, 0, s>>>(p);
+    return;
+  }
+  const uint32_t ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const uint32_t threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+  // As many blocks as fit (2048 threads an SM), each walking the rows.
+  const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(sms) * (2048u / threads)));
+  if (threads <= 512 && ch == 1) norm_kernel<1, 512, VEC><<<grid, threads, 0, s>>>(p);
+  else if (ch == 1) norm_kernel<1, 1024, VEC><<<grid, threads, 0, s>>>(p);
+  else if (ch == 2) norm_kernel<2, 1024, VEC><<<grid, threads, 0, s>>>(p);
+  else norm_kernel<4, 1024, VEC><<<grid, threads, 0, s>>>(p);
 }
 
 mla_status_t check_rows(const mla_tensor_t* t, const char* name, mla_dtype_t dt, int64_t rows, int64_t dim,
@@ -205,7 +247,7 @@ extern "C" mla_status_t mla_rms_norm(const mla_tensor_t* out, const mla_tensor_t
     return fail(MLA_ERR_INVALID_ARG, "out_fp8 and out_scales must both be given or both be NULL");
   if (residual_out && !residual) return fail(MLA_ERR_INVALID_ARG, "residual_out without residual");
   NormParams p = {};
-  p.vec = 1;
+  p.vec = dim % 8 == 0;
   if ((st = check_rows(x, "x", MLA_DTYPE_BF16, rows, dim, &p.vec)) != MLA_OK) return st;
   if (!weight) return fail(MLA_ERR_INVALID_ARG, "weight descriptor is NULL");
   if (weight->dtype != MLA_DTYPE_BF16 && weight->dtype != MLA_DTYPE_F32)
@@ -252,22 +294,9 @@ extern "C" mla_status_t mla_rms_norm(const mla_tensor_t* out, const mla_tensor_t
   p.rows = rows;
   p.dim = static_cast<uint32_t>(dim);
   p.eps = eps;
-  const uint32_t chunks = static_cast<uint32_t>((dim + 7) / 8);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (chunks <= 128) {
-    const dim3 block(32, 8);
-    const uint32_t grid = static_cast<uint32_t>((rows + 7) / 8);
-    if (chunks <= 32) norm_kernel<1, true><<<grid, block, 0, s>>>(p);
-    else if (chunks <= 64) norm_kernel<2, true><<<grid, block, 0, s>>>(p);
-    else norm_kernel<4, true><<<grid, block, 0, s>>>(p);
-  } else {
-    const uint32_t ch = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
-    const uint32_t threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-    const uint32_t grid = static_cast<uint32_t>(rows);
-    if (ch == 1) norm_kernel<1, false><<<grid, threads, 0, s>>>(p);
-    else if (ch == 2) norm_kernel<2, false><<<grid, threads, 0, s>>>(p);
-    else norm_kernel<4, false><<<grid, threads, 0, s>>>(p);
-  }
+  if (p.vec) launch_norm<true>(p, sms, s);
+  else launch_norm<false>(p, sms, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "norm launch: %s", cudaGetErrorString(e));
   return MLA_OK;

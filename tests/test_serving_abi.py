@@ -30,7 +30,7 @@ def _desc(shape, dtype=binding.MLA_DTYPE_BF16, ptr=0x10000, stride=None, scale=N
 
 
 def _ref(d):
-    return None if d is None else ctypes.byref(d)
+    return None if d is None else ctypes.addressof(d)
 
 
 def _norm(lib, **over):
@@ -143,6 +143,19 @@ def test_good_arguments_reach_the_device_check(lib):
         pytest.skip("would launch on made-up addresses")
     for call in (_norm, _matmul, _append, _decode):
         assert call(lib) in (binding.MLA_ERR_UNSUPPORTED, binding.MLA_ERR_CUDA)
+
+
+def test_packed_descriptors_have_the_structs_layout():
+    for n in range(1, 5):
+        t = torch.zeros([3, 4, 5, 6][:n], dtype=torch.bfloat16).transpose(0, n - 1)
+        raw = binding._pack(t, 1, 0x50000, 2)
+        d = binding.MlaTensor.from_buffer_copy(raw)
+        assert len(raw) == ctypes.sizeof(binding.MlaTensor)
+        assert (d.data, d.dtype, d.ndim, d.scale, d.scale_gran) == (t.data_ptr(), 1, n, 0x50000, 2)
+        assert list(d.shape)[:n] == list(t.shape) and list(d.stride)[:n] == list(t.stride())
+    with pytest.raises(binding.MlaError):
+        binding._pack(torch.zeros(()), 1)
+    assert binding._pack(None, 1) is None
 
 
 def test_binding_refuses_host_tensors_and_other_types(lib):
