@@ -24,7 +24,7 @@
 // them, so that a row which hangs on one key is exact.  (lse takes the unrounded
 // sum.)  Sums are fp32, in tensor memory.
 //
-// Softmax.  A thread owns one key and half the rows of the tile, so the key's
+// Softmax.  A thread owns one key and a quarter of the rows of the tile, so the key's
 // scale is a scalar of the thread: with y = x + log2(s_j) (log2 units) the weight
 // that multiplies the codes is w_j = 2^(y_j - mu + 7) <= 2^8.5 and the one that
 // is summed is w_j / s_j.  The reference mu of a row rises when a key passes
@@ -60,8 +60,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kKeys = 128;               // keys per tile
 constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent dims
 constexpr uint32_t kRopeBytes = kKeys * 64;
-constexpr int kDecThreads = 384;              // producer, three UMMA issuers; two softmax warpgroups
-constexpr int kDecRegs = 168;
+constexpr int kGroups = 4;                    // softmax warpgroups
+constexpr int kSoftmaxWarps = 4 * kGroups;
+constexpr int kDecThreads = 128 + 128 * kGroups;  // producer and three UMMA issuers before them
+constexpr int kDecRegs = 96;
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
@@ -107,7 +109,7 @@ struct DecodeParams {
 
 template <int NR>
 struct Rows {
-  static constexpr int kCols = NR / 2;            // rows of one softmax warpgroup
+  static constexpr int kCols = NR / kGroups;      // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
   // P: a row of codes per key.  64 rows: an array of 64-byte rows per term; 32
   // rows: both terms side by side in one.
@@ -124,8 +126,8 @@ struct __align__(1024) DecodeSmem {
   uint8_t q[4][R::kQChunk];
   uint8_t q_rope[2 * NR * 64];
   uint8_t p[R::kPBytes];
-  float warp_red[2][4][32];
-  float row_val[2][32];
+  float warp_red[kGroups][4][R::kCols];
+  float row_val[kGroups][R::kCols];
   float col_factor[NR];
   uint64_t full[2][4], empty[2][4];
   uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
@@ -399,14 +401,14 @@ __device__ __forceinline__ float warp_transpose_reduce(const float (&in)[N], int
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 32) tmem_ld_32x32b_x32(addr, r);
-  else tmem_ld_32x32b_x16(addr, r);
+  if constexpr (N == 16) tmem_ld_32x32b_x16(addr, r);
+  else tmem_ld_32x32b_x8(addr, r);
 }
 // The queries of a row tile as two e4m3 terms, rows t1 at r and t2 at NR + r of
 // the K-major operand; col_factor[r] takes the row's power of two back.
 template <int NR>
 __device__ void load_queries(DecodeSmem<NR>& s, const DecodeParams& p, const Segment& g, int tid) {
-  constexpr int kPer = 256 / NR;                  // threads per row
+  constexpr int kPer = 128 * kGroups / NR;        // threads per row
   constexpr int kPieces = (36 + kPer - 1) / kPer;  // of 16 dims
   const uint32_t r = tid / kPer, part = tid % kPer;
   const uint64_t row = static_cast<uint64_t>(g.rt) * NR + r;
@@ -497,7 +499,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
   using R = Rows<NR>;
   constexpr int N = R::kCols;
-  const int tid = group * 128 + quarter * 32 + lane;     // 0 .. 255
+  const int tid = group * 128 + quarter * 32 + lane;
   const uint32_t key = quarter * 32 + lane;              // this thread's key of a tile
   const uint32_t lane_at = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t bar = 1 + group;
@@ -515,7 +517,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
-    asm volatile("bar.sync 3, 256;" ::: "memory");       // col_factor is written by both warpgroups
+    named_bar_sync(1 + kGroups, 128 * kGroups);          // col_factor is written by all warpgroups
     const uint64_t live = static_cast<uint64_t>(g.s.n) * p.H;   // rows of the sequence
     const uint64_t first_row = static_cast<uint64_t>(g.rt) * NR;
     const uint32_t tok0 = static_cast<uint32_t>(first_row / p.H);
@@ -599,10 +601,10 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       float factor = 1.f;
       if (form) {
         const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
-        s.warp_red[group][quarter][lane] = wm;
+        if (lane < N) s.warp_red[group][quarter][lane] = wm;
         named_bar_sync(bar, 128);
-        const float tm = fmaxf(fmaxf(s.warp_red[group][0][lane], s.warp_red[group][1][lane]),
-                               fmaxf(s.warp_red[group][2][lane], s.warp_red[group][3][lane]));
+        const float tm = fmaxf(fmaxf(s.warp_red[group][0][my_row], s.warp_red[group][1][my_row]),
+                               fmaxf(s.warp_red[group][2][my_row], s.warp_red[group][3][my_row]));
         // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
         float next = mu;
         if (tm > mu + kRaise || (tm < mu - kDrop && tm > -INFINITY)) next = fmaxf(rintf(tm) + kMargin, peak - kDepth);
@@ -613,7 +615,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         mu = next;
         if (quarter == 0 && lane < N) s.row_val[group][lane] = mu == -INFINITY ? -1e30f : mu - kShift;  // (no key yet: the first one passes)
         moved = __ballot_sync(0xffffffffu, factor != 1.f && !first);
-        if (N < 32) moved &= (1u << (N & 31)) - 1u;
+        moved &= (1u << N) - 1u;
         named_bar_sync(bar, 128);
         if (moved) {
           look = kt + 2;
@@ -668,16 +670,12 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         const uint32_t swz = (key >> 1) & 3;
         uint8_t* row = s.p + key * 64;
         if constexpr (NR == 32) {
-          *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-          *reinterpret_cast<uint4*>(row + (((2 + group) ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          uint8_t* at = row + 8 * (group & 1);
+          *reinterpret_cast<uint2*>(at + (((group >> 1) ^ swz) << 4)) = make_uint2(t1[0], t1[1]);
+          *reinterpret_cast<uint2*>(at + (((2 + (group >> 1)) ^ swz) << 4)) = make_uint2(t2[0], t2[1]);
         } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            *reinterpret_cast<uint4*>(row + (((2 * group + h) ^ swz) << 4)) =
-                make_uint4(t1[4 * h], t1[4 * h + 1], t1[4 * h + 2], t1[4 * h + 3]);
-            *reinterpret_cast<uint4*>(row + R::kPTerm + (((2 * group + h) ^ swz) << 4)) =
-                make_uint4(t2[4 * h], t2[4 * h + 1], t2[4 * h + 2], t2[4 * h + 3]);
-          }
+          *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(row + R::kPTerm + ((group ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
         }
       }
       if (group == 0 && (!ok || partial)) {
@@ -713,10 +711,11 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
     tc_fence_after();
     auto row_sum = [&](const float (&v)[N]) {
-      s.warp_red[group][quarter][lane] = warp_transpose_reduce<N>(v, lane, add2);
+      const float mine = warp_transpose_reduce<N>(v, lane, add2);
+      if (lane < N) s.warp_red[group][quarter][lane] = mine;
       named_bar_sync(bar, 128);
-      const float sum = (s.warp_red[group][0][lane] + s.warp_red[group][1][lane]) +
-                        (s.warp_red[group][2][lane] + s.warp_red[group][3][lane]);
+      const float sum = (s.warp_red[group][0][my_row] + s.warp_red[group][1][my_row]) +
+                        (s.warp_red[group][2][my_row] + s.warp_red[group][3][my_row]);
       named_bar_sync(bar, 128);
       return sum;
     };
@@ -807,10 +806,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s.s_full[i]), 1);
-      mbar_init(smem_u32(&s.s_empty[i]), 8);   // the eight softmax warps
+      mbar_init(smem_u32(&s.s_empty[i]), kSoftmaxWarps);
     }
-    mbar_init(smem_u32(&s.q_full), 8);
-    mbar_init(smem_u32(&s.p_full), 8);
+    mbar_init(smem_u32(&s.q_full), kSoftmaxWarps);
+    mbar_init(smem_u32(&s.p_full), kSoftmaxWarps);
     mbar_init(smem_u32(&s.pv_done), 2);        // both output issuers
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     fence_barrier_init();
@@ -873,16 +872,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   sh.left = u1 - u0;
   __syncthreads();     // the scratch becomes query space
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
-    if (warp > 0 && lane == 0) {
+    if (warp > 0 && elect_one()) {
       if (warp == 1) issue_scores<NR>(s, p, sh, tmem, abort);
       else issue_output<NR>(s, p, sh, tmem, 2 * (warp - 2), abort);
       drain_umma(&s.drain[warp - 1]);
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 128 x 88 + 256 x 208 = 384 x 168
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");  // 128 x 64 + 512 x 104 = 640 x 96
     decode_softmax<NR>(s, p, sh, units, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   }
   tc_fence_before();
