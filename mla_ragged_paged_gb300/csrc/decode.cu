@@ -72,7 +72,6 @@ constexpr float kRaise = 1.5f;                // mu rises when a key is that far
 constexpr float kDrop = 12.f;                 // and falls when a tile's maximum is that far below it,
 constexpr float kMargin = 2.f;                // in both cases to that far above the maximum
 constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
-constexpr uint32_t kAhead = 3;                // tiles the producer prefetches into L2
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
 // The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
 // 1e27 neither end leaves fp32.
@@ -103,6 +102,7 @@ struct DecodeParams {
   float* part_ml;                  // [slots][3][kMaxRows]: mu, the sum of the weights, and as the products see them
   float* part_o;                   // [slots][kMaxRows][512]
   float sl2;                       // scale * log2(e)
+  uint32_t step_col, step_off;     // kKeys = step_col * P + step_off
   uint32_t box_rows;               // power of two that divides P, up to 128; 1: row gathers
   uint32_t per_token, causal, Tq, H, B, P, num_pages, max_pages, max_keys;
 };
@@ -139,27 +139,40 @@ static_assert(sizeof(DecodeSmem<64>) + 1024 <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem<32>) + 1024 <= 232448, "decode shared memory");
 
 // ------------------------------------------------------------ the work's order
+struct RawSeq {
+  uint32_t lo, hi, prior;
+};
+__device__ __forceinline__ RawSeq load_raw(const DecodeParams& p, uint32_t b) {
+  RawSeq r = {0u, 0u, 0u};
+  if (b < p.B) {
+    r.lo = __ldg(p.ro + b);
+    r.hi = __ldg(p.ro + b + 1);
+    r.prior = __ldg(p.lens + b);
+  }
+  return r;
+}
 struct Seq {
-  uint32_t q0, n, prior, keys, row_tiles, key_tiles;
+  uint32_t q0, rows, prior, keys, row_tiles, key_tiles;  // rows: (token, head) queries
 };
 template <int NR>
-__device__ __forceinline__ Seq sequence(const DecodeParams& p, uint32_t b) {
+__device__ __forceinline__ Seq sequence(const DecodeParams& p, const RawSeq& r) {
   Seq s;
-  const uint32_t lo = p.ro[b], hi = p.ro[b + 1];
-  s.prior = p.lens[b];
-  s.q0 = lo;
-  s.n = lo < hi && hi <= p.Tq ? hi - lo : 0u;
-  const uint64_t keys = static_cast<uint64_t>(s.prior) + s.n;
-  s.keys = static_cast<uint32_t>(min(keys, static_cast<uint64_t>(p.max_keys)));
-  s.row_tiles = static_cast<uint32_t>((static_cast<uint64_t>(s.n) * p.H + NR - 1) / NR);
+  const uint32_t n = r.lo < r.hi && r.hi <= p.Tq ? r.hi - r.lo : 0u;
+  s.prior = r.prior;
+  s.q0 = r.lo;
+  s.rows = n * p.H;
+  s.keys = static_cast<uint32_t>(min(static_cast<uint64_t>(r.prior) + n, static_cast<uint64_t>(p.max_keys)));
+  s.row_tiles = (s.rows + NR - 1) / NR;
   s.key_tiles = (s.keys + kKeys - 1) / kKeys;
   return s;
 }
 
-// A CTA's share: units [first, first + left) from unit `at` of sequence b.
+// What is left of a CTA's share: `left` units from key tile kt of row tile rt of
+// sequence b, whose lengths have been read ahead.
 struct Share {
-  unsigned long long at, left;
-  uint32_t b;
+  unsigned long long left;
+  uint32_t b, rt, kt;
+  RawSeq raw;
 };
 struct Segment {
   Seq s;
@@ -168,37 +181,46 @@ struct Segment {
 template <int NR>
 __device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, Segment& g) {
   while (sh.left && sh.b < p.B) {
-    const Seq s = sequence<NR>(p, sh.b);
-    const unsigned long long units = static_cast<unsigned long long>(s.row_tiles) * s.key_tiles;
-    if (sh.at >= units) {
-      sh.at = 0;
-      ++sh.b;
+    const Seq s = sequence<NR>(p, sh.raw);
+    if (!s.row_tiles || !s.key_tiles) {
+      sh.raw = load_raw(p, ++sh.b);
       continue;
     }
     g.s = s;
     g.b = sh.b;
-    g.rt = static_cast<uint32_t>(sh.at / s.key_tiles);
-    g.kt0 = static_cast<uint32_t>(sh.at - static_cast<unsigned long long>(g.rt) * s.key_tiles);
-    g.kt1 = static_cast<uint32_t>(min(static_cast<unsigned long long>(s.key_tiles), g.kt0 + sh.left));
+    g.rt = sh.rt;
+    g.kt0 = sh.kt;
+    g.kt1 = static_cast<uint32_t>(min(static_cast<unsigned long long>(s.key_tiles), sh.kt + sh.left));
     sh.left -= g.kt1 - g.kt0;
-    sh.at += g.kt1 - g.kt0;
+    sh.kt = g.kt1;
+    if (g.kt1 == s.key_tiles) {
+      sh.kt = 0;
+      if (++sh.rt == s.row_tiles) {
+        sh.rt = 0;
+        sh.raw = load_raw(p, ++sh.b);
+      }
+    }
     return true;
   }
   return false;
 }
 
-// A key's place in the cache, in two steps so that the page-table read is not
-// waited for where it is issued: the page id (kNoPage past the table or past
-// the keys), and then the slot.
+// The keys a thread looks up, one tile after another: page-table column and
+// offset move on by a tile without dividing, and the page id (kNoPage past the
+// table or past the keys) is read before it is needed.
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
-__device__ __forceinline__ uint32_t page_of(const DecodeParams& p, uint32_t b, uint32_t j, uint32_t keys) {
-  const uint32_t col = j / p.P;
-  return j < keys && col < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col) : kNoPage;
-}
-__device__ __forceinline__ bool slot_of(const DecodeParams& p, uint32_t page, uint32_t j, uint32_t& slot) {
-  slot = page < p.num_pages ? page * p.P + j % p.P : 0u;
-  return page < p.num_pages;
-}
+struct KeyWalk {
+  uint32_t col, off;
+  __device__ __forceinline__ KeyWalk(const DecodeParams& p, uint32_t key) : col(key / p.P) { off = key - col * p.P; }
+  __device__ __forceinline__ uint32_t page(const DecodeParams& p, uint32_t b, bool wanted) const {
+    return wanted && col < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col) : kNoPage;
+  }
+  __device__ __forceinline__ void next(const DecodeParams& p) {
+    col += p.step_col;
+    off += p.step_off;
+    if (off >= p.P) off -= p.P, ++col;
+  }
+};
 
 // ------------------------------------------------------------ producer
 template <int NR>
@@ -213,50 +235,28 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
     // Boxes: lane l < 128 / box_rows takes the rows from box_rows * l; row
     // gathers: rows 4 lane .. 4 lane + 3.  What lies past the context or on a
     // bad page is read from slot 0 on, whatever it holds (the softmax zeroes it).
-    const uint32_t first = boxed ? lane * p.box_rows : 4 * lane;
-    const bool mine = !boxed || lane < boxes;
-    auto look_up = [&](uint32_t kt, int e) {
-      return mine && kt < g.kt1 ? page_of(p, g.b, kt * kKeys + first + e, g.s.keys) : kNoPage;
+    const uint32_t at = boxed ? lane * p.box_rows : 4 * lane, first = g.kt0 * kKeys + at;
+    KeyWalk walk[4] = {KeyWalk(p, first), KeyWalk(p, first + 1), KeyWalk(p, first + 2), KeyWalk(p, first + 3)};
+    uint32_t page[4];
+    auto look_up = [&](uint32_t kt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool mine = kt < g.kt1 && (boxed ? e == 0 && lane < boxes : true);
+        page[e] = walk[e].page(p, g.b, mine && kt * kKeys + at + e < g.s.keys);
+      }
     };
-    // Boxes: page[i] is that of tile kt + i, the reads running one tile ahead of
-    // the L2 prefetch, which runs kAhead tiles ahead of the loads: the two
-    // tiles of shared memory alone do not cover the latency of HBM.  Row
-    // gathers: page[e] is that of row e of the next tile.
-    uint32_t page[kAhead + 2];
-    auto prefetch = [&](uint32_t kt, uint32_t pg) {
-      uint32_t slot;
-      if (!slot_of(p, pg, kt * kKeys + first, slot)) return;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, static_cast<int32_t>(slot));
-      tma_prefetch_2d(&p.tm_rope, kLatent, static_cast<int32_t>(slot));
-    };
-    if (boxed) {
-#pragma unroll
-      for (uint32_t i = 0; i < kAhead + 1; ++i) page[i] = look_up(g.kt0 + i, 0);
-#pragma unroll
-      for (uint32_t i = 1; i < kAhead; ++i) prefetch(g.kt0 + i, page[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) page[e] = look_up(g.kt0, e);
-    }
+    look_up(g.kt0);
     for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
       int32_t rows[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        uint32_t slot;
-        const uint32_t j = kt * kKeys + first + e;
-        if (!slot_of(p, page[e], j, slot) && mine && j < g.s.keys && (e == 0 || !boxed)) bad |= MLA_DEVICE_STATUS_BAD_PAGE;
-        rows[e] = static_cast<int32_t>(slot);
+        const bool mine = boxed ? e == 0 && lane < boxes : true;
+        const bool ok = page[e] < p.num_pages;
+        if (!ok && mine && kt * kKeys + at + e < g.s.keys) bad |= MLA_DEVICE_STATUS_BAD_PAGE;
+        rows[e] = ok ? static_cast<int32_t>(page[e] * p.P + walk[e].off) : 0;
+        walk[e].next(p);
       }
-      if (boxed) {
-        page[kAhead + 1] = look_up(kt + kAhead + 1, 0);
-        prefetch(kt + kAhead, page[kAhead]);
-#pragma unroll
-        for (uint32_t i = 0; i < kAhead + 1; ++i) page[i] = page[i + 1];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) page[e] = look_up(kt + 1, e);
-      }
+      look_up(kt + 1);
       for (int c = 0; c < 5 && alive; ++c) {
         const uint32_t buf = tile & 1, rs = tile % R::kRopeSlots;
         uint64_t* full = c < 4 ? &s.full[buf][c] : &s.rope_full[rs];
@@ -411,9 +411,8 @@ __device__ void load_queries(DecodeSmem<NR>& s, const DecodeParams& p, const Seg
   constexpr int kPer = 128 * kGroups / NR;        // threads per row
   constexpr int kPieces = (36 + kPer - 1) / kPer;  // of 16 dims
   const uint32_t r = tid / kPer, part = tid % kPer;
-  const uint64_t row = static_cast<uint64_t>(g.rt) * NR + r;
-  const bool live = row < static_cast<uint64_t>(g.s.n) * p.H;
-  const uint32_t tok = static_cast<uint32_t>(row / p.H), head = static_cast<uint32_t>(row - static_cast<uint64_t>(tok) * p.H);
+  const uint32_t row = g.rt * NR + r, tok = row / p.H, head = row - tok * p.H;
+  const bool live = row < g.s.rows;
   const uint16_t* src = p.q + (g.s.q0 + static_cast<long long>(live ? tok : 0u)) * p.q_tok + (live ? head : 0u) * p.q_head;
   uint4 v[kPieces][2];
   uint32_t m = 0;
@@ -511,48 +510,50 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
   uint32_t head_valid = 0, part_b = 0, part_rt = 0, part_last = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
-    // ---- queries.  The previous segment's products with the old ones are
-    // done: this warp has seen its last score tile.
-    load_queries<NR>(s, p, g, tid);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
-    named_bar_sync(1 + kGroups, 128 * kGroups);          // col_factor is written by all warpgroups
-    const uint64_t live = static_cast<uint64_t>(g.s.n) * p.H;   // rows of the sequence
-    const uint64_t first_row = static_cast<uint64_t>(g.rt) * NR;
-    const uint32_t tok0 = static_cast<uint32_t>(first_row / p.H);
-    const uint32_t tok1 = static_cast<uint32_t>(min(first_row + NR, live) - 1) / p.H;
+    const uint32_t first_row = g.rt * NR, tok0 = first_row / p.H;
+    const uint32_t tok1 = (min(first_row + NR, g.s.rows) - 1) / p.H;
     // Keys below `shared` are visible to every row of the tile, keys from `end` on to none.
     auto seen_by = [&](uint32_t tok) {
       return p.causal ? static_cast<uint32_t>(min(static_cast<uint64_t>(g.s.keys), static_cast<uint64_t>(g.s.prior) + tok + 1))
                       : g.s.keys;
     };
     const uint32_t shared = seen_by(tok0), end = seen_by(tok1);
+    // The key's scale is two dependent reads away (page table, scale): the page
+    // is read two tiles ahead and the scale one tile ahead, so that neither is
+    // waited for.
+    KeyWalk walk(p, g.kt0 * kKeys + key);
+    auto scale_of = [&](uint32_t page, uint32_t off, float& sc) {
+      const bool ok = page < p.num_pages;
+      sc = ok ? __ldg(p.scales + (p.per_token ? page * p.P + off : 0u)) : 1.f;
+      return ok;
+    };
+    const uint32_t page_first = walk.page(p, g.b, g.kt0 * kKeys + key < end), off_first = walk.off;
+    walk.next(p);
+    uint32_t page_after = walk.page(p, g.b, (g.kt0 + 1) * kKeys + key < end), off_after = walk.off;   // (a tile past kt1 is read, not used)
+    walk.next(p);
+    // ---- queries.  The previous segment's products with the old ones are
+    // done: this warp has seen its last score tile.
+    load_queries<NR>(s, p, g, tid);
+    float sc_next;
+    bool ok_next = scale_of(page_first, off_first, sc_next);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+    named_bar_sync(1 + kGroups, 128 * kGroups);          // col_factor is written by all warpgroups
     float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
     uint32_t look = g.kt0 + 2;                           // form the maxima in all tiles before this one
     float l[N], lq[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = lq[i] = 0.f;
-    // The key's scale is two dependent reads away (page table, scale): the page
-    // is read two tiles ahead and the scale one tile ahead, so that neither is
-    // waited for.
-    auto look_up = [&](uint32_t kt) { return kt < g.kt1 ? page_of(p, g.b, kt * kKeys + key, end) : kNoPage; };
-    auto scale_of = [&](uint32_t kt, uint32_t page, float& sc) {
-      uint32_t slot;
-      const bool ok = slot_of(p, page, kt * kKeys + key, slot);
-      sc = ok ? __ldg(p.scales + (p.per_token ? slot : 0u)) : 1.f;
-      return ok;
-    };
-    float sc_next;
-    bool ok_next = scale_of(g.kt0, look_up(g.kt0), sc_next);
-    uint32_t page_after = look_up(g.kt0 + 1);
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
       const float sc = sc_next;
       const bool ok = ok_next;
-      ok_next = scale_of(kt + 1, page_after, sc_next);
-      page_after = look_up(kt + 2);
+      ok_next = scale_of(page_after, off_after, sc_next);
+      page_after = walk.page(p, g.b, (kt + 2) * kKeys + key < end);
+      off_after = walk.off;
+      walk.next(p);
       const uint32_t j = kt * kKeys + key;
-      const float ls = log2f(fmaxf(sc, 0x1p-120f));      // NaN and 0 give finite factors; the score carries the NaN
+      const float ls = __log2f(fmaxf(sc, 0x1p-120f));    // NaN and 0 give finite factors; the score carries the NaN
       const float to_sum = ex2_approx(-kShift - kSumShift - ls);
       // ---- scores
       softmax_wait(smem_u32(&s.s_full[tile & 1]), (tile >> 1) & 1u, abort);
@@ -583,7 +584,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       } else if (partial) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (j > g.s.prior + static_cast<uint32_t>((first_row + r0 + i) / p.H)) y[i] = -INFINITY;
+          if (j > g.s.prior + (first_row + r0 + i) / p.H) y[i] = -INFINITY;
       }
       // ---- the rows' references: formed anew, or still good for every key?
       bool form = kt < look || (kt - g.kt0) % kLook == 0;
@@ -723,7 +724,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     const bool begins = g.kt0 == 0, ends = g.kt1 == g.s.key_tiles;
     const bool whole = begins && ends;
     const uint32_t slot = 2 * blockIdx.x + (begins ? 1 : 0);
-    const uint64_t row = first_row + r0 + my_row;
+    const uint32_t row = first_row + r0 + my_row;
     if (quarter == 0 && lane < N) {
       // 2^(mu - kShift) and 2^(mu + kSumShift) are the units of O and l.
       s.row_val[group][lane] = seen != 0.f ? kUnit / seen : 0.f;
@@ -732,9 +733,9 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         ml[0] = mu;
         ml[kMaxRows] = total;
         ml[2 * kMaxRows] = seen;
-      } else if (p.lse && row < live) {
-        const uint32_t tok = static_cast<uint32_t>(row / p.H);
-        p.lse[(g.s.q0 + static_cast<long long>(tok)) * p.l_tok + static_cast<long long>(row - static_cast<uint64_t>(tok) * p.H) * p.l_head] =
+      } else if (p.lse && row < g.s.rows) {
+        const uint32_t tok = row / p.H;
+        p.lse[(g.s.q0 + static_cast<long long>(tok)) * p.l_tok + (row - tok * p.H) * p.l_head] =
             total != 0.f ? (mu + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
       }
     }
@@ -747,11 +748,10 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       tmem_ld_wait();
       const uint32_t dim = c * 128 + key;
       if (whole) {
-        uint32_t tok = static_cast<uint32_t>((first_row + r0) / p.H);
-        uint32_t head = static_cast<uint32_t>(first_row + r0 - static_cast<uint64_t>(tok) * p.H);
+        uint32_t tok = (first_row + r0) / p.H, head = first_row + r0 - tok * p.H;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          if (first_row + r0 + i < live) {
+          if (first_row + r0 + i < g.s.rows) {
             const float v = s.row_val[group][i];
             p.out[(g.s.q0 + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + dim] =
                 static_cast<uint16_t>(pack_bf16x2(v != 0.f ? __uint_as_float(o[i]) * v : 0.f, 0.f));
@@ -790,8 +790,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   volatile uint32_t* abort = &s.abort_flag;
   // Scratch of the prologue, in the place of the queries.
   struct Prologue {
-    unsigned long long warp_sum[kDecThreads / 32], at;
-    uint32_t b;
+    unsigned long long warp_sum[kDecThreads / 32];
+    Share start;
   };
   Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
   if (threadIdx.x == 0) {
@@ -826,10 +826,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   unsigned long long mine = 0;
   uint32_t bad = 0;
   for (uint32_t b = b0; b < b1; ++b) {
-    const Seq q = sequence<NR>(p, b);
+    const RawSeq raw = load_raw(p, b);
+    const Seq q = sequence<NR>(p, raw);
     mine += static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
-    if (p.ro[b + 1] < p.ro[b] || p.ro[b + 1] > p.Tq) bad |= MLA_DEVICE_STATUS_BAD_OFFSETS;
-    if (q.n && static_cast<uint64_t>(q.prior) + q.n > p.max_keys) bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
+    if (raw.hi < raw.lo || raw.hi > p.Tq) bad |= MLA_DEVICE_STATUS_BAD_OFFSETS;
+    if (q.rows && q.keys < static_cast<uint64_t>(raw.prior) + (raw.hi - raw.lo)) bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
   }
   if (bad && p.status && blockIdx.x == 0) atomicOr(p.status, bad);
   unsigned long long incl = mine;
@@ -855,21 +856,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   unsigned long long start = before + incl - mine;
   if (u0 < u1 && start <= u0 && u0 < start + mine) {
     for (uint32_t b = b0; b < b1; ++b) {
-      const Seq q = sequence<NR>(p, b);
+      const RawSeq raw = load_raw(p, b);
+      const Seq q = sequence<NR>(p, raw);
       const unsigned long long here = static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
       if (u0 < start + here) {
-        pro.b = b;
-        pro.at = u0 - start;
+        pro.start.left = u1 - u0;
+        pro.start.b = b;
+        pro.start.rt = static_cast<uint32_t>((u0 - start) / q.key_tiles);
+        pro.start.kt = static_cast<uint32_t>((u0 - start) % q.key_tiles);
+        pro.start.raw = raw;
         break;
       }
       start += here;
     }
   }
   __syncthreads();
-  Share sh;
-  sh.b = u0 < u1 ? pro.b : p.B;
-  sh.at = u0 < u1 ? pro.at : 0;
-  sh.left = u1 - u0;
+  Share sh = {};
+  if (u0 < u1) sh = pro.start;
   __syncthreads();     // the scratch becomes query space
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -894,55 +897,73 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------ joining parts
-// Row r of the row tile that CTA c begins and others end: out = sum of the
-// parts' O in units of the largest reference, over their l.  Four groups of 128
-// threads take every fourth part, four dims a thread.
-__global__ void __launch_bounds__(512) decode_join_kernel(const DecodeParams p, uint32_t nr) {
-  __shared__ float so[4][kLatent];
-  __shared__ float sl[4], sq[4];
-  const uint32_t c = blockIdx.x, r = blockIdx.y;
-  const PartHeader h = p.headers[c];
-  if (!h.valid) return;
-  const uint32_t lo = p.ro[h.b], n = p.ro[h.b + 1] - lo;
-  const uint64_t row = static_cast<uint64_t>(h.rt) * nr + r;
-  if (row >= static_cast<uint64_t>(n) * p.H) return;
-  const uint32_t parts = h.last_cta - c + 1;
-  auto slot = [&](uint32_t i) { return 2 * (c + i) + (i == 0 ? 1u : 0u); };
-  const int group = threadIdx.x >> 7, t = threadIdx.x & 127;
-  float m = -INFINITY;
-  for (uint32_t i = t & 31; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(slot(i)) * 3 * kMaxRows + r]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f, lq = 0.f;
-#pragma unroll 4
-  for (uint32_t i = group; i < parts; i += 4) {
-    const size_t s = slot(i);
+// The row tile that CTA c begins and others end: out = sum of the parts' O in
+// units of the largest reference, over their l, in the parts' order.  A warp
+// takes one row: for a few parts all 512 dims (blockIdx.z 0), 16 a lane; for many,
+// when few rows are joined, 128 dims, four a lane, in each of four blocks.
+constexpr uint32_t kFewParts = 8;
+constexpr int kJoinRows = 8;
+template <int V>
+__device__ __forceinline__ void join_row(const DecodeParams& p, uint32_t c, uint32_t parts, uint32_t r, uint32_t d0, float m,
+                                         float4 (&acc)[V], float& l, float& lq) {
+#pragma unroll V == 1 ? 8 : 2
+  for (uint32_t i = 0; i < parts; ++i) {
+    const size_t s = 2 * (c + i) + (i == 0 ? 1u : 0u);
     const float* ml = p.part_ml + s * 3 * kMaxRows + r;
+    const float* src = p.part_o + (s * kMaxRows + r) * kLatent + d0;
     const float mi = ml[0], li = ml[kMaxRows], qi = ml[2 * kMaxRows];
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * kMaxRows + r) * kLatent + 4 * t);
+    float4 v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = *reinterpret_cast<const float4*>(src + 128 * k);
     if (li != 0.f) {
       const float f = exp2f(mi - m);
       l = fmaf(li, f, l);
       lq = fmaf(qi, f, lq);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        acc[k].x = fmaf(v[k].x, f, acc[k].x);
+        acc[k].y = fmaf(v[k].y, f, acc[k].y);
+        acc[k].z = fmaf(v[k].z, f, acc[k].z);
+        acc[k].w = fmaf(v[k].w, f, acc[k].w);
+      }
     }
   }
-  *reinterpret_cast<float4*>(&so[group][4 * t]) = acc;
-  if (t == 0) sl[group] = l, sq[group] = lq;
-  __syncthreads();
-  const float total = (sl[0] + sl[1]) + (sl[2] + sl[3]), seen = (sq[0] + sq[1]) + (sq[2] + sq[3]);
-  const uint32_t tok = static_cast<uint32_t>(row / p.H), head = static_cast<uint32_t>(row - static_cast<uint64_t>(tok) * p.H);
-  const int d = threadIdx.x;
-  const float o = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
-  p.out[(lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + d] =
-      static_cast<uint16_t>(pack_bf16x2(seen != 0.f ? o * (kUnit / seen) : 0.f, 0.f));
-  if (d == 0 && p.lse)
+}
+
+__global__ void __launch_bounds__(32 * kJoinRows) decode_join_kernel(const DecodeParams p, uint32_t nr) {
+  const uint32_t c = blockIdx.x, lane = threadIdx.x & 31u, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), z = blockIdx.z;
+  const PartHeader h = p.headers[c];
+  if (!h.valid) return;
+  const uint32_t parts = h.last_cta - c + 1;
+  if (z && parts <= kFewParts) return;
+  const uint32_t lo = p.ro[h.b], row = h.rt * nr + r;
+  if (row >= (p.ro[h.b + 1] - lo) * p.H) return;
+  const uint32_t tok = row / p.H, head = row - tok * p.H;
+  float m = -INFINITY;
+  for (uint32_t i = lane; i < parts; i += 32)
+    m = fmaxf(m, p.part_ml[static_cast<size_t>(2 * (c + i) + (i == 0 ? 1u : 0u)) * 3 * kMaxRows + r]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, lq = 0.f;
+  uint16_t* out = p.out + (lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + 4 * lane;
+  auto store = [&](uint16_t* dst, const float4& v) {
+    const float f = lq != 0.f ? kUnit / lq : 0.f;
+    *reinterpret_cast<uint2*>(dst) = lq != 0.f ? make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f))
+                                               : make_uint2(0u, 0u);
+  };
+  if (parts <= kFewParts) {
+    float4 acc[4] = {};
+    join_row<4>(p, c, parts, r, 4 * lane, m, acc, l, lq);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store(out + 128 * k, acc[k]);
+  } else {
+    float4 acc[1] = {};
+    join_row<1>(p, c, parts, r, 128 * z + 4 * lane, m, acc, l, lq);
+    store(out + 128 * z, acc[0]);
+  }
+  if (lane == 0 && z == 0 && p.lse)
     p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
-        total != 0.f ? (m + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
+        l != 0.f ? (m + log2f(l * 0x1p30f)) * kLn2 : -INFINITY;
 }
 
 constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 256;
@@ -960,7 +981,7 @@ mla_status_t launch_decode(const DecodeParams& p, int dev, int sms, int slot, cu
   decode_kernel<NR><<<ctas, kDecThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-  decode_join_kernel<<<dim3(ctas, NR), 512, 0, stream>>>(p, NR);
+  decode_join_kernel<<<dim3(ctas, NR / kJoinRows, 4), 32 * kJoinRows, 0, stream>>>(p, NR);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
   return MLA_OK;
@@ -991,6 +1012,7 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   if (cache->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "cache must be [num_pages, P, %d]", kWidth);
   if (!cache->scale || (cache->scale_gran != MLA_SCALE_PER_TOKEN && cache->scale_gran != MLA_SCALE_PER_TENSOR))
     return fail(MLA_ERR_INVALID_ARG, "cache needs per-token or per-tensor scales");
+  if (Tq * H > 0x7FFFFFFFll) return fail(MLA_ERR_INVALID_ARG, "q exceeds 2^31 rows");
   if (H < 1 || H > 1024) return fail(MLA_ERR_INVALID_ARG, "heads must be 1..1024");
   if (B < 1 || B > 16384 || page_table->shape[1] < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be 1..16384 with a page-table column");
   if (NP < 1 || P < 1) return fail(MLA_ERR_INVALID_ARG, "empty cache");
@@ -1066,6 +1088,8 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   // One box of as many rows as divide a page; pages without a multiple of the
   // swizzle's eight rows take row gathers (measured: a 128-row tile in gathers
   // of four costs the producer twice a tile's time).
+  p.step_col = kKeys / p.P;
+  p.step_off = kKeys % p.P;
   p.box_rows = static_cast<uint32_t>(box_rows);
   // 32-row tiles where an average sequence's queries fit one.
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;

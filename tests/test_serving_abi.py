@@ -130,7 +130,8 @@ def _decode(lib, **over):
     dict(cache=_cache(dtype=binding.MLA_DTYPE_BF16)), dict(cache=_cache(ptr=0x10008)),
     dict(cache=_cache(stride=[17 * 576, 576, 1])), dict(cache=_cache(stride=[16 * 584, 584, 1])),
     dict(cache=_cache((0, 16, 576))), dict(cache=_cache((1 << 20, 1 << 12, 576))),
-    dict(pt=_desc([2, 0], U32)), dict(pt=_desc([16385, 4], U32)), dict(scale=-1.0), dict(scale=float("nan")),
+    dict(pt=_desc([2, 0], U32)), dict(pt=_desc([16385, 4], U32)),
+    dict(q=_desc([1 << 29, 8, 576]), out=_desc([1 << 29, 8, 512]), lse=None), dict(scale=-1.0), dict(scale=float("nan")),
     dict(scale=float("inf")), dict(mask=7), dict(ws=0x40010), dict(ws_bytes=16),
 ])
 def test_decode_refuses(lib, change):
