@@ -104,6 +104,7 @@ struct DecodeParams {
   float sl2;                       // scale * log2(e)
   uint32_t step_col, step_off;     // kKeys = step_col * P + step_off
   uint32_t box_rows;               // power of two that divides P, up to 128; 1: row gathers
+  uint32_t ctas;                   // of the decode kernel's launch
   uint32_t per_token, causal, Tq, H, B, P, num_pages, max_pages, max_keys;
 };
 
@@ -897,73 +898,101 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------ joining parts
-// The row tile that CTA c begins and others end: out = sum of the parts' O in
-// units of the largest reference, over their l, in the parts' order.  A warp
-// takes one row: for a few parts all 512 dims (blockIdx.z 0), 16 a lane; for many,
-// when few rows are joined, 128 dims, four a lane, in each of four blocks.
-constexpr uint32_t kFewParts = 8;
-constexpr int kJoinRows = 8;
-template <int V>
-__device__ __forceinline__ void join_row(const DecodeParams& p, uint32_t c, uint32_t parts, uint32_t r, uint32_t d0, float m,
-                                         float4 (&acc)[V], float& l, float& lq) {
-#pragma unroll V == 1 ? 8 : 2
-  for (uint32_t i = 0; i < parts; ++i) {
-    const size_t s = 2 * (c + i) + (i == 0 ? 1u : 0u);
-    const float* ml = p.part_ml + s * 3 * kMaxRows + r;
-    const float* src = p.part_o + (s * kMaxRows + r) * kLatent + d0;
-    const float mi = ml[0], li = ml[kMaxRows], qi = ml[2 * kMaxRows];
-    float4 v[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = *reinterpret_cast<const float4*>(src + 128 * k);
-    if (li != 0.f) {
-      const float f = exp2f(mi - m);
-      l = fmaf(li, f, l);
-      lq = fmaf(qi, f, lq);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        acc[k].x = fmaf(v[k].x, f, acc[k].x);
-        acc[k].y = fmaf(v[k].y, f, acc[k].y);
-        acc[k].z = fmaf(v[k].z, f, acc[k].z);
-        acc[k].w = fmaf(v[k].w, f, acc[k].w);
-      }
-    }
-  }
-}
+// The row tiles whose keys several CTAs shared: out = sum of the parts' O in
+// units of the largest reference, over their l.  The parts of a row tile are
+// those of consecutive CTAs, from the one whose header says that it begins
+// and does not end it.  Two forms, by how many row tiles there can be:
+// * WARP: many, of few parts each.  A warp per row, eight rows of the tile that
+//   CTA blockIdx.x begins.
+// * else: few, of many parts.  A block per row, a warp per eighth part, of the
+//   blockIdx.x-th tile that some CTA begins; the warps' sums meet in shared
+//   memory, in order.
+constexpr int kJoinWarps = 8;
+constexpr uint32_t kFewTiles = 24;
 
-__global__ void __launch_bounds__(32 * kJoinRows) decode_join_kernel(const DecodeParams p, uint32_t nr) {
-  const uint32_t c = blockIdx.x, lane = threadIdx.x & 31u, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), z = blockIdx.z;
+struct JoinSum {
+  float4 o[4];  // dims 128 k + 4 lane .. + 3
+  float l, lq;
+};
+__device__ __forceinline__ uint32_t part_slot(uint32_t c, uint32_t i) { return 2 * (c + i) + (i == 0 ? 1u : 0u); }
+
+template <bool WARP>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const DecodeParams p, uint32_t nr) {
+  __shared__ JoinSum sums[WARP ? 1 : kJoinWarps][32];
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  uint32_t c = blockIdx.x;
+  if constexpr (!WARP) {
+    uint32_t nth = blockIdx.x;
+    c = p.ctas;
+    for (uint32_t at = 0; at < p.ctas && c == p.ctas; at += 32) {
+      const uint32_t found = __ballot_sync(0xffffffffu, at + lane < p.ctas && p.headers[at + lane].valid);
+      const uint32_t n = __popc(found);
+      if (nth < n) c = at + __fns(found, 0, nth + 1);
+      nth -= min(nth, n);
+    }
+    if (c == p.ctas) return;
+  }
   const PartHeader h = p.headers[c];
   if (!h.valid) return;
+  const uint32_t r = WARP ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
   const uint32_t parts = h.last_cta - c + 1;
-  if (z && parts <= kFewParts) return;
   const uint32_t lo = p.ro[h.b], row = h.rt * nr + r;
   if (row >= (p.ro[h.b + 1] - lo) * p.H) return;
   const uint32_t tok = row / p.H, head = row - tok * p.H;
   float m = -INFINITY;
-  for (uint32_t i = lane; i < parts; i += 32)
-    m = fmaxf(m, p.part_ml[static_cast<size_t>(2 * (c + i) + (i == 0 ? 1u : 0u)) * 3 * kMaxRows + r]);
+  for (uint32_t i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(part_slot(c, i)) * 3 * kMaxRows + r]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f, lq = 0.f;
-  uint16_t* out = p.out + (lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + 4 * lane;
-  auto store = [&](uint16_t* dst, const float4& v) {
-    const float f = lq != 0.f ? kUnit / lq : 0.f;
-    *reinterpret_cast<uint2*>(dst) = lq != 0.f ? make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f))
-                                               : make_uint2(0u, 0u);
-  };
-  if (parts <= kFewParts) {
-    float4 acc[4] = {};
-    join_row<4>(p, c, parts, r, 4 * lane, m, acc, l, lq);
+  JoinSum a = {};
+#pragma unroll 2
+  for (uint32_t i = WARP ? 0 : warp; i < parts; i += WARP ? 1 : kJoinWarps) {
+    const size_t s = part_slot(c, i);
+    const float* ml = p.part_ml + s * 3 * kMaxRows + r;
+    const float* src = p.part_o + (s * kMaxRows + r) * kLatent + 4 * lane;
+    const float mi = ml[0], li = ml[kMaxRows], qi = ml[2 * kMaxRows];
+    float4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) store(out + 128 * k, acc[k]);
-  } else {
-    float4 acc[1] = {};
-    join_row<1>(p, c, parts, r, 128 * z + 4 * lane, m, acc, l, lq);
-    store(out + 128 * z, acc[0]);
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4*>(src + 128 * k);
+    if (li != 0.f) {
+      const float f = exp2f(mi - m);
+      a.l = fmaf(li, f, a.l);
+      a.lq = fmaf(qi, f, a.lq);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a.o[k].x = fmaf(v[k].x, f, a.o[k].x);
+        a.o[k].y = fmaf(v[k].y, f, a.o[k].y);
+        a.o[k].z = fmaf(v[k].z, f, a.o[k].z);
+        a.o[k].w = fmaf(v[k].w, f, a.o[k].w);
+      }
+    }
   }
-  if (lane == 0 && z == 0 && p.lse)
+  if constexpr (!WARP) {
+    sums[warp][lane] = a;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < kJoinWarps; ++w) {
+      const JoinSum& b = sums[w][lane];
+      a.l += b.l;
+      a.lq += b.lq;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a.o[k].x += b.o[k].x;
+        a.o[k].y += b.o[k].y;
+        a.o[k].z += b.o[k].z;
+        a.o[k].w += b.o[k].w;
+      }
+    }
+  }
+  uint16_t* out = p.out + (lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + 4 * lane;
+  const float f = a.lq != 0.f ? kUnit / a.lq : 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint2*>(out + 128 * k) =
+        a.lq != 0.f ? make_uint2(pack_bf16x2(a.o[k].x * f, a.o[k].y * f), pack_bf16x2(a.o[k].z * f, a.o[k].w * f))
+                    : make_uint2(0u, 0u);
+  if (lane == 0 && p.lse)
     p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
-        l != 0.f ? (m + log2f(l * 0x1p30f)) * kLn2 : -INFINITY;
+        a.l != 0.f ? (m + log2f(a.l * 0x1p30f)) * kLn2 : -INFINITY;
 }
 
 constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 256;
@@ -971,17 +1000,21 @@ constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 3 * kMaxRows;
 constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * kLatent;
 
 template <int NR>
-mla_status_t launch_decode(const DecodeParams& p, int dev, int sms, int slot, cudaStream_t stream) {
+mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR>);
   const int smem = static_cast<int>(sizeof(DecodeSmem<NR>) + 1024);
   mla_status_t st;
   if ((st = check_registers(kernel, kDecRegs, dev, slot)) != MLA_OK) return st;
   if ((st = set_max_dynamic_smem(kernel, smem, dev, slot)) != MLA_OK) return st;
   const uint32_t ctas = std::min<uint32_t>(static_cast<uint32_t>(sms), kMaxCtas);
+  p.ctas = ctas;
   decode_kernel<NR><<<ctas, kDecThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-  decode_join_kernel<<<dim3(ctas, NR / kJoinRows, 4), 32 * kJoinRows, 0, stream>>>(p, NR);
+  // Row tiles: each sequence's last one may be partial.
+  const uint64_t tiles = static_cast<uint64_t>(p.Tq) * p.H / NR + std::min(p.B, p.Tq);
+  if (tiles > kFewTiles) decode_join_kernel<true><<<dim3(ctas, NR / kJoinWarps), 32 * kJoinWarps, 0, stream>>>(p, NR);
+  else decode_join_kernel<false><<<dim3(static_cast<uint32_t>(tiles), NR), 32 * kJoinWarps, 0, stream>>>(p, NR);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
   return MLA_OK;
