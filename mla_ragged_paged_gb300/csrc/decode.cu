@@ -116,13 +116,14 @@ struct Rows {
   // rows: both terms side by side in one.
   static constexpr uint32_t kPBytes = kKeys * 2 * NR;
   static constexpr uint32_t kPTerm = NR == 64 ? kKeys * 64 : 32;  // bytes from the first term to the second
-  static constexpr int kRopeSlots = NR <= 32 ? 2 : 1;   // (what fits beside two tiles of latent chunks)
+  // What fits: 8 latent chunks are two tiles.
+  static constexpr uint32_t kSlots = NR <= 32 ? 10 : 8, kRopeSlots = NR <= 32 ? 2 : 1;
 };
 
 template <int NR>
 struct __align__(1024) DecodeSmem {
   using R = Rows<NR>;
-  uint8_t chunk[2][4][kChunk];
+  uint8_t chunk[R::kSlots][kChunk];
   uint8_t rope[R::kRopeSlots][kRopeBytes];
   uint8_t q[4][R::kQChunk];
   uint8_t q_rope[2 * NR * 64];
@@ -130,7 +131,7 @@ struct __align__(1024) DecodeSmem {
   float warp_red[kGroups][4][R::kCols];
   float row_val[kGroups][R::kCols];
   float col_factor[NR];
-  uint64_t full[2][4], empty[2][4];
+  uint64_t full[R::kSlots], empty[R::kSlots];
   uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain[3];
   uint32_t tmem_base;
@@ -223,6 +224,17 @@ struct KeyWalk {
   }
 };
 
+// Ring place of latent chunk c of a tile.
+template <int NR>
+struct Place {
+  uint32_t slot, phase;
+  __device__ __forceinline__ Place(uint32_t tile, uint32_t c) {
+    const uint32_t pos = tile * 4 + c;
+    slot = pos % Rows<NR>::kSlots;
+    phase = (pos / Rows<NR>::kSlots) & 1u;
+  }
+};
+
 // ------------------------------------------------------------ producer
 template <int NR>
 __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
@@ -259,15 +271,16 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
       }
       look_up(kt + 1);
       for (int c = 0; c < 5 && alive; ++c) {
-        const uint32_t buf = tile & 1, rs = tile % R::kRopeSlots;
-        uint64_t* full = c < 4 ? &s.full[buf][c] : &s.rope_full[rs];
-        uint64_t* empty = c < 4 ? &s.empty[buf][c] : &s.rope_empty[rs];
-        const uint32_t phase = c < 4 ? tile >> 1 : tile / R::kRopeSlots;
-        if (!(alive = mbar_wait(smem_u32(empty), (phase & 1u) ^ 1u, abort))) break;
+        const Place<NR> at_c(tile, c);
+        const uint32_t rs = tile % R::kRopeSlots;
+        uint64_t* full = c < 4 ? &s.full[at_c.slot] : &s.rope_full[rs];
+        uint64_t* empty = c < 4 ? &s.empty[at_c.slot] : &s.rope_empty[rs];
+        const uint32_t phase = c < 4 ? at_c.phase : (tile / R::kRopeSlots) & 1u;
+        if (!(alive = mbar_wait(smem_u32(empty), phase ^ 1u, abort))) break;
         const uint32_t bar = smem_u32(full);
         if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
         __syncwarp();
-        const uint32_t dst = c < 4 ? smem_u32(s.chunk[buf][c]) : smem_u32(s.rope[rs]);
+        const uint32_t dst = c < 4 ? smem_u32(s.chunk[at_c.slot]) : smem_u32(s.rope[rs]);
         const uint32_t row_bytes = c < 4 ? 128u : 64u;
         const CUtensorMap* map = c < 4 ? &p.tm_latent : &p.tm_rope;
         if (!boxed)
@@ -282,12 +295,12 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   if (*abort) {
     // Let the copies still in flight land before the CTA exits.
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 0; i < 2 && i <= tile; ++i) {
-      const uint32_t q = tile - i;
-      for (int c = 0; c < 4; ++c)
-        while (!mbar_try_wait(smem_u32(&s.full[q & 1][c]), (q >> 1) & 1u))
+    for (uint32_t i = 0; i < 3 && i <= tile; ++i)
+      for (uint32_t c = 0; c < 4; ++c) {
+        const Place<NR> at_c(tile - i, c);
+        while (!mbar_try_wait(smem_u32(&s.full[at_c.slot]), at_c.phase))
           if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
-    }
+      }
     for (uint32_t i = 0; i < R::kRopeSlots && i <= tile; ++i) {
       const uint32_t q = tile - i;
       while (!mbar_try_wait(smem_u32(&s.rope_full[q % R::kRopeSlots]), (q / R::kRopeSlots) & 1u))
@@ -305,7 +318,7 @@ template <int NR>
 __device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
   using R = Rows<NR>;
   const uint32_t id_s = make_idesc(128, 2 * NR, 0, false);
-  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0][0])), q_desc = sw128_desc_at(smem_u32(s.q[0]));
+  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0])), q_desc = sw128_desc_at(smem_u32(s.q[0]));
   uint32_t tile = 0, segs = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
@@ -315,12 +328,12 @@ __device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
       const uint32_t par = tile & 1, phase = (tile >> 1) & 1u;
       if (!mbar_wait(smem_u32(&s.s_empty[par]), phase ^ 1u, abort)) return;
       const uint32_t d = tmem + kColS + par * (2 * NR);
-      const uint64_t kd0 = chunk_desc + par * (4 * kChunk >> 4);
 #pragma unroll 1
       for (uint32_t c = 0; c < 4; ++c) {
-        if (!mbar_wait(smem_u32(&s.full[par][c]), phase, abort)) return;
+        const Place<NR> at(tile, c);
+        if (!mbar_wait(smem_u32(&s.full[at.slot]), at.phase, abort)) return;
         tc_fence_after();
-        const uint64_t kd = kd0 + c * (kChunk >> 4), qd = q_desc + c * (R::kQChunk >> 4);
+        const uint64_t kd = chunk_desc + at.slot * (kChunk >> 4), qd = q_desc + c * (R::kQChunk >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, (c | k) != 0);
       }
@@ -343,18 +356,18 @@ __device__ void issue_output(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
                              volatile uint32_t* abort) {
   using R = Rows<NR>;
   const uint32_t id_o = make_idesc(128, NR, 0, true) | (1u << 15);
-  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0][c0])), p_desc = sw64_desc_at(smem_u32(s.p));
+  const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0])), p_desc = sw64_desc_at(smem_u32(s.p));
   uint32_t tile = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
-      const uint32_t par = tile & 1;
       if (!mbar_wait(smem_u32(&s.p_full), tile & 1u, abort)) return;
       tc_fence_after();
       const uint32_t more = kt != g.kt0;
 #pragma unroll 1
       for (uint32_t c = 0; c < 2; ++c) {
-        const uint64_t vd = chunk_desc + par * (4 * kChunk >> 4) + c * (kChunk >> 4);
+        const Place<NR> at(tile, c0 + c);
+        const uint64_t vd = chunk_desc + at.slot * (kChunk >> 4);
         const uint32_t d = tmem + (c0 + c) * NR;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -362,7 +375,7 @@ __device__ void issue_output(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
           for (int term = 0; term < 2; ++term)
             umma_f8_ss(d, vd + k * (32 * 128 >> 4), p_desc + term * (R::kPTerm >> 4) + k * (32 * 64 >> 4),
                        term ? id_o | 1u << 10 : id_o, term || k ? 1u : more);
-        umma_commit(smem_u32(&s.empty[par][c0 + c]));
+        umma_commit(smem_u32(&s.empty[at.slot]));
       }
       umma_commit(smem_u32(&s.pv_done));
     }
@@ -685,11 +698,13 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         // some rows do not see and that holds a NaN, becomes zeros.  (Rows that
         // see the NaN have NaN weights already: the scores read the same codes.)
         uint32_t nan = !ok;
-        for (int c = 0; c < 4; ++c)   // (complete long ago: orders this thread after the copies)
-          softmax_wait(smem_u32(&s.full[tile & 1][c]), (tile >> 1) & 1u, abort);
+        for (int c = 0; c < 4; ++c) {  // (complete long ago: orders this thread after the copies)
+          const Place<NR> at(tile, c);
+          softmax_wait(smem_u32(&s.full[at.slot]), at.phase, abort);
+        }
 #pragma unroll 1
         for (int c = 0; c < 4 && !nan; ++c) {
-          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[tile & 1][c] + key * 128);
+          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[Place<NR>(tile, c).slot] + key * 128);
           for (int i = 0; i < 8; ++i) {
             const uint4 v = row[i];
             nan |= (((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -699,7 +714,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         if (nan) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint4* row = reinterpret_cast<uint4*>(s.chunk[tile & 1][c] + key * 128);
+            uint4* row = reinterpret_cast<uint4*>(s.chunk[Place<NR>(tile, c).slot] + key * 128);
             for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -797,11 +812,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(smem_u32(&s.full[i >> 2][i & 3]), 1);
-      mbar_init(smem_u32(&s.empty[i >> 2][i & 3]), 1);
+    for (uint32_t i = 0; i < R::kSlots; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
     }
-    for (int i = 0; i < R::kRopeSlots; ++i) {
+    for (uint32_t i = 0; i < R::kRopeSlots; ++i) {
       mbar_init(smem_u32(&s.rope_full[i]), 1);
       mbar_init(smem_u32(&s.rope_empty[i]), 1);
     }
