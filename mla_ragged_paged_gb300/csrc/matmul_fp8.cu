@@ -35,33 +35,38 @@ constexpr uint32_t kKB = 128;                 // columns of one scale block (byt
 constexpr uint32_t kTileM = 128, kTileN = 256;
 
 struct MatmulParams {
-  CUtensorMap tm_x, tm_w;
+  CUtensorMap tm_x, tm_w, tm_out;   // tm_out: tile kernel, where `tma` is set
   const float* xs;
   const float* ws;
   void* out;
   long long xs_row, xs_col, ws_row, ws_col, out_row;
   uint32_t M, N, kblocks;
   uint32_t out_f32;
-  uint32_t access;              // bytes an output row may be stored in at once: 32, 16, or its element's
+  uint32_t tma;                 // every output row starts 16-byte aligned
   uint32_t m_tiles, n_tiles;    // tile kernel: m_tiles counts pairs of 128 rows
   uint32_t* status;
 };
 
 // ---------------------------------------------------------------- many tiles
 constexpr int kStages = 4;
-constexpr int kAccWarps = 16;         // accumulating warps: four warpgroups of 64 columns each
-constexpr int kAccCols = 64;
+constexpr int kAccWarps = 8;          // accumulating warps: a warpgroup for each half tile
+constexpr int kAccCols = 128;
 constexpr int kTileThreads = 128 + 32 * kAccWarps;
-constexpr int kTileRegs = 96;         // what 65536 / 640 threads allows; split by setmaxnreg below
+constexpr int kTileRegs = 168;        // what 65536 / 384 threads allows; split by setmaxnreg below
 constexpr uint32_t kXBytes = kTileM * kKB, kWBytes = kTileN * kKB;
+constexpr uint32_t kStageBytes = 2560;
+constexpr int kScaleBlocks = 8;       // blocks whose scales are read together
 constexpr uint32_t kBand = 8;         // pairs of row tiles walked together, so their x stays in L2
 
 struct __align__(1024) TileSmem {
   uint8_t x[kStages][kXBytes];
   uint8_t w[kStages][kWBytes];
-  float stage[kAccWarps][16][33];      // per accumulating warp: 16 x 32 outputs on their way to narrow stores
+  uint8_t stage[kAccWarps][kStageBytes];       // per accumulating warp: 32 rows x 64 bytes of output, or 32 x 17 floats
+  float x_scale[2][kScaleBlocks][kTileM + 4];  // two chunks of blocks; rows padded against bank conflicts
+  float w_scale[2][2][kScaleBlocks];           // ... and half tiles
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[4], acc_empty[4];  // a half tile of 128 columns each
+  uint64_t scale_full[2], scale_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
@@ -117,20 +122,29 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, uint32_t rank,
 
 __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
-  const uint32_t idesc = make_idesc(kTileM, kTileN, 0, false);  // e4m3, both K-major
+  // e4m3, both K-major.  A block's two halves of 128 columns have accumulators
+  // of their own, so that the first is added up while the second is computed.
+  const uint32_t idesc = make_idesc(kTileM, kTileN / 2, 0, false);
+  const uint64_t x_desc = sw128_desc_at(smem_u32(s.x[0])), w_desc = sw128_desc_at(smem_u32(s.w[0]));
   uint32_t pos = 0;
   bool alive = true;
   for (uint32_t t = blockIdx.x >> 1; t < tiles && alive; t += gridDim.x >> 1) {
     for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
-      const uint32_t st = pos % kStages, buf = pos & 1u;
-      if (!(alive = mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort))) break;
+      const uint32_t st = pos % kStages;
       if (!(alive = mbar_wait(smem_u32(&s.full[st]), (pos / kStages) & 1u, abort))) break;
-      tc_fence_after();
-      const uint64_t ad = sw128_desc_at(smem_u32(s.x[st])), bd = sw128_desc_at(smem_u32(s.w[st]));
+      const uint64_t ad = x_desc + st * (kXBytes >> 4), bd = w_desc + st * (kWBytes >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) umma_f8_ss(tmem + buf * kTileN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+      for (uint32_t half = 0; half < 2; ++half) {
+        const uint32_t buf = (pos & 1u) * 2 + half;
+        if (!(alive = mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f8_ss(tmem + buf * (kTileN / 2), ad + 2 * k, bd + half * (kWBytes >> 5) + 2 * k, idesc, k != 0);
+        umma_commit(smem_u32(&s.acc_full[buf]));
+      }
+      if (!alive) break;
       umma_commit_multicast(smem_u32(&s.empty[st]), 3);
-      umma_commit(smem_u32(&s.acc_full[buf]));
     }
   }
   // No UMMA may still be in flight when tensor memory is released.
@@ -140,138 +154,151 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, vola
     if (global_timer_ns() - tw > kWaitTimeoutNs) break;
 }
 
-// Stores kAccCols output columns of row m from fp32 pairs.  Rows that allow wide
-// accesses are stored by their own thread; others go through shared memory,
-// so that a warp stores 32 neighbouring columns of one row at a time.
-template <typename Stage>
-__device__ __forceinline__ void store_row(const MatmulParams& p, Stage& stage, const uint64_t (&acc)[kAccCols / 2], uint32_t m,
-                                          uint32_t n0, int lane) {
-  if (p.access >= 16) {
-    if (m >= p.M) return;
-    if (p.out_f32) {
-      float* dst = static_cast<float*>(p.out) + m * p.out_row + n0;
+// One of two warps, 64 rows each: the scales of the tile's rows for
+// kScaleBlocks blocks at a time, and those of w, into shared memory, the next ones
+// already on their way.  A lane reads one block of every fourth row, so that eight
+// lanes share a 32-byte sector: a thread per row would touch a line of its own
+// for each block (measured: 8192^3 in 690 us against 463 us without the reads).
+__device__ void tile_scales(TileSmem& s, const MatmulParams& p, uint32_t rank, uint32_t half, int lane, volatile uint32_t* abort) {
+  const uint32_t tiles = p.m_tiles * p.n_tiles;
+  const uint32_t block = lane & (kScaleBlocks - 1), sub = lane / kScaleBlocks;
+  uint32_t pos = 0;
+  for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
+    uint32_t mt, nt;
+    tile_of(p, t, mt, nt);
+    const uint32_t m = (2 * mt + rank) * kTileM + half * 64 + sub, n = nt * kTileN + half * (kTileN / 2);
+    const float* ws = p.ws + (n < p.N ? n >> 7 : 0u) * p.ws_row;
+    float x[16] = {}, w = 0.f;
+    auto fetch = [&](uint32_t kb) {
+      if (kb >= p.kblocks) return;
+      w = __ldg(ws + kb * p.ws_col);
 #pragma unroll
-      for (int c = 0; c < kAccCols / 8; ++c) {
-        uint32_t w[8];
+      for (int i = 0; i < 16; ++i) x[i] = m + 4 * i < p.M ? __ldg(p.xs + (m + 4 * i) * p.xs_row + kb * p.xs_col) : 0.f;
+    };
+    fetch(block);
+    for (uint32_t kb = 0; kb < p.kblocks; kb += kScaleBlocks, ++pos) {
+      const uint32_t buf = pos & 1u;
+      if (!mbar_wait(smem_u32(&s.scale_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort)) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[2 * e] = static_cast<uint32_t>(acc[4 * c + e]);
-          w[2 * e + 1] = static_cast<uint32_t>(acc[4 * c + e] >> 32);
-        }
-        if (n0 + 8 * c + 8 <= p.N) {
-          if (p.access == 32) {
-            st_global_v8(dst + 8 * c, w);
-          } else {
-            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + 8 * c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-        } else {
+      for (int i = 0; i < 16; ++i) s.x_scale[buf][block][half * 64 + sub + 4 * i] = x[i];
+      if (sub == 0) s.w_scale[buf][half][block] = w;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.scale_full[buf]));
+      fetch(kb + kScaleBlocks + block);
+    }
+  }
+}
+
+// Stores kAccCols columns from n0 of a warp's 32 rows from m0 (a row per lane),
+// 64 bytes of every row at a time through the warp's staging buffer: by TMA, which
+// writes whole sectors while the warp goes on (a lane storing its own row would
+// touch a line of its own with every store: measured 11 000 cycles a tile), or, where
+// rows are not 16-byte aligned, by neighbouring lanes.
+__device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* stage, const float (&acc)[kAccCols], uint32_t m0,
+                                           uint32_t n0, int lane) {
+  if (p.tma) {
+    const uint32_t base = smem_u32(stage), row = base + lane * 64;
+    auto put = [&](uint32_t n, const uint32_t (&w)[16]) {
+      // The store that last read the buffer must be done with it.
+      if (lane == 0) bulk_wait_group_read<0>();
+      __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n0 + 8 * c + e < p.N) dst[8 * c + e] = __uint_as_float(w[e]);
-        }
+      for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((q ^ ((lane >> 1) & 3)) << 4)), "r"(w[4 * q]),
+                     "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && n < p.N && m0 < p.M) {
+        tma_store_2d(&p.tm_out, base, static_cast<int32_t>(n), static_cast<int32_t>(m0));
+        bulk_commit_group();
       }
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.out_row + n0;
+    };
+    uint32_t w[16];
+    if (p.out_f32) {
 #pragma unroll
       for (int c = 0; c < kAccCols / 16; ++c) {
-        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float lo, hi;
-          f2_unpack(acc[8 * c + e], lo, hi);
-          w[e] = pack_bf16x2(lo, hi);
-        }
-        if (n0 + 16 * c + 16 <= p.N) {
-          if (p.access == 32) {
-            st_global_v8(dst + 16 * c, w);
-          } else {
-            *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-        } else {
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[16 * c + e]);
+        put(n0 + 16 * c, w);
+      }
+    } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (n0 + 16 * c + e < p.N) dst[16 * c + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-        }
+      for (int c = 0; c < kAccCols / 32; ++c) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(acc[32 * c + 2 * e], acc[32 * c + 2 * e + 1]);
+        put(n0 + 32 * c, w);
       }
     }
     return;
   }
+  float* buf = reinterpret_cast<float*>(stage);
+  const uint32_t col = lane & 15, sub = lane >> 4;
 #pragma unroll
-  for (int c = 0; c < kAccCols / 32; ++c) {
+  for (int c = 0; c < kAccCols / 16; ++c) {
+    __syncwarp();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {   // rows 0..15, then 16..31 of the warp
-      __syncwarp();
-      if ((lane >> 4) == half) {
+    for (int e = 0; e < 16; ++e) buf[lane * 17 + e] = acc[16 * c + e];
+    __syncwarp();
+    const uint32_t n = n0 + 16 * c + col;
+    float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float lo, hi;
-          f2_unpack(acc[16 * c + e], lo, hi);
-          stage[lane & 15][2 * e] = lo;
-          stage[lane & 15][2 * e + 1] = hi;
-        }
-      }
-      __syncwarp();
-      const uint32_t n = n0 + 32 * c + lane, m0 = m - lane + 16 * half;
-      if (n < p.N) {
-#pragma unroll 4
-        for (int r = 0; r < 16; ++r) {
-          if (m0 + r >= p.M) break;
-          if (p.out_f32) static_cast<float*>(p.out)[(m0 + r) * p.out_row + n] = stage[r][lane];
-          else static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(stage[r][lane], 0.f));
-        }
+    for (int r = 0; r < 16; ++r) v[r] = buf[(2 * r + sub) * 17 + col];
+    if (n < p.N) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t m = m0 + 2 * r + sub;
+        if (m >= p.M) continue;
+        if (p.out_f32) static_cast<float*>(p.out)[m * p.out_row + n] = v[r];
+        else static_cast<uint16_t*>(p.out)[m * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(v[r], 0.f));
       }
     }
   }
 }
 
-// One of four warpgroups: columns [64 * group, 64 * group + 64) of the tile, a
-// row per thread.
-__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, int group, int quarter,
+// One of two warpgroups: half of the tile's columns, a row per thread.
+__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, uint32_t half, int quarter,
                                 int lane, volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
-  const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kAccCols;
-  uint32_t pos = 0;
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kAccCols;
+  uint32_t pos = 0, chunk = 0;
   for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
     uint32_t mt, nt;
     tile_of(p, t, mt, nt);
-    const uint32_t m = (2 * mt + rank) * kTileM + quarter * 32 + lane;
-    const uint32_t n0 = nt * kTileN + group * kAccCols;
-    const float* xs = p.xs + (m < p.M ? m : 0u) * p.xs_row;
-    const float* ws = p.ws + (n0 < p.N ? n0 >> 7 : 0u) * p.ws_row;
-    uint64_t acc[kAccCols / 2];
+    const uint32_t m0 = (2 * mt + rank) * kTileM + quarter * 32, n0 = nt * kTileN + half * kAccCols;
+    float acc[kAccCols];
 #pragma unroll
-    for (int e = 0; e < kAccCols / 2; ++e) acc[e] = 0;
-    float scale = __ldg(xs) * __ldg(ws);
+    for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
     for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
-      const uint32_t buf = pos & 1u;
-      const uint64_t s2 = f2_pack(scale, scale);
-      if (kb + 1 < p.kblocks) {
-        xs += p.xs_col;
-        ws += p.ws_col;
-        scale = __ldg(xs) * __ldg(ws);
+      const uint32_t buf = (pos & 1u) * 2 + half, at = kb % kScaleBlocks, cb = chunk & 1u;
+      if (at == 0 && !mbar_wait(smem_u32(&s.scale_full[cb]), (chunk >> 1) & 1u, abort)) return;
+      const float scale = s.x_scale[cb][at][quarter * 32 + lane] * s.w_scale[cb][half][at];
+      if (at == kScaleBlocks - 1 || kb + 1 == p.kblocks) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[cb]));
+        ++chunk;
       }
       if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) return;
       tc_fence_after();
-      const uint32_t col = taddr + buf * kTileN;
+      const uint32_t col = taddr + (pos & 1u) * kTileN;
+      uint32_t v[2][32];
+      tmem_ld_32x32b_x32(col, v[0]);
 #pragma unroll
       for (int c = 0; c < kAccCols / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(col + 32 * c, v);
         tmem_ld_wait();
-        if (c == kAccCols / 32 - 1) {
+        if (c + 1 < kAccCols / 32) {
+          tmem_ld_32x32b_x32(col + 32 * (c + 1), v[(c + 1) & 1]);
+        } else {
           // The accumulator is in registers: the block after next may use it.
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[16 * c + e] = f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2, acc[16 * c + e]);
+        for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(v[c & 1][e]), scale, acc[32 * c + e]);
       }
     }
-    store_row(p, s.stage[group * 4 + quarter], acc, m, n0, lane);
+    store_rows(p, s.stage[half * 4 + quarter], acc, m0, n0, lane);
   }
 }
 
@@ -288,9 +315,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 2);   // both CTAs' UMMA threads: a slot is filled for both at once
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
-      mbar_init(smem_u32(&s.acc_empty[i]), kAccWarps);
+      mbar_init(smem_u32(&s.acc_empty[i]), kAccWarps / 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.scale_full[i]), 2);
+      mbar_init(smem_u32(&s.scale_empty[i]), kAccWarps);
     }
     mbar_init(smem_u32(&s.drain), 1);
     fence_barrier_init();
@@ -306,13 +337,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (warp == 0 && lane == 0) tile_producer(s, p, rank, abort);
-    if (warp == 1 && lane == 0) tile_mma(s, p, tmem, abort);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0 && elect_one()) tile_producer(s, p, rank, abort);
+    if (warp == 1 && elect_one()) tile_mma(s, p, tmem, abort);
+    if (warp >= 2) tile_scales(s, p, rank, warp - 2, lane, abort);
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");  // 128 x 32 + 512 x 112 = 640 x 96
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 128 x 88 + 256 x 208 = 384 x 168
     tile_accumulate(s, p, tmem, rank, (warp - 4) >> 2, warp & 3, lane, abort);
+    if (lane == 0) bulk_wait_group_all();   // the staging buffers outlive their stores
   }
   tc_fence_before();
   cluster_sync();   // the other CTA no longer copies into this one or arrives on its barriers
@@ -612,9 +645,6 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   p.N = static_cast<uint32_t>(N);
   p.kblocks = static_cast<uint32_t>(kb);
   p.out_f32 = out->dtype == MLA_DTYPE_F32;
-  const uint32_t es = p.out_f32 ? 4 : 2;
-  const uint64_t place = reinterpret_cast<uintptr_t>(out->data) | (M > 1 ? static_cast<uint64_t>(out->stride[0]) * es : 0);
-  p.access = place % 32 == 0 ? 32 : place % 16 == 0 ? 16 : es;
   p.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
@@ -624,6 +654,16 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
     if (pairs * wide > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
     if ((st = encode_codes(&p.tm_x, x, kTileM, "x")) != MLA_OK) return st;
     if ((st = encode_codes(&p.tm_w, w, kTileN / 2, "w")) != MLA_OK) return st;
+    const uint64_t es = p.out_f32 ? 4 : 2;
+    p.tma = aligned16(out->data) && (static_cast<uint64_t>(out->stride[0]) * es) % 16 == 0 && out->stride[0] < (1ll << 38);
+    if (p.tma) {
+      const uint64_t dims[2] = {static_cast<uint64_t>(N), static_cast<uint64_t>(M)};
+      const uint64_t str[1] = {static_cast<uint64_t>(out->stride[0]) * es};
+      const uint32_t box[2] = {static_cast<uint32_t>(64 / es), 32};
+      if ((st = encode_tiled(&p.tm_out, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                             out->data, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B, "out")) != MLA_OK)
+        return st;
+    }
     p.m_tiles = static_cast<uint32_t>(pairs);
     p.n_tiles = static_cast<uint32_t>(wide);
     const int smem = static_cast<int>(sizeof(TileSmem) + 1024);
