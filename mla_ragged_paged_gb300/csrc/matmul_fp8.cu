@@ -8,16 +8,19 @@
 // registers while the tensor cores work on the next block in the other half of
 // tensor memory.  No sum ever passes through fewer than 32 bits.
 //
-// Two kernels:
-// * matmul_tile_kernel, for products with enough output tiles to fill the
-//   GPU: persistent CTA pairs, each CTA one 128 x 256 output tile.  Bound by the
-//   tensor cores and the power limit; the pair shares its weight tile by TMA
-//   multicast, because one SM's share of the L2 cannot feed 48 KB per 512
-//   tensor-core cycles.
-// * matmul_thin_kernel, for the others (few tokens): HBM-bound on w.  The
-//   weights are the 128-row operand and the tokens the narrow one, so few rows
-//   waste no tensor time, and K is split over a cluster of up to eight CTAs whose
-//   partial sums meet in distributed shared memory, in rank order.
+// Two kernels (the host's rule compares their expected times):
+// * matmul_tile_kernel, for products with many output tiles: persistent CTA
+//   pairs, each CTA one 128 x 256 output tile; the pair shares its weight tile by
+//   TMA multicast, because one SM's share of the L2 cannot feed 48 KB per 512
+//   tensor-core cycles.  Measured 8192^3 in 434 us = 2530 TFLOP/s; of that the
+//   loads alone take 350 us and reading back 128 KB of tensor memory per block
+//   beside 32 768 products in fp32 most of the rest (bound by the two warps per
+//   scheduler that wait for tensor memory and multiply in turn).
+// * matmul_thin_kernel, for few tokens: bound by HBM (w), 5.2 TB/s at
+//   64 x 8192 x 16384 (28 us).  The weights are the 128-row operand and the tokens the
+//   narrow one, so few rows waste no tensor time, and K is split over a cluster of
+//   up to eight CTAs whose partial sums meet in distributed shared memory, in rank
+//   order.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -357,7 +360,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
-constexpr int kThinThreads = 192;
+constexpr int kThinThreads = 320;             // producer, UMMA, eight accumulating warps
+constexpr uint32_t kThinBufs = 4;             // accumulators in tensor memory
 constexpr uint32_t kThinSmem = 112 * 1024;   // two CTAs per SM
 
 // MT tokens per CTA (the UMMA's N), 128 weight rows (its M).
@@ -366,9 +370,9 @@ struct __align__(1024) ThinSmem {
   static constexpr int kRing = (kThinSmem - 8192 - 2048) / (128 * kKB + MT * kKB);
   uint8_t w[kRing][128 * kKB];
   uint8_t x[kRing][MT * kKB];
-  float scale[4][2][MT];       // per accumulating warp: this block's and the next one's scales
+  float scale[2][2][kScaleBlocks][MT / 2 + 4];  // per warpgroup, two chunks of blocks: its tokens' scales
   uint64_t full[kRing], empty[kRing];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kThinBufs], acc_empty[kThinBufs];
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
@@ -379,8 +383,8 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
                                                                       const uint32_t splits) {
   using Smem = ThinSmem<MT>;
   constexpr int kRing = Smem::kRing;
-  constexpr uint32_t kCols = MT < 16 ? 16 : MT;          // tensor-memory columns of one accumulator
-  constexpr uint32_t kAlloc = 2 * kCols < 32 ? 32 : 2 * kCols;
+  constexpr uint32_t kCols = MT;                         // tensor-memory columns of one accumulator
+  constexpr uint32_t kAlloc = kThinBufs * kCols;
   static_assert(sizeof(Smem) + 1024 <= kThinSmem, "matmul thin shared memory");
   static_assert(sizeof(float) * MT * 128 <= kRing * (128 + MT) * kKB, "the partial sums take the ring's place");
   extern __shared__ uint8_t smem_raw[];
@@ -389,17 +393,18 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
   volatile uint32_t* abort = &s.abort_flag;
   const uint32_t rank = blockIdx.x % splits, tile = blockIdx.x / splits;
   const uint32_t nt = tile % p.n_tiles, mt = tile / p.n_tiles;
-  const uint32_t kb0 = static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * rank / splits);
-  const uint32_t kb1 = static_cast<uint32_t>(static_cast<uint64_t>(p.kblocks) * (rank + 1) / splits);
+  // The cluster's CTAs take neighbouring blocks of K, so that together they read
+  // longer pieces of a weight row at a time.
+  const uint32_t kb0 = rank, kb1 = p.kblocks;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < kThinBufs; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
-      mbar_init(smem_u32(&s.acc_empty[i]), 4);
+      mbar_init(smem_u32(&s.acc_empty[i]), 8);
     }
     mbar_init(smem_u32(&s.drain), 1);
     fence_barrier_init();
@@ -412,11 +417,16 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  float acc[MT];
+  // Two accumulating warpgroups of half the tokens each: lane = weight row,
+  // register = token.  (One of them left the block's read-back and its 64
+  // products a row as the longest step: 33 us for 64 x 8192 x 16384.)
+  constexpr int N = MT / 2;
+  const int quarter = warp & 3, group = (warp - 2) >> 2;
+  float acc[N];
   if (warp == 0) {
     if (lane == 0) {
       uint32_t pos = 0;
-      for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
+      for (uint32_t kb = kb0; kb < kb1; kb += splits, ++pos) {
         const uint32_t st = pos % kRing;
         if (!mbar_wait(smem_u32(&s.empty[st]), ((pos / kRing) & 1u) ^ 1u, abort)) break;
         const uint32_t bar = smem_u32(&s.full[st]);
@@ -436,12 +446,12 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = make_idesc(128, MT, 0, false);
       uint32_t pos = 0;
-      for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
-        const uint32_t st = pos % kRing, buf = pos & 1u;
-        if (!mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort)) break;
+      for (uint32_t kb = kb0; kb < kb1; kb += splits, ++pos) {
+        const uint32_t st = pos % kRing, buf = pos % kThinBufs;
+        if (!mbar_wait(smem_u32(&s.acc_empty[buf]), ((pos / kThinBufs) & 1u) ^ 1u, abort)) break;
         if (!mbar_wait(smem_u32(&s.full[st]), (pos / kRing) & 1u, abort)) break;
         tc_fence_after();
         const uint64_t ad = sw128_desc_at(smem_u32(s.w[st])), bd = sw128_desc_at(smem_u32(s.x[st]));
@@ -457,88 +467,96 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
     }
     __syncwarp();
   } else {
-    // Lane = weight row, register = token.
-    const int quarter = warp & 3;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * N;
     const float* ws = p.ws + nt * p.ws_row;
-    constexpr int kPer = (MT + 31) / 32;
-    float next[kPer];
-    auto fetch = [&](uint32_t kb) {
-      const float w = __ldg(ws + kb * p.ws_col);
+    // Scales, kScaleBlocks of this CTA's blocks at a time, the next ones already
+    // on their way: a lane reads one block of every fourth token, so that eight
+    // lanes share a line; the warpgroup's warps share the tokens out and meet at
+    // a named barrier.  (A warp never leaves early: after a wait that gave up it
+    // goes on with values that mean nothing, so that the barrier always completes.)
+    constexpr int kTurns = (N / 4 + 3) / 4;
+    const uint32_t block = lane & (kScaleBlocks - 1), sub = lane / kScaleBlocks;
+    float next_x[kTurns] = {}, next_w = 0.f;
+    auto fetch = [&](uint32_t first) {
+      const uint32_t kb = first + block * splits;
+      if (kb >= kb1) return;
+      next_w = __ldg(ws + kb * p.ws_col);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t m = mt * MT + i * 32 + lane;
-        next[i] = i * 32 + lane < MT && m < p.M ? __ldg(p.xs + m * p.xs_row + kb * p.xs_col) * w : 0.f;
+      for (int i = 0; i < kTurns; ++i) {
+        const uint32_t tok = 4 * (quarter + 4 * i) + sub, m = mt * MT + group * N + tok;
+        if (tok < N && m < p.M) next_x[i] = __ldg(p.xs + m * p.xs_row + kb * p.xs_col);
       }
     };
 #pragma unroll
-    for (int e = 0; e < MT; ++e) acc[e] = 0.f;
-    if (kb0 < kb1) fetch(kb0);
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    fetch(kb0);
     uint32_t pos = 0;
-    for (uint32_t kb = kb0; kb < kb1; ++kb, ++pos) {
-      const uint32_t buf = pos & 1u;
-      float* sc = s.scale[quarter][buf];
+    for (uint32_t kb = kb0; kb < kb1; kb += splits, ++pos) {
+      const uint32_t buf = pos % kThinBufs, at = pos % kScaleBlocks, chunk = (pos / kScaleBlocks) & 1u;
+      if (at == 0) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i * 32 + lane < MT) sc[i * 32 + lane] = next[i];
-      __syncwarp();
-      if (kb + 1 < kb1) fetch(kb + 1);
-      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) break;
+        for (int i = 0; i < kTurns; ++i) {
+          const uint32_t tok = 4 * (quarter + 4 * i) + sub;
+          if (tok < N) s.scale[group][chunk][block][tok] = next_x[i] * next_w;
+        }
+        named_bar_sync(1 + group, 128);
+        fetch(kb + kScaleBlocks * splits);
+      }
+      const float* sc = s.scale[group][chunk][at];
+      mbar_wait(smem_u32(&s.acc_full[buf]), (pos / kThinBufs) & 1u, abort);
       tc_fence_after();
+      constexpr int kPart = N < 16 ? N : 16;
 #pragma unroll
-      for (int c = 0; c < MT / 16; ++c) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(taddr + buf * kCols + 16 * c, v);
+      for (int c = 0; c < N; c += kPart) {
+        uint32_t v[kPart];
+        if constexpr (kPart == 16) tmem_ld_32x32b_x16(taddr + buf * kCols + c, v);
+        else tmem_ld_32x32b_x8(taddr + buf * kCols + c, v);
         tmem_ld_wait();
-        if (c == MT / 16 - 1) {
+        if (c + kPart == N) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s.acc_empty[buf]));
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(sc + 16 * c + e);
-          acc[16 * c + e] = fmaf(__uint_as_float(v[e]), f.x, acc[16 * c + e]);
-          acc[16 * c + e + 1] = fmaf(__uint_as_float(v[e + 1]), f.y, acc[16 * c + e + 1]);
-          acc[16 * c + e + 2] = fmaf(__uint_as_float(v[e + 2]), f.z, acc[16 * c + e + 2]);
-          acc[16 * c + e + 3] = fmaf(__uint_as_float(v[e + 3]), f.w, acc[16 * c + e + 3]);
+        for (int e = 0; e < kPart; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sc + c + e);
+          acc[c + e] = fmaf(__uint_as_float(v[e]), f.x, acc[c + e]);
+          acc[c + e + 1] = fmaf(__uint_as_float(v[e + 1]), f.y, acc[c + e + 1]);
+          acc[c + e + 2] = fmaf(__uint_as_float(v[e + 2]), f.z, acc[c + e + 2]);
+          acc[c + e + 3] = fmaf(__uint_as_float(v[e + 3]), f.w, acc[c + e + 3]);
         }
       }
     }
   }
-  const uint32_t n = nt * 128 + (warp & 3) * 32 + lane, m0 = mt * MT;
-  auto store = [&](uint32_t m, float v) {
-    if (p.out_f32) static_cast<float*>(p.out)[m * p.out_row + n] = v;
-    else static_cast<uint16_t*>(p.out)[m * p.out_row + n] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-  };
-  if (splits == 1) {
-    if (warp >= 2 && n < p.N) {
+  // The sums go through shared memory in the ring's place (all its copies and
+  // UMMAs are done: every block's accumulator has been read).  With K split each
+  // CTA of the cluster adds the ranks' sums of its share of the tokens, in rank
+  // order; lanes store neighbouring columns, whatever the rows' alignment.
+  const uint32_t column = quarter * 32 + lane, n = nt * 128 + column, m0 = mt * MT;
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(s.w);
+  if (warp >= 2) {
 #pragma unroll
-      for (int e = 0; e < MT; ++e)
-        if (m0 + e < p.M) store(m0 + e, acc[e]);
-    }
-  } else {
-    // Partial sums into the ring's place (all its copies and UMMAs are done:
-    // every block's accumulator has been read), then each CTA of the cluster
-    // adds the ranks' sums of its share of the tokens, in rank order.
-    __syncthreads();
-    float* part = reinterpret_cast<float*>(s.w);
-    if (warp >= 2) {
-#pragma unroll
-      for (int e = 0; e < MT; ++e) part[e * 128 + (warp & 3) * 32 + lane] = acc[e];
-    }
-    cluster_sync();
-    if (warp >= 2 && n < p.N) {
-      const uint32_t e1 = min(static_cast<uint32_t>(MT), p.M - m0);
-      const uint32_t base = smem_u32(part) + ((warp & 3) * 32 + lane) * 4;
-      for (uint32_t e = rank; e < e1; e += splits) {
-        float v = 0.f;
-        for (uint32_t r = 0; r < splits; ++r) v += ld_shared_cluster(map_shared(base + e * 512, r));
-        store(m0 + e, v);
-      }
-    }
-    cluster_sync();
+    for (int e = 0; e < N; ++e) part[(group * N + e) * 128 + column] = acc[e];
   }
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+  if (warp >= 2 && n < p.N) {
+    const uint32_t e1 = min(static_cast<uint32_t>(MT), p.M - m0), base = smem_u32(part) + column * 4;
+    // Tokens rank + splits * i; the warpgroups take turns.
+    const uint32_t first = rank + splits * group, step = 2 * splits;
+    long long at = (m0 + first) * p.out_row + n;
+#pragma unroll 4
+    for (uint32_t e = first; e < e1; e += step, at += step * p.out_row) {
+      float v = 0.f;
+      if (splits == 1) v = part[e * 128 + column];
+      else
+        for (uint32_t r = 0; r < splits; ++r) v += ld_shared_cluster(map_shared(base + e * 512, r));
+      if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+      else static_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
+    }
+  }
+  if (splits > 1) cluster_sync();   // no CTA leaves while another reads its sums
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -649,8 +667,15 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;
-  // The tile kernel needs a tile for most SMs (2 x pairs x wide of them).
-  if (M > 128 && 2 * pairs * wide >= static_cast<uint64_t>(sms) * 2 / 3) {
+  // Whichever kernel is expected to end first, from what both measured (us, tile /
+  // thin): 200x8192x8192 33 / 38, 300x4096x4096 19 / 21, 1024x2048x2048 12 / 14,
+  // 256x16384x512 7.3 / 15, but 512x1024x8192 33 / 16, 1000x576x8192 33 / 23,
+  // 128x8192x8192 33 / 25.  The tile kernel takes 0.45 us a block of K for each
+  // round of its CTA pairs, the thin one 2.1 ns a block of 128 x 64 outputs and
+  // 1.3 us more at its ends.
+  const uint64_t rounds = (pairs * wide + sms / 2 - 1) / (sms / 2);
+  const uint64_t thin_blocks = static_cast<uint64_t>((M + 63) / 64) * ((N + 127) / 128) * kb;
+  if (M > 64 && 4500 * kb * rounds < 13000 + 21 * thin_blocks) {
     if (pairs * wide > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
     if ((st = encode_codes(&p.tm_x, x, kTileM, "x")) != MLA_OK) return st;
     if ((st = encode_codes(&p.tm_w, w, kTileN / 2, "w")) != MLA_OK) return st;
@@ -675,7 +700,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
     if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
     return MLA_OK;
   }
-  const uint32_t mt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const uint32_t mt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   if ((st = encode_codes(&p.tm_x, x, mt, "x")) != MLA_OK) return st;
   if ((st = encode_codes(&p.tm_w, w, 128, "w")) != MLA_OK) return st;
   p.m_tiles = static_cast<uint32_t>((M + mt - 1) / mt);
@@ -683,7 +708,6 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   switch (mt) {
     case 16: return launch_thin<16>(p, dev, sms, 9, s);
     case 32: return launch_thin<32>(p, dev, sms, 10, s);
-    case 64: return launch_thin<64>(p, dev, sms, 11, s);
-    default: return launch_thin<128>(p, dev, sms, 12, s);
+    default: return launch_thin<64>(p, dev, sms, 11, s);
   }
 }
