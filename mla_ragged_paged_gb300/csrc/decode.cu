@@ -270,6 +270,14 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
         walk[e].next(p);
       }
       look_up(kt + 1);
+      if (boxed && lane < boxes) {
+        // The tile's shared memory comes free chunk by chunk, most of a tile's time
+        // from now; into L2 the rows can come at once (measured: 118 -> 108 us
+        // for 152 sequences x 4500 x 64 heads).
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, rows[0]);
+        tma_prefetch_2d(&p.tm_rope, kLatent, rows[0]);
+      }
       for (int c = 0; c < 5 && alive; ++c) {
         const Place<NR> at_c(tile, c);
         const uint32_t rs = tile % R::kRopeSlots;
@@ -442,11 +450,12 @@ __device__ void load_queries(DecodeSmem<NR>& s, const DecodeParams& p, const Seg
     for (int h = 0; h < 2; ++h) {
       const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = max(m, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+      for (int e = 0; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
     }
   }
 #pragma unroll
-  for (int o = kPer / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = kPer / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = max(m << 16, m & 0xFFFF0000u);   // the larger of the pair of bf16 values, as fp32 bits
   // A power of two that takes the row's largest value into [128, 256); a row
   // with an infinity or a NaN becomes NaN codes.
   int k = 134 - static_cast<int>(m >> 23);
