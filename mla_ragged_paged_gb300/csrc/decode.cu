@@ -259,6 +259,14 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
       }
     };
     look_up(g.kt0);
+    // The segment's queries into L2: the softmax warps come to them up to two
+    // tiles later, and would wait for HBM.
+    for (uint32_t r = lane; r < NR && g.rt * NR + r < g.s.rows; r += 32) {
+      const uint32_t row = g.rt * NR + r, tok = row / p.H;
+      const uint16_t* q = p.q + (g.s.q0 + static_cast<long long>(tok)) * p.q_tok + (row - tok * p.H) * p.q_head;
+#pragma unroll
+      for (int i = 0; i < kWidth; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+    }
     for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
       int32_t rows[4];
 #pragma unroll
@@ -530,7 +538,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
   auto fmax2 = [](float a, float b) { return fmaxf(a, b); };
   auto add2 = [](float a, float b) { return a + b; };
   uint32_t tile = 0;
-  uint32_t head_valid = 0, part_b = 0, part_rt = 0, part_last = 0;
+  uint32_t head_valid = 0, part_b = 0, part_rt = 0, part_rest = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
     const uint32_t first_row = g.rt * NR, tok0 = first_row / p.H;
@@ -736,16 +744,18 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     // ---- the segment's result
     softmax_wait(smem_u32(&s.pv_done), (tile - 1) & 1u, abort);
     tc_fence_after();
-    auto row_sum = [&](const float (&v)[N]) {
-      const float mine = warp_transpose_reduce<N>(v, lane, add2);
-      if (lane < N) s.warp_red[group][quarter][lane] = mine;
-      named_bar_sync(bar, 128);
-      const float sum = (s.warp_red[group][0][my_row] + s.warp_red[group][1][my_row]) +
-                        (s.warp_red[group][2][my_row] + s.warp_red[group][3][my_row]);
-      named_bar_sync(bar, 128);
-      return sum;
+    // The rows' sums over the warps meet in P's place, which is free now.
+    float(*sums)[4][2][N] = reinterpret_cast<float(*)[4][2][N]>(s.p);
+    const float mine = warp_transpose_reduce<N>(l, lane, add2), mine_q = warp_transpose_reduce<N>(lq, lane, add2);
+    if (lane < N) {
+      sums[group][quarter][0][lane] = mine;
+      sums[group][quarter][1][lane] = mine_q;
+    }
+    named_bar_sync(bar, 128);
+    auto row_sum = [&](int k) {
+      return (sums[group][0][k][my_row] + sums[group][1][k][my_row]) + (sums[group][2][k][my_row] + sums[group][3][k][my_row]);
     };
-    const float total = row_sum(l), seen = row_sum(lq);
+    const float total = row_sum(0), seen = row_sum(1);
     const bool begins = g.kt0 == 0, ends = g.kt1 == g.s.key_tiles;
     const bool whole = begins && ends;
     const uint32_t slot = 2 * blockIdx.x + (begins ? 1 : 0);
@@ -794,14 +804,17 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       head_valid = 1;
       part_b = g.b;
       part_rt = g.rt;
-      // The CTA that holds the row tile's last key tile.
-      const unsigned long long u1 = units * (blockIdx.x + 1) / ctas, last = u1 + (g.s.key_tiles - g.kt1) - 1;
-      part_last = static_cast<uint32_t>(((last + 1) * ctas - 1) / units);
+      part_rest = g.s.key_tiles - g.kt1;
     }
-    named_bar_sync(bar, 128);                            // row_val and warp_red are free again
+    named_bar_sync(bar, 128);                            // row_val and P are free again
   }
   if (tid == 0) {
-    PartHeader h = {head_valid, part_b, part_rt, part_last};
+    PartHeader h = {head_valid, part_b, part_rt, 0u};
+    if (head_valid) {
+      // The CTA that holds the row tile's last key tile.
+      const unsigned long long last = units * (blockIdx.x + 1) / ctas + part_rest - 1;
+      h.last_cta = static_cast<uint32_t>(((last + 1) * ctas - 1) / units);
+    }
     p.headers[blockIdx.x] = h;
   }
 }
