@@ -63,8 +63,8 @@ typedef enum {
 typedef enum {
   MLA_SCALE_NONE = 0,
   MLA_SCALE_PER_TENSOR = 1, /* `scale` points at one float */
-  MLA_SCALE_PER_TOKEN = 2,  /* one float per token: K_rope pool slot (index page * P + slot),
-                               contiguous K_rope row, or fp8 K_nope row (index = K row) */
+  MLA_SCALE_PER_TOKEN = 2,  /* one float per token: K_rope pool or latent cache slot (index page * P +
+                               slot), contiguous K_rope row, or fp8 K_nope row (index = K row) */
 } mla_scale_gran_t;
 
 /* A strided view of device memory.  `data` addresses element [0, 0, ...];
@@ -638,16 +638,21 @@ size_t mla_decode_latent_workspace_size(void);
  *   q            device bf16 [Tq, H, 576]; 1 <= H <= 1024
  *   cache        device e4m3 [num_pages, P, 576], pages contiguous (page
  *                stride = P x token stride), token stride a multiple of 16
- *                bytes; scales per token ([num_pages * P] floats) or one for all
+ *                bytes; positive scales, per token ([num_pages * P] floats) or
+ *                one for all.  Pages of a multiple of 8 tokens are read in boxes,
+ *                others row by row (about two thirds slower)
  *   page_table   device uint32 [B, max_pages], B <= 16384
  *   row_offsets, cache_lens, scale, mask  as in mla_prefill_ragged
  *   status       device uint32 or NULL: an out-of-range page id or page-table
  *                column ORs MLA_DEVICE_STATUS_BAD_PAGE / _BAD_COLUMN and its
  *                keys count as masked; a pipeline wait that gives up ORs
- *                MLA_DEVICE_STATUS_TIMEOUT
+ *                MLA_DEVICE_STATUS_TIMEOUT; row offsets that decrease or exceed
+ *                Tq OR MLA_DEVICE_STATUS_BAD_OFFSETS and skip their sequence
  *   workspace    device, mla_decode_latent_workspace_size() bytes, 256-byte
  *                aligned; its contents before the call do not matter.  Calls
  *                that may overlap on the GPU need distinct workspaces.
+ * Sums and softmax statistics are 32-bit; the weights that multiply the cached
+ * codes carry seven significant bits and are normalised by their own sum.
  * Slots past a sequence's context may hold anything.  A query all of whose
  * keys are masked gets 0 and lse -inf.  Rows outside [row_offsets[0],
  * row_offsets[B]) are not written.

@@ -183,6 +183,21 @@ def test_matmul_strides(lib, m, n, k, dtype):
     assert (buf == 3).all()
 
 
+@pytest.mark.parametrize("dtype,pad", [(torch.bfloat16, 24), (torch.float32, 4), (torch.float32, 12)])
+def test_matmul_aligned_padded_rows(lib, dtype, pad):
+    """Output rows that start 16-byte aligned and end inside a store's width:
+    what lies behind them stays."""
+    from mla_ragged_paged_gb300 import binding
+    m, n, k = 700, 2280, 400
+    x, xs, w, ws = _matmul_case(m, n, k, 4)
+    buf = torch.full((m + 1, n + pad), 3.0, dtype=dtype, device="cuda")
+    out = buf[:m, :n]
+    binding.matmul_fp8(out, x, xs, w, ws)
+    _check_matmul(out, x, xs, w, ws)
+    out.fill_(3)
+    assert (buf == 3).all()
+
+
 def test_matmul_accumulates_in_32_bits(lib):
     """Terms that a narrower accumulator would lose: one large product, then
     many small ones that sum to something of float32's resolution of it."""
@@ -449,6 +464,80 @@ def test_decode_repeats_and_shares_a_workspace(lib):
         again, _ = _run_decode(a)
     side.synchronize()
     assert torch.equal(again, first)
+
+
+def test_decode_graph_follows_lengths(lib):
+    """A captured call reads lengths, offsets and pages when it runs: replays
+    after the sequences have grown, and with one of them gone."""
+    from mla_ragged_paged_gb300 import binding
+    d = Decode([1, 1, 1], [700, 90, 2000], 16, 16, seed=61)
+    ro, cl = (t.cuda() for t in d.offsets())
+    q, cache, scales, table = d.q.cuda(), d.codes.cuda(), d.scales.cuda(), d.table.cuda()
+    out = torch.empty(3, 16, LATENT, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, 16, device="cuda")
+    ws = binding.alloc_decode_workspace()
+    call = lambda: binding.decode_latent(out, q, cache, scales, table, ro, cl, d.scale, workspace=ws, lse=lse)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for prior, offsets in [([3, 90, 1200], [0, 1, 2, 3]), ([700, 0, 2000], [0, 1, 2, 3]), ([700, 90, 15], [0, 1, 1, 3])]:
+        cl.copy_(torch.tensor(prior, dtype=torch.int32))
+        ro.copy_(torch.tensor(offsets, dtype=torch.int32))
+        d.prior, d.ro = prior, np.array(offsets)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_decode(d, out, lse)
+
+
+def test_decode_on_two_streams(lib):
+    """Two calls that overlap, each with its own workspace."""
+    from mla_ragged_paged_gb300 import binding
+    a, b = Decode([1], [9000], 64, 64, seed=62), Decode([1] * 6, [1500] * 6, 16, 64, seed=63)
+    ref_a, ref_b = _run_decode(a)[0], _run_decode(b)[0]
+    _check_decode(a, ref_a, None)
+    _check_decode(b, ref_b, None)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for d, st in ((a, streams[0]), (b, streams[1])):
+            with torch.cuda.stream(st):
+                outs.append((d, _run_decode(d, lse=False)[0]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref_a if d is a else ref_b) for d, o in outs)
+
+
+def test_decode_impossible_lengths_and_offsets(lib):
+    """A length past the page table masks the keys there; offsets that decrease
+    or leave the queries skip their sequence; the others are right."""
+    d = Decode([1, 1, 1, 1], [40, 100, 60, 30], 8, 16, seed=64)
+    d.prior = [40, -1, 60, 30]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = _run_decode(d, status=status)
+    assert int(status) & 0x2
+    d.prior[1] = 100
+    keep = [0, 2, 3]
+    ref, _, mag, _ = ora.decode(d.q.float().numpy(), d.codes.numpy(), d.scales.numpy(), d.table.numpy(), d.ro, d.prior,
+                                d.scale)
+    tol = 2.0 ** -6 * mag + 2.0 ** -8 * np.abs(ref)
+    _within(_f64(out)[keep], ref[keep], tol[keep], "out")
+    for bad in ([0, 3, 2, 3, 4], [0, 1, 2, 3, 9]):
+        d.ro = np.array(bad)
+        status.zero_()
+        out, _ = _run_decode(d, status=status)
+        assert int(status) & 0x4
+        if bad[1] == 1:                         # sequence 0 has its offsets still
+            _within(_f64(out)[0], ref[0], tol[0], "out")
+
+
+def test_decode_many_heads(lib):
+    d = Decode([1, 2], [70, 300], 1024, 64, seed=65)
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
 
 
 def test_decode_offsets_past_32_bits(lib):
