@@ -4,10 +4,14 @@
 // written at the slot of its context position, page_table[b, a / P] * P + a % P
 // with a = cache_lens[b] + i for new token i of sequence b.
 //
-// HBM-bound: 2 W bytes read, W + 4 written per token.  One warp per row, the
-// row in registers between its maximum and its codes; the row's sequence is
-// found by a 32-way search (one load per lane and step: two dependent reads
-// for up to 1024 sequences instead of ten).
+// 2 W bytes read, W + 4 written per token.  One warp per row, the row in registers
+// between its maximum and its codes; the row's sequence is found by a 32-way search
+// (one load per lane and step: two dependent reads for up to 1024 sequences instead
+// of ten).  32768 rows of 576 (16 sequences): 15.7 us = 3.6 TB/s; bound by the chain
+// of search, length, page and maximum that each short-lived warp walks, and by the
+// instructions of the quotients (13.4 us with single products in their place).  Warps
+// that walk several rows and keep sequence and page hold twice the registers and
+// measured slower (21.5 against 20.5 us before the quotients were shortened).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -50,6 +54,38 @@ __device__ __forceinline__ uint32_t find_sequence(const uint32_t* ro, uint32_t B
   return lo;
 }
 
+// The codes of eight bf16 numbers x divided by scale = fl(amax / 448), as if each
+// quotient were first rounded to fp32 (as a plain program rounds it).  A correctly
+// rounded division for each number would be most of the kernel's work (32768 rows of
+// 576: 21.1 us, without any 13.4 us), so the product with `to` = fl(1 / scale) is
+// corrected once by its remainder, which an fma gives exactly (Markstein, IBM J. Res.
+// Dev. 34, 1990): that is the rounded x / scale (1 + d), |d| < 2^-46.  Its code can
+// differ from the division's only next to a tie T of e4m3.  There 448 x = T amax
+// exactly, because products of 3 and 8 and of 5 and 8 significant bits that differ
+// do so by 2^-13 of their size; so the two mantissas decide, and all 128 x 128 pairs
+// are tested.  (-r in both places: a negative zero keeps its sign.)
+__device__ __forceinline__ uint2 codes8(const uint4& v, float scale, float to) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[4];
+  auto over = [&](float x) {
+    const float g = x * to, r = fmaf(g, scale, -x);
+    return fmaf(-r, to, g);
+  };
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    q[e] = pack_e4m3x2(over(__uint_as_float(w[e] << 16)), over(__uint_as_float(w[e] & 0xFFFF0000u)));
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+// By division: scales whose remainders could underflow, infinity, NaN.
+__device__ __noinline__ uint2 codes8_extreme(uint4 v, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    q[e] = pack_e4m3x2(__fdiv_rn(__uint_as_float(w[e] << 16), scale), __fdiv_rn(__uint_as_float(w[e] & 0xFFFF0000u), scale));
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
 template <int CH>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
@@ -90,6 +126,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
   for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   m = max(m, __float_as_uint(1e-30f));
   const float scale = __fdiv_rn(__uint_as_float(m), 448.f);
+  const float to = __fdiv_rn(1.f, scale);
+  const bool plain = scale >= 0x1p-80f && scale <= 0x1p100f;
   const uint32_t slot = static_cast<uint32_t>(a - col * p.P);
   if (lane == 0) p.scales[static_cast<long long>(page) * p.P + slot] = scale;
   uint8_t* dst = p.cache + page * p.page_bytes + slot * p.tok_bytes;
@@ -97,13 +135,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
   for (int c = 0; c < CH; ++c) {
     const uint32_t i = c * 32 + lane;
     if (i >= p.chunks) continue;
-    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-    uint32_t q[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      q[e] = pack_e4m3x2(__fdiv_rn(__uint_as_float(w[e] << 16), scale),
-                         __fdiv_rn(__uint_as_float(w[e] & 0xFFFF0000u), scale));
-    *reinterpret_cast<uint2*>(dst + 8 * i) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    *reinterpret_cast<uint2*>(dst + 8 * i) = plain ? codes8(v[c], scale, to) : codes8_extreme(v[c], scale);
   }
 }
 

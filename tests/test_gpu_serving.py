@@ -274,6 +274,31 @@ def test_append(lib, W, P, new, prior):
     assert (wide[:, :, W:] == 9).all() and int(status) == 0
 
 
+def test_append_codes_next_to_ties(lib):
+    """Every bf16 mantissa at seven exponents over every mantissa of the largest number:
+    quotients on both sides of a tie and on it, subnormal codes, infinities."""
+    from mla_ragged_paged_gb300 import binding
+    W = 896
+    mantissas = torch.arange(128) / 128 + 1
+    body = (mantissas[None] * 2.0 ** torch.tensor([-1, -2, -5, -11, -14, -15, -16])[:, None]).reshape(-1)
+    rows = body.repeat(129, 1) * torch.where(torch.arange(W) % 3 == 0, -1.0, 1.0)
+    rows[:128, 5] = 2 * mantissas
+    rows[128, 5] = float("inf")
+    rows = torch.cat([rows, rows[:128] * 2.0 ** -100, rows[:128] * 2.0 ** 120]).to(torch.bfloat16)
+    n = rows.shape[0]
+    cache = torch.zeros(1, n, W, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(1, n, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.append_latent(cache, scales, rows.cuda(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                          torch.tensor([0, n], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda(), status)
+    want = rows.float().abs().amax(1).clamp_min(1e-30) / 448
+    quotient = rows.float() / want[:, None]
+    assert int(status) == 0 and torch.equal(scales.cpu()[0], want)
+    assert torch.equal(cache.cpu()[0] & 0x7F, quotient.to(E4M3).view(torch.uint8) & 0x7F)
+    finite = quotient == quotient
+    assert torch.equal(cache.cpu()[0][finite], quotient.to(E4M3).view(torch.uint8)[finite])
+
+
 def test_append_bad_pages_and_nan(lib):
     from mla_ragged_paged_gb300 import binding
     table = torch.tensor([[1, 99], [0, 2]], dtype=torch.int32, device="cuda")
