@@ -37,8 +37,11 @@
 // themselves (transposed through the warps) are only formed in the first two
 // tiles, in every eighth one and after a change.
 //
-// Work.  The units are (sequence, row tile, 128 keys) in that order; each CTA,
-// one per SM, takes an equal contiguous share, however long the sequences are.
+// Work.  Each CTA, one per SM, takes an equal contiguous share of the steps of all row
+// tiles in order, however long the sequences are: a step for every 128 keys and four
+// for a row tile's beginning, whose queries, pipeline fill and result take about as
+// long (64 sequences of up to 4500 with 128 heads: 127 us with equal numbers of key
+// tiles, 108 us with four steps, 110 us with six; 256 of up to 500: 144 and 101 us).
 // What a CTA's share cuts out of a row tile's keys goes to the workspace as
 // (O, mu, l), and decode_join_kernel adds the parts in order.
 #include <cuda.h>
@@ -76,6 +79,9 @@ constexpr float kDepth = 60.f;                // mu stays within 2^60 of the lar
 // The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
 // 1e27 neither end leaves fp32.
 constexpr float kSumShift = 30.f;
+// Steps that beginning a row tile counts for: its queries, pipeline fill and result take as
+// long as about four key tiles.
+constexpr uint32_t kStartSteps = 4;
 constexpr float kUnit = 0x1p-37f;             // 2^-(kShift + kSumShift): out = O / l in these units
 
 // Part of a row tile's result: slot 2 c of CTA c for one that continues an
@@ -169,11 +175,12 @@ __device__ __forceinline__ Seq sequence(const DecodeParams& p, const RawSeq& r) 
   return s;
 }
 
-// What is left of a CTA's share: `left` units from key tile kt of row tile rt of
-// sequence b, whose lengths have been read ahead.
+// What is left of a CTA's share: `left` steps from step `at` of row tile rt of
+// sequence b, whose lengths have been read ahead.  A row tile's steps are
+// kStartSteps that stand for what beginning it costs, then one for each key tile.
 struct Share {
   unsigned long long left;
-  uint32_t b, rt, kt;
+  uint32_t b, rt, at;
   RawSeq raw;
 };
 struct Segment {
@@ -191,17 +198,20 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, S
     g.s = s;
     g.b = sh.b;
     g.rt = sh.rt;
-    g.kt0 = sh.kt;
-    g.kt1 = static_cast<uint32_t>(min(static_cast<unsigned long long>(s.key_tiles), sh.kt + sh.left));
-    sh.left -= g.kt1 - g.kt0;
-    sh.kt = g.kt1;
-    if (g.kt1 == s.key_tiles) {
-      sh.kt = 0;
+    const uint32_t steps = kStartSteps + s.key_tiles;
+    const uint32_t end = static_cast<uint32_t>(min(static_cast<unsigned long long>(steps), sh.at + sh.left));
+    g.kt0 = max(sh.at, kStartSteps) - kStartSteps;
+    g.kt1 = max(end, kStartSteps) - kStartSteps;
+    sh.left -= end - sh.at;
+    sh.at = end;
+    if (end == steps) {
+      sh.at = 0;
       if (++sh.rt == s.row_tiles) {
         sh.rt = 0;
         sh.raw = load_raw(p, ++sh.b);
       }
     }
+    if (g.kt0 == g.kt1) continue;   // the share ends before the row tile's first key tile
     return true;
   }
   return false;
@@ -525,7 +535,7 @@ __device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& first
 }
 
 template <int NR>
-__device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, unsigned long long units, uint32_t ctas,
+__device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
   using R = Rows<NR>;
   constexpr int N = R::kCols;
@@ -812,8 +822,8 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     PartHeader h = {head_valid, part_b, part_rt, 0u};
     if (head_valid) {
       // The CTA that holds the row tile's last key tile.
-      const unsigned long long last = units * (blockIdx.x + 1) / ctas + part_rest - 1;
-      h.last_cta = static_cast<uint32_t>(((last + 1) * ctas - 1) / units);
+      const unsigned long long last = steps * (blockIdx.x + 1) / ctas + part_rest - 1;
+      h.last_cta = static_cast<uint32_t>(((last + 1) * ctas - 1) / steps);
     }
     p.headers[blockIdx.x] = h;
   }
@@ -858,15 +868,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
     tmem_alloc(smem_u32(&s.tmem_base), 512);
     tmem_relinquish();
   }
-  // ---- this CTA's share: prefix sums of the sequences' units
+  // ---- this CTA's share: prefix sums of the sequences' steps
   const uint32_t per = (p.B + kDecThreads - 1) / kDecThreads;
   const uint32_t b0 = min(p.B, threadIdx.x * per), b1 = min(p.B, b0 + per);
+  auto steps_of = [](const Seq& q) {
+    return q.key_tiles ? static_cast<unsigned long long>(q.row_tiles) * (kStartSteps + q.key_tiles) : 0ull;
+  };
   unsigned long long mine = 0;
   uint32_t bad = 0;
   for (uint32_t b = b0; b < b1; ++b) {
     const RawSeq raw = load_raw(p, b);
     const Seq q = sequence<NR>(p, raw);
-    mine += static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
+    mine += steps_of(q);
     if (raw.hi < raw.lo || raw.hi > p.Tq) bad |= MLA_DEVICE_STATUS_BAD_OFFSETS;
     if (q.rows && q.keys < static_cast<uint64_t>(raw.prior) + (raw.hi - raw.lo)) bad |= MLA_DEVICE_STATUS_BAD_COLUMN;
   }
@@ -882,26 +895,29 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  unsigned long long before = 0, units = 0;
+  unsigned long long before = 0, steps = 0;
   for (int w = 0; w < kDecThreads / 32; ++w) {
     if (w < warp) before += pro.warp_sum[w];
-    units += pro.warp_sum[w];
+    steps += pro.warp_sum[w];
   }
-  // CTAs with a share: all, or the first of them when there are fewer units.
-  const uint32_t ctas = static_cast<uint32_t>(min(static_cast<unsigned long long>(gridDim.x), units));
-  const unsigned long long u0 = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
-  const unsigned long long u1 = blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
+  // CTAs with a share: all, or the first of them when there are fewer steps.  A
+  // share of nothing but start steps stays idle: no row tile's key tiles lie on both
+  // sides of it.
+  const uint32_t ctas = static_cast<uint32_t>(min(static_cast<unsigned long long>(gridDim.x), steps));
+  const unsigned long long u0 = blockIdx.x < ctas ? steps * blockIdx.x / ctas : 0;
+  const unsigned long long u1 = blockIdx.x < ctas ? steps * (blockIdx.x + 1) / ctas : 0;
   unsigned long long start = before + incl - mine;
   if (u0 < u1 && start <= u0 && u0 < start + mine) {
     for (uint32_t b = b0; b < b1; ++b) {
       const RawSeq raw = load_raw(p, b);
       const Seq q = sequence<NR>(p, raw);
-      const unsigned long long here = static_cast<unsigned long long>(q.row_tiles) * q.key_tiles;
+      const uint32_t each = kStartSteps + q.key_tiles;
+      const unsigned long long here = steps_of(q);
       if (u0 < start + here) {
         pro.start.left = u1 - u0;
         pro.start.b = b;
-        pro.start.rt = static_cast<uint32_t>((u0 - start) / q.key_tiles);
-        pro.start.kt = static_cast<uint32_t>((u0 - start) % q.key_tiles);
+        pro.start.rt = static_cast<uint32_t>((u0 - start) / each);
+        pro.start.at = static_cast<uint32_t>((u0 - start) % each);
         pro.start.raw = raw;
         break;
       }
@@ -923,7 +939,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");  // 128 x 64 + 512 x 104 = 640 x 96
-    decode_softmax<NR>(s, p, sh, units, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+    decode_softmax<NR>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   }
   tc_fence_before();
   __syncthreads();

@@ -370,6 +370,16 @@ def test_decode(lib, n, prior, heads, P, mask):
     _check_decode(d, out, lse, mask)
 
 
+@pytest.mark.parametrize("n,prior,heads", [
+    ([1] * 170, [0, 200, 20, 127, 128] * 34, 128), ([1] * 151, [0] * 151, 16), ([1, 0, 1] * 100, [130, 9, 300] * 100, 8),
+    ([1] * 31, [0] * 31, 64), ([1] * 30 + [2], [0] * 30 + [4000], 64), ([1] * 77, list(range(100, 870, 10)), 65)])
+def test_decode_shares_that_end_anywhere(lib, n, prior, heads):
+    """Row tiles of one to a few key tiles, so that the SMs' shares end before, behind and inside them."""
+    d = Decode(n, prior, heads, 16, seed=sum(prior) + heads)
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
 @pytest.mark.parametrize("q_std,spread,sink", [(0.0, 0.5, 0.0), (4.0, 0.5, 0.0), (12.0, 3.0, 0.0), (1.0, 6.0, 0.0),
                                                (1.5, 0.5, 3.0), (1e-20, 0.5, 0.0), (60.0, 0.1, 0.0)])
 def test_decode_value_ranges(lib, q_std, spread, sink):
