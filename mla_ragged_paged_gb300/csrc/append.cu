@@ -151,6 +151,8 @@ extern "C" mla_status_t mla_append_latent(const mla_tensor_t* cache, const mla_t
   if ((st = check_tensor(rows, "rows", 2, MLA_DTYPE_BF16, true)) != MLA_OK) return st;
   if ((st = check_tensor(page_table, "page_table", 2, MLA_DTYPE_U32)) != MLA_OK) return st;
   if (!row_offsets || !cache_lens) return fail(MLA_ERR_INVALID_ARG, "row_offsets / cache_lens is NULL");
+  if (!aligned4(page_table->data) || !aligned4(row_offsets) || !aligned4(cache_lens) || !aligned4(status))
+    return fail(MLA_ERR_INVALID_ARG, "page_table, row_offsets, cache_lens and status must be 4-byte aligned");
   if (!cache->scale || cache->scale_gran != MLA_SCALE_PER_TOKEN)
     return fail(MLA_ERR_INVALID_ARG, "cache needs per-token scales (MLA_SCALE_PER_TOKEN)");
   const int64_t NP = cache->shape[0], P = cache->shape[1], W = cache->shape[2];

@@ -1090,6 +1090,8 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   if ((st = check_tensor(cache, "cache", 3, MLA_DTYPE_FP8_E4M3)) != MLA_OK) return st;
   if ((st = check_tensor(page_table, "page_table", 2, MLA_DTYPE_U32)) != MLA_OK) return st;
   if (!row_offsets || !cache_lens) return fail(MLA_ERR_INVALID_ARG, "row_offsets / cache_lens is NULL");
+  if (!aligned4(page_table->data) || !aligned4(row_offsets) || !aligned4(cache_lens) || !aligned4(status))
+    return fail(MLA_ERR_INVALID_ARG, "page_table, row_offsets, cache_lens and status must be 4-byte aligned");
   const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
   const int64_t NP = cache->shape[0], P = cache->shape[1];
   if (q->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "q must be [Tq, H, %d]", kWidth);
@@ -1098,6 +1100,7 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   if (cache->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "cache must be [num_pages, P, %d]", kWidth);
   if (!cache->scale || (cache->scale_gran != MLA_SCALE_PER_TOKEN && cache->scale_gran != MLA_SCALE_PER_TENSOR))
     return fail(MLA_ERR_INVALID_ARG, "cache needs per-token or per-tensor scales");
+  if (!aligned4(cache->scale)) return fail(MLA_ERR_INVALID_ARG, "cache scales must be 4-byte aligned");
   if (Tq * H > 0x7FFFFFFFll) return fail(MLA_ERR_INVALID_ARG, "q exceeds 2^31 rows");
   if (H < 1 || H > 1024) return fail(MLA_ERR_INVALID_ARG, "heads must be 1..1024");
   if (B < 1 || B > 16384 || page_table->shape[1] < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be 1..16384 with a page-table column");
@@ -1111,10 +1114,18 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
     return fail(MLA_ERR_INVALID_ARG, "q must start 16-byte aligned with 16-byte-multiple strides");
   if (!aligned16(out->data) || (out->stride[0] * 2) % 16 != 0 || (out->stride[1] * 2) % 16 != 0)
     return fail(MLA_ERR_INVALID_ARG, "out must start 16-byte aligned with 16-byte-multiple strides");
+  // Rows of an output that share memory would be written by several CTAs at once.
+  auto apart = [&](const mla_tensor_t* t, int64_t width) {
+    const __int128 tok = t->stride[0], head = t->stride[1];
+    return (Tq <= 1 || tok >= width) && (H <= 1 || head >= width) &&
+           (Tq <= 1 || H <= 1 || tok - width >= (H - 1) * head || head - width >= (Tq - 1) * tok);
+  };
+  if (!apart(out, kLatent)) return fail(MLA_ERR_INVALID_ARG, "out rows overlap");
   if (lse) {
     if ((st = check_tensor(lse, "lse", 2, MLA_DTYPE_F32, true)) != MLA_OK) return st;
     if (lse->shape[0] != Tq || lse->shape[1] != H) return fail(MLA_ERR_INVALID_ARG, "lse must be [Tq, H]");
-    if (reinterpret_cast<uintptr_t>(lse->data) & 3u) return fail(MLA_ERR_INVALID_ARG, "lse data must be 4-byte aligned");
+    if (!aligned4(lse->data)) return fail(MLA_ERR_INVALID_ARG, "lse data must be 4-byte aligned");
+    if (!apart(lse, 1)) return fail(MLA_ERR_INVALID_ARG, "lse rows overlap");
   }
   if (!(scale >= 0.f) || std::isinf(scale)) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (mask != MLA_MASK_CAUSAL && mask != MLA_MASK_NULL) return fail(MLA_ERR_INVALID_ARG, "unknown mask %d", (int)mask);

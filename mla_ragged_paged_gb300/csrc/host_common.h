@@ -26,6 +26,7 @@ mla_status_t encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t 
                           const uint32_t* box, CUtensorMapSwizzle swizzle, const char* what);
 
 bool aligned16(const void* ptr);
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Descriptor checks: non-NULL data, rank, dtype, shapes in [0, 2^31),
 // non-negative strides, innermost stride 1.  empty_ok: a tensor without

@@ -646,6 +646,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   if (M > 1 && out->stride[0] < N) return fail(MLA_ERR_INVALID_ARG, "out rows overlap");
   if (reinterpret_cast<uintptr_t>(out->data) % (out->dtype == MLA_DTYPE_F32 ? 4 : 2))
     return fail(MLA_ERR_INVALID_ARG, "out data is not aligned to its type");
+  if (!aligned4(status)) return fail(MLA_ERR_INVALID_ARG, "status must be 4-byte aligned");
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   if (M == 0) return MLA_OK;

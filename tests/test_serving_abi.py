@@ -139,6 +139,40 @@ def test_decode_refuses(lib, change):
     assert lib.mla_last_error_string()
 
 
+@pytest.mark.parametrize("change", [
+    dict(ro=0x20002), dict(cl=0x30001), dict(status=0x60002), dict(pt=_desc([2, 4], U32, ptr=0x10002)),
+    dict(cache=_cache(scale=0x50001)),
+    dict(out=_desc([6, 4, 512], stride=[2048, 0, 1])), dict(out=_desc([6, 4, 512], stride=[0, 512, 1])),
+    dict(out=_desc([6, 4, 512], stride=[1024, 512, 1])), dict(out=_desc([6, 4, 512], stride=[512, 2560, 1])),
+    dict(lse=_desc([6, 4], F32, stride=[0, 1])), dict(lse=_desc([6, 4], F32, stride=[3, 1])),
+])
+def test_decode_refuses_stray_addresses_and_shared_rows(lib, change):
+    a = dict(dict(out=_desc([6, 4, 512]), lse=_desc([6, 4], F32), cache=_cache(), pt=_desc([2, 4], U32), ro=0x20000,
+                  cl=0x30000, status=0x60000), **change)
+    assert lib.mla_decode_latent(_ref(a["out"]), _ref(a["lse"]), _ref(_desc([6, 4, 576])), _ref(a["cache"]), _ref(a["pt"]),
+                                 a["ro"], a["cl"], 0.07, 0, a["status"], 0x40000, binding.decode_workspace_size(),
+                                 None) == binding.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("shape,stride", [([6, 4, 512], [512, 3200, 1]), ([1, 4, 512], [0, 512, 1]),
+                                          ([6, 1, 512], [512, 0, 1]), ([6, 4, 512], [1 << 45, 1 << 40, 1])])
+def test_decode_takes_rows_in_any_order(lib, shape, stride):
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    assert _decode(lib, out=_desc(shape, stride=stride), q=_desc([shape[0], shape[1], 576]),
+                   lse=None) in (binding.MLA_ERR_UNSUPPORTED, binding.MLA_ERR_CUDA)
+
+
+def test_append_and_matmul_refuse_stray_addresses(lib):
+    for change in (dict(ro=0x20002), dict(cl=0x30001), dict(pt=_desc([2, 4], U32, ptr=0x10002))):
+        assert _append(lib, **change) == binding.MLA_ERR_INVALID_ARG
+    assert lib.mla_append_latent(_ref(_cache()), _ref(_desc([6, 576])), _ref(_desc([2, 4], U32)), 0x20000, 0x30000,
+                                 0x60002, None) == binding.MLA_ERR_INVALID_ARG
+    assert lib.mla_matmul_fp8(_ref(_desc([5, 300])), _ref(_desc([5, 272], F8)), _ref(_desc([5, 3], F32)),
+                              _ref(_desc([300, 272], F8)), _ref(_desc([3, 3], F32)), 0x60002,
+                              None) == binding.MLA_ERR_INVALID_ARG
+
+
 def test_good_arguments_reach_the_device_check(lib):
     if torch.cuda.is_available():
         pytest.skip("would launch on made-up addresses")
