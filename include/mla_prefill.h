@@ -640,7 +640,7 @@ size_t mla_decode_latent_workspace_size(void);
  *                stride = P x token stride), token stride a multiple of 16
  *                bytes; positive scales, per token ([num_pages * P] floats) or
  *                one for all.  Pages of a multiple of 8 tokens are read in boxes,
- *                others row by row (about two thirds slower)
+ *                others row by row (up to twice as slow)
  *   page_table   device uint32 [B, max_pages], B <= 16384
  *   row_offsets, cache_lens, scale, mask  as in mla_prefill_ragged
  *   status       device uint32 or NULL: an out-of-range page id or page-table

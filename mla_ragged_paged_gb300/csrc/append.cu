@@ -7,9 +7,8 @@
 // 2 W bytes read, W + 4 written per token.  One warp per row, the row in registers
 // between its maximum and its codes; the row's sequence is found by a 32-way search
 // (one load per lane and step: two dependent reads for up to 1024 sequences instead
-// of ten).  32768 rows of 576 (16 sequences): 15.7 us = 3.6 TB/s; bound by the chain
-// of search, length, page and maximum that each short-lived warp walks, and by the
-// instructions of the quotients (13.4 us with single products in their place).  Warps
+// of ten).  38438 rows of 576 (16 sequences): 15.9 us = 4.2 TB/s; bound by instruction
+// issue (72 % of the slots; 13.4 us with single products in place of the quotients).  Warps
 // that walk several rows and keep sequence and page hold twice the registers and
 // measured slower (21.5 against 20.5 us before the quotients were shortened).
 #include <cuda_runtime.h>
@@ -56,7 +55,7 @@ __device__ __forceinline__ uint32_t find_sequence(const uint32_t* ro, uint32_t B
 
 // The codes of eight bf16 numbers x divided by scale = fl(amax / 448), as if each
 // quotient were first rounded to fp32 (as a plain program rounds it).  A correctly
-// rounded division for each number would be most of the kernel's work (32768 rows of
+// rounded division for each number would be most of the kernel's work (38438 rows of
 // 576: 21.1 us, without any 13.4 us), so the product with `to` = fl(1 / scale) is
 // corrected once by its remainder, which an fma gives exactly (Markstein, IBM J. Res.
 // Dev. 34, 1990): that is the rounded x / scale (1 + d), |d| < 2^-46.  Its code can

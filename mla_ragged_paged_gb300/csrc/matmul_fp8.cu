@@ -12,11 +12,12 @@
 // * matmul_tile_kernel, for products with many output tiles: persistent CTA
 //   pairs, each CTA one 128 x 256 output tile; the pair shares its weight tile by
 //   TMA multicast, because one SM's share of the L2 cannot feed 48 KB per 512
-//   tensor-core cycles.  Measured 8192^3 in 434 us = 2530 TFLOP/s; of that the
-//   loads alone take 350 us and reading back 128 KB of tensor memory per block
-//   beside 32 768 products in fp32 most of the rest (bound by the two warps per
-//   scheduler that wait for tensor memory and multiply in turn).
-// * matmul_thin_kernel, for few tokens: bound by HBM (w), 5.2 TB/s at
+//   tensor-core cycles.  Measured 8192^3 in 434 us = 2530 TFLOP/s;
+//   without the sums in fp32 333 us, without the UMMAs as well 278 us.  What bounds it
+//   is how far the 32 768 fp32 products a block hide behind the tensor cores; more
+//   warps for them, scales read earlier and UMMAs over the CTA pair measured slower
+//   (450 .. 527 us).
+// * matmul_thin_kernel, for few tokens: bound by HBM (w), 4.8 TB/s at
 //   64 x 8192 x 16384 (28 us).  The weights are the 128-row operand and the tokens the
 //   narrow one, so few rows waste no tensor time, and K is split over a cluster of
 //   up to eight CTAs whose partial sums meet in distributed shared memory, in rank
