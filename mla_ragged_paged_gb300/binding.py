@@ -492,7 +492,7 @@ def merge(out, partial_out, partial_lse, row_offsets, buffer_row_offsets, stream
 # their marshalling is kept short: descriptors are packed as bytes in the layout
 # of MlaTensor (whose size the tests compare), devices and streams are read as
 # plain integers.
-_LAYOUT = {n: struct.Struct(f"=Qii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}xQi4x") for n in range(1, 5)}
+_LAYOUT = {n: struct.Struct(f"=Qii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}xQi4x").pack for n in range(1, 5)}
 
 
 def _pack(t, dtype, scale=0, scale_gran=MLA_SCALE_NONE):
@@ -503,7 +503,7 @@ def _pack(t, dtype, scale=0, scale_gran=MLA_SCALE_NONE):
     n = len(shape)
     if not 1 <= n <= 4:
         raise MlaError(MLA_ERR_INVALID_ARG, f"tensors have 1 to 4 dimensions (got {tuple(shape)})")
-    return _LAYOUT[n].pack(t.data_ptr(), dtype, n, *shape, *t.stride(), scale, scale_gran)
+    return _LAYOUT[n](t.data_ptr(), dtype, n, *shape, *t.stride(), scale, scale_gran)
 
 
 def _address(t):
@@ -520,13 +520,34 @@ def _typed(t, what, *dtypes):
         raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
 
 
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
 _INDEX = (torch.int32, torch.uint32)
 
 
+def _operand(t, what, dtypes, dtype):
+    """_typed, then _pack, in one call."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        _typed(t, what, *dtypes)
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        return _pack(t, dtype)
+    return _LAYOUT[n](t.data_ptr(), dtype, n, *shape, *t.stride(), 0, MLA_SCALE_NONE)
+
+
+def _bf16_or_f32(t):
+    return MLA_DTYPE_F32 if t.dtype is torch.float32 else MLA_DTYPE_BF16
+
+
 def _indices(t, what, numel):
     """The address of a packed device array of 32-bit indices."""
-    _typed(t, what, *_INDEX)
+    if t.dtype not in _INDEX:
+        _typed(t, what, *_INDEX)
     if t.numel() != numel or not t.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, f"{what} must hold {numel} packed elements (got {tuple(t.shape)})")
     return t.data_ptr()
@@ -550,7 +571,7 @@ def _device_of(*tensors):
             _on_device(t)
         if dev < 0:
             dev = at
-            if dev != torch.cuda.current_device():
+            if dev != torch._C._cuda_getDevice():   # (a CUDA tensor exists: no lazy start)
                 raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on the current device (got {t.device})")
         elif at != dev:
             raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on one device (got cuda:{dev} and {t.device})")
@@ -563,18 +584,14 @@ def rms_norm(x, weight, eps, residual=None, residual_out=None, out=None, out_fp8
     sqrt(mean(h^2) + eps) as bf16 `out` and / or e4m3 `out_fp8` with one scale
     per 128 columns of a row in `out_scales`.  Returns the outputs given."""
     dev = _device_of(x, weight, residual, residual_out, out, out_fp8, out_scales)
-    bf16 = torch.bfloat16
-    _typed(x, "x", bf16)
-    _typed(residual, "residual", bf16)
-    _typed(residual_out, "residual_out", bf16)
-    _typed(out, "out", bf16)
-    _typed(weight, "weight", bf16, torch.float32)
-    _typed(out_fp8, "out_fp8", *_FP8)
-    _typed(out_scales, "out_scales", torch.float32)
-    _check(load().mla_rms_norm(_pack(out, MLA_DTYPE_BF16), _pack(out_fp8, MLA_DTYPE_FP8_E4M3),
-                               _pack(out_scales, MLA_DTYPE_F32), _pack(x, MLA_DTYPE_BF16),
-                               _pack(residual, MLA_DTYPE_BF16), _pack(residual_out, MLA_DTYPE_BF16),
-                               _pack(weight, _dtype_code(weight)), eps, _raw_stream(stream, dev)))
+    _check(load().mla_rms_norm(_operand(out, "out", _BF16, MLA_DTYPE_BF16),
+                               _operand(out_fp8, "out_fp8", _FP8, MLA_DTYPE_FP8_E4M3),
+                               _operand(out_scales, "out_scales", _F32, MLA_DTYPE_F32),
+                               _operand(x, "x", _BF16, MLA_DTYPE_BF16),
+                               _operand(residual, "residual", _BF16, MLA_DTYPE_BF16),
+                               _operand(residual_out, "residual_out", _BF16, MLA_DTYPE_BF16),
+                               _operand(weight, "weight", _BF16_F32, _bf16_or_f32(weight)), eps,
+                               _raw_stream(stream, dev)))
     return tuple(t for t in (out, out_fp8, out_scales, residual_out) if t is not None)
 
 
@@ -583,14 +600,12 @@ def matmul_fp8(out, x, x_scales, w, w_scales, status=None, stream=None):
     e4m3 with a scale per row and 128 columns of x ([M, ceil(K / 128)]; an
     expanded column is one scale a row) and per 128 x 128 block of w."""
     dev = _device_of(out, x, x_scales, w, w_scales, status)
-    _typed(out, "out", torch.bfloat16, torch.float32)
-    _typed(x, "x", *_FP8)
-    _typed(w, "w", *_FP8)
-    _typed(x_scales, "x_scales", torch.float32)
-    _typed(w_scales, "w_scales", torch.float32)
-    _check(load().mla_matmul_fp8(_pack(out, _dtype_code(out)), _pack(x, MLA_DTYPE_FP8_E4M3),
-                                 _pack(x_scales, MLA_DTYPE_F32), _pack(w, MLA_DTYPE_FP8_E4M3),
-                                 _pack(w_scales, MLA_DTYPE_F32), _status_word(status), _raw_stream(stream, dev)))
+    _check(load().mla_matmul_fp8(_operand(out, "out", _BF16_F32, _bf16_or_f32(out)),
+                                 _operand(x, "x", _FP8, MLA_DTYPE_FP8_E4M3),
+                                 _operand(x_scales, "x_scales", _F32, MLA_DTYPE_F32),
+                                 _operand(w, "w", _FP8, MLA_DTYPE_FP8_E4M3),
+                                 _operand(w_scales, "w_scales", _F32, MLA_DTYPE_F32), _status_word(status),
+                                 _raw_stream(stream, dev)))
     return out
 
 
@@ -614,11 +629,10 @@ def append_latent(cache, cache_scales, rows, page_table, row_offsets, cache_lens
     e4m3 cache [num_pages, P, W] and its scales [num_pages, P], at context
     positions cache_lens[b] + i."""
     dev = _device_of(cache, cache_scales, rows, page_table, row_offsets, cache_lens, status)
-    _typed(rows, "rows", torch.bfloat16)
-    _typed(page_table, "page_table", *_INDEX)
     B = page_table.shape[0]
-    _check(load().mla_append_latent(_latent_cache(cache, cache_scales, False), _pack(rows, MLA_DTYPE_BF16),
-                                    _pack(page_table, MLA_DTYPE_U32), _indices(row_offsets, "row_offsets", B + 1),
+    _check(load().mla_append_latent(_latent_cache(cache, cache_scales, False),
+                                    _operand(rows, "rows", _BF16, MLA_DTYPE_BF16),
+                                    _operand(page_table, "page_table", _INDEX, MLA_DTYPE_U32), _indices(row_offsets, "row_offsets", B + 1),
                                     _indices(cache_lens, "cache_lens", B), _status_word(status),
                                     _raw_stream(stream, dev)))
     return cache, cache_scales
@@ -640,10 +654,6 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
     scales ([num_pages, P], or one float); out [Tq, H, 512] stays in the latent
     space, lse [Tq, H] is optional."""
     dev = _device_of(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, workspace, lse, status)
-    _typed(out, "out", torch.bfloat16)
-    _typed(q, "q", torch.bfloat16)
-    _typed(lse, "lse", torch.float32)
-    _typed(page_table, "page_table", *_INDEX)
     if workspace is None:
         # From the launch stream's pool: its memory is not reused before the call is done.
         with torch.cuda.stream(stream):
@@ -651,8 +661,9 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
     elif not workspace.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
     B = page_table.shape[0]
-    _check(load().mla_decode_latent(_pack(out, MLA_DTYPE_BF16), _pack(lse, MLA_DTYPE_F32), _pack(q, MLA_DTYPE_BF16),
-                                    _latent_cache(cache, cache_scales, True), _pack(page_table, MLA_DTYPE_U32),
+    _check(load().mla_decode_latent(_operand(out, "out", _BF16, MLA_DTYPE_BF16), _operand(lse, "lse", _F32, MLA_DTYPE_F32),
+                                    _operand(q, "q", _BF16, MLA_DTYPE_BF16), _latent_cache(cache, cache_scales, True),
+                                    _operand(page_table, "page_table", _INDEX, MLA_DTYPE_U32),
                                     _indices(row_offsets, "row_offsets", B + 1),
                                     _indices(cache_lens, "cache_lens", B), scale, int(mask), _status_word(status),
                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
