@@ -18,7 +18,7 @@
 // lane's eight.  Rows of up to 1024 columns take one warp each, eight to a block
 // (no barrier); wider rows, and few rows of more than 256 columns, a block each, which
 // walks the rows and, where the registers allow, reads the next one while it finishes
-// the current one.  Measured, residual and codes: 16384 x 8192 in 165 us = 5.7 TB/s,
+// the current one.  Measured, residual and codes: 16384 x 8192 in 160 us = 5.9 TB/s,
 // 100000 x 1024 in 116 us = 6.2 TB/s (HBM); 1 x 8192 in 3.0 us (launch).
 #include <cuda_runtime.h>
 
@@ -62,10 +62,23 @@ __device__ __forceinline__ void widen(float (&v)[8], uint4 u) {
 }
 
 // CH: chunks of 8 columns per thread.  THREADS 32: a row per warp, blockDim.y rows
-// a block; otherwise a row per block of at most THREADS threads at a time.
+// a block; otherwise a row per block of at most THREADS threads at a time.  A row's
+// loads, two reductions and stores follow one another, so an SM needs two rows at
+// once.  One chunk a thread and up to 512 threads leave room for that at 64 registers,
+// weights and the next row's inputs included; wider rows are held by their launch
+// bounds to what lets two blocks in: they read the weights anew for every row (they
+// stay in L1) and, but for one form, no row ahead.  (16384 rows, us with one block an
+// SM / two: 4608 columns 124 / 92, 6144 138 / 129, 8192 164 / 160, 10240 262 / 193,
+// 12288 286 / 220, 16384 338 / 295, 20480 533 / 383.)  From 24577 columns on a second
+// block has no registers left.
+__host__ __device__ constexpr bool two_blocks(int ch, int threads) {
+  return threads != 32 && threads <= 768 && (ch > 1 || threads > 512);
+}
 template <int CH, int THREADS, bool VEC>
-__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS) norm_kernel(const NormParams p) {
-  constexpr bool kWarp = THREADS == 32, kAhead = !kWarp && CH == 1;
+__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, two_blocks(CH, THREADS) ? 2 : 0)
+    norm_kernel(const NormParams p) {
+  constexpr bool kWarp = THREADS == 32, kAhead = !kWarp && CH == 1 && THREADS <= 640;
+  constexpr bool kHeld = !two_blocks(CH, THREADS);   // weights in registers
   __shared__ float part[2][32];
   const uint32_t t = threadIdx.x, threads = blockDim.x, lane = t & 31u;
   long long row = kWarp ? static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y : blockIdx.x;
@@ -107,7 +120,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS) norm_kernel(con
     }
   };
   fetch(row);
-  if (!p.w_f32) {
+  if (kHeld && !p.w_f32) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) rw[c] = load(static_cast<const uint16_t*>(p.w), c);
   }
@@ -145,6 +158,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS) norm_kernel(con
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = col_of(c, e) < p.dim ? __ldg(static_cast<const float*>(p.w) + col_of(c, e)) : 0.f;
       } else {
+        if (!kHeld) rw[c] = load(static_cast<const uint16_t*>(p.w), c);
         widen(w, rw[c]);
       }
 #pragma unroll
@@ -205,14 +219,26 @@ void launch_norm(const NormParams& p, int sms, cudaStream_t s) {
     else norm_kernel<4, 32, VEC><<<grid, block, 0, s>>>(p);
     return;
   }
-  const uint32_t ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const uint32_t ch = chunks <= 768 ? 1 : chunks <= 1536 ? 2 : 4;
   const uint32_t threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-  // As many blocks as fit (2048 threads an SM), each walking the rows.
-  const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(sms) * (2048u / threads)));
-  if (threads <= 512 && ch == 1) norm_kernel<1, 512, VEC><<<grid, threads, 0, s>>>(p);
-  else if (ch == 1) norm_kernel<1, 1024, VEC><<<grid, threads, 0, s>>>(p);
-  else if (ch == 2) norm_kernel<2, 1024, VEC><<<grid, threads, 0, s>>>(p);
-  else norm_kernel<4, 1024, VEC><<<grid, threads, 0, s>>>(p);
+  // The blocks that fit, each walking the rows.
+  const uint32_t per_sm = threads > 768 ? 1u : threads > 512 ? 2u : 1024u / threads;
+  const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(sms) * per_sm));
+  auto launch = [&](auto kernel) { kernel<<<grid, threads, 0, s>>>(p); };
+  if (ch == 1) {
+    if (threads <= 512) launch(norm_kernel<1, 512, VEC>);
+    else if (threads <= 640) launch(norm_kernel<1, 640, VEC>);
+    else launch(norm_kernel<1, 768, VEC>);
+  } else if (ch == 2) {
+    if (threads <= 512) launch(norm_kernel<2, 512, VEC>);
+    else if (threads <= 640) launch(norm_kernel<2, 640, VEC>);
+    else launch(norm_kernel<2, 768, VEC>);
+  } else {
+    if (threads <= 512) launch(norm_kernel<4, 512, VEC>);
+    else if (threads <= 640) launch(norm_kernel<4, 640, VEC>);
+    else if (threads <= 768) launch(norm_kernel<4, 768, VEC>);
+    else launch(norm_kernel<4, 1024, VEC>);
+  }
 }
 
 mla_status_t check_rows(const mla_tensor_t* t, const char* name, mla_dtype_t dt, int64_t rows, int64_t dim,

@@ -85,6 +85,18 @@ def test_norm(lib, rows, dim):
     _check_norm(x, None, w, 1e-6, None, only, scales, None)
 
 
+@pytest.mark.parametrize("dim", [600, 2100, 4600, 5100, 6100, 7001, 9000, 9999, 12000, 14000, 18001, 24000, 26000])
+def test_norm_blocks_that_walk_several_rows(lib, dim):
+    from mla_ragged_paged_gb300 import binding
+    rows = 900 if dim < 4000 else 330
+    x, r, w = _norm_case(rows, dim, dim)
+    out, res_out = torch.empty_like(r), torch.empty_like(r)
+    codes = torch.empty(rows, dim, dtype=E4M3, device="cuda")
+    scales = torch.empty(rows, -(-dim // 128), device="cuda")
+    binding.rms_norm(x, w, 1e-6, residual=r, residual_out=res_out, out=out, out_fp8=codes, out_scales=scales)
+    _check_norm(x, r, w, 1e-6, out, codes, scales, res_out)
+
+
 @pytest.mark.parametrize("rows,dim,stride,offset,w_dtype", [
     (50, 512, 576, 0, torch.bfloat16), (7, 512, 513, 1, torch.float32), (6, 1100, 1112, 8, torch.float32),
     (5, 2049, 2050, 3, torch.bfloat16), (4, 640, 0, 0, torch.bfloat16)])
