@@ -37,8 +37,8 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
 // Allow `bytes` of dynamic shared memory for `func` on `device`, cached per
 // (device, slot): each kernel needs a slot of its own (0 plan, 1 scheduler,
 // 2 / 3 / 4 attention bf16 / fp8 / fp8 with per-token K scales, 6 / 7 the last
-// two with two-term precision, 5 up-projection, 8 fp8 product, 9 .. 11 its form
-// for few tokens, 13 / 14 latent decode).
+// two with two-term precision, 5 up-projection, 8 / 12 fp8 product, 9 .. 11 its
+// form for few tokens, 13 / 14 latent decode).
 constexpr int kSmemSlots = 16;
 mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int slot);
 

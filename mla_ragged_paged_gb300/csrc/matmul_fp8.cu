@@ -17,6 +17,9 @@
 //   is how far the 32 768 fp32 products a block hide behind the tensor cores; more
 //   warps for them, scales read earlier and UMMAs over the CTA pair measured slower
 //   (450 .. 527 us).
+//   Where tiles are few and K is long, two or four pairs share a tile's K as one
+//   cluster and add their sums through distributed shared memory
+//   (2000 x 576 x 16384: 69 -> 42 us).
 // * matmul_thin_kernel, for few tokens: bound by HBM (w), 4.8 TB/s at
 //   64 x 8192 x 16384 (28 us).  The weights are the 128-row operand and the tokens the
 //   narrow one, so few rows waste no tensor time, and K is split over a cluster of
@@ -48,6 +51,7 @@ struct MatmulParams {
   uint32_t out_f32;
   uint32_t tma;                 // every output row starts 16-byte aligned
   uint32_t m_tiles, n_tiles;    // tile kernel: m_tiles counts pairs of 128 rows
+  uint32_t splits;              // tile kernel: CTA pairs that share a tile's K, a cluster
   uint32_t* status;
 };
 
@@ -76,6 +80,7 @@ struct __align__(1024) TileSmem {
   uint32_t abort_flag;
 };
 static_assert(sizeof(TileSmem) + 1024 <= 232448, "matmul tile shared memory");
+static_assert(sizeof(float) * kTileM * kTileN <= kStages * (kXBytes + kWBytes), "a tile's sums take the ring's place");
 
 // Tile t: bands of kBand row pairs, inside a band the row pairs of one column
 // tile follow each other.
@@ -87,16 +92,43 @@ __device__ __forceinline__ void tile_of(const MatmulParams& p, uint32_t t, uint3
   m = band * kBand + (r - n * rows);
 }
 
-__device__ void tile_producer(TileSmem& s, const MatmulParams& p, uint32_t rank, volatile uint32_t* abort) {
-  const uint32_t tiles = p.m_tiles * p.n_tiles;
+// A CTA's place: which tiles its cluster walks, which blocks of K its pair takes
+// (SPLIT: of the p.splits pairs of a cluster; else the cluster is one pair).
+template <bool SPLIT>
+struct TilePlace {
+  uint32_t rank, pair;          // in the pair, in the cluster
+  uint32_t first, step;         // tiles
+  uint32_t kb0, kb1;
+  __device__ __forceinline__ explicit TilePlace(const MatmulParams& p) {
+    const uint32_t r = cluster_rank();
+    rank = r & 1u;
+    if constexpr (SPLIT) {
+      pair = r >> 1;
+      first = blockIdx.x / (2 * p.splits);
+      step = gridDim.x / (2 * p.splits);
+      kb0 = p.kblocks * pair / p.splits;
+      kb1 = p.kblocks * (pair + 1) / p.splits;
+    } else {
+      pair = 0;
+      first = blockIdx.x >> 1;
+      step = gridDim.x >> 1;
+      kb0 = 0;
+      kb1 = p.kblocks;
+    }
+  }
+};
+
+template <bool SPLIT>
+__device__ void tile_producer(TileSmem& s, const MatmulParams& p, const TilePlace<SPLIT>& at, volatile uint32_t* abort) {
+  const uint32_t tiles = p.m_tiles * p.n_tiles, rank = at.rank;
   uint32_t pos = 0;
   bool alive = true;
-  for (uint32_t t = blockIdx.x >> 1; t < tiles && alive; t += gridDim.x >> 1) {
+  for (uint32_t t = at.first; t < tiles && alive; t += at.step) {
     uint32_t m, n;
     tile_of(p, t, m, n);
     const int32_t mr = static_cast<int32_t>((2 * m + rank) * kTileM);
     const int32_t nr = static_cast<int32_t>(n * kTileN + rank * (kTileN / 2));
-    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
+    for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
       const uint32_t st = pos % kStages;
       if (!(alive = mbar_wait(smem_u32(&s.empty[st]), ((pos / kStages) & 1u) ^ 1u, abort))) break;
       const uint32_t bar = smem_u32(&s.full[st]);
@@ -104,7 +136,8 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, uint32_t rank,
       const int32_t k = static_cast<int32_t>(kb * kKB);
       tma_load_2d(smem_u32(s.x[st]), &p.tm_x, bar, k, mr);
       // Half of the pair's weight tile, into both CTAs.
-      tma_load_2d_multicast(smem_u32(s.w[st]) + rank * (kWBytes / 2), &p.tm_w, bar, k, nr, 3);
+      tma_load_2d_multicast(smem_u32(s.w[st]) + rank * (kWBytes / 2), &p.tm_w, bar, k, nr,
+                            static_cast<uint16_t>(3u << (2 * at.pair)));
     }
   }
   // Both CTAs' UMMA threads have arrived on every slot before this CTA exits.
@@ -124,7 +157,8 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, uint32_t rank,
   }
 }
 
-__device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, volatile uint32_t* abort) {
+template <bool SPLIT>
+__device__ void tile_mma(TileSmem& s, const MatmulParams& p, const TilePlace<SPLIT>& at, uint32_t tmem, volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
   // e4m3, both K-major.  A block's two halves of 128 columns have accumulators
   // of their own, so that the first is added up while the second is computed.
@@ -132,8 +166,8 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, vola
   const uint64_t x_desc = sw128_desc_at(smem_u32(s.x[0])), w_desc = sw128_desc_at(smem_u32(s.w[0]));
   uint32_t pos = 0;
   bool alive = true;
-  for (uint32_t t = blockIdx.x >> 1; t < tiles && alive; t += gridDim.x >> 1) {
-    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
+  for (uint32_t t = at.first; t < tiles && alive; t += at.step) {
+    for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
       const uint32_t st = pos % kStages;
       if (!(alive = mbar_wait(smem_u32(&s.full[st]), (pos / kStages) & 1u, abort))) break;
       const uint64_t ad = x_desc + st * (kXBytes >> 4), bd = w_desc + st * (kWBytes >> 4);
@@ -148,7 +182,7 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, vola
         umma_commit(smem_u32(&s.acc_full[buf]));
       }
       if (!alive) break;
-      umma_commit_multicast(smem_u32(&s.empty[st]), 3);
+      umma_commit_multicast(smem_u32(&s.empty[st]), static_cast<uint16_t>(3u << (2 * at.pair)));
     }
   }
   // No UMMA may still be in flight when tensor memory is released.
@@ -163,24 +197,26 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, uint32_t tmem, vola
 // already on their way.  A lane reads one block of every fourth row, so that eight
 // lanes share a 32-byte sector: a thread per row would touch a line of its own
 // for each block (measured: 8192^3 in 690 us against 463 us without the reads).
-__device__ void tile_scales(TileSmem& s, const MatmulParams& p, uint32_t rank, uint32_t half, int lane, volatile uint32_t* abort) {
+template <bool SPLIT>
+__device__ void tile_scales(TileSmem& s, const MatmulParams& p, const TilePlace<SPLIT>& at, uint32_t half, int lane,
+                            volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
   const uint32_t block = lane & (kScaleBlocks - 1), sub = lane / kScaleBlocks;
   uint32_t pos = 0;
-  for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
+  for (uint32_t t = at.first; t < tiles; t += at.step) {
     uint32_t mt, nt;
     tile_of(p, t, mt, nt);
-    const uint32_t m = (2 * mt + rank) * kTileM + half * 64 + sub, n = nt * kTileN + half * (kTileN / 2);
+    const uint32_t m = (2 * mt + at.rank) * kTileM + half * 64 + sub, n = nt * kTileN + half * (kTileN / 2);
     const float* ws = p.ws + (n < p.N ? n >> 7 : 0u) * p.ws_row;
     float x[16] = {}, w = 0.f;
     auto fetch = [&](uint32_t kb) {
-      if (kb >= p.kblocks) return;
+      if (kb >= at.kb1) return;
       w = __ldg(ws + kb * p.ws_col);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = m + 4 * i < p.M ? __ldg(p.xs + (m + 4 * i) * p.xs_row + kb * p.xs_col) : 0.f;
     };
-    fetch(block);
-    for (uint32_t kb = 0; kb < p.kblocks; kb += kScaleBlocks, ++pos) {
+    fetch(at.kb0 + block);
+    for (uint32_t kb = at.kb0; kb < at.kb1; kb += kScaleBlocks, ++pos) {
       const uint32_t buf = pos & 1u;
       if (!mbar_wait(smem_u32(&s.scale_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort)) return;
 #pragma unroll
@@ -260,29 +296,42 @@ __device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* stage
   }
 }
 
-// One of two warpgroups: half of the tile's columns, a row per thread.
-__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tmem, uint32_t rank, uint32_t half, int quarter,
+// One of two warpgroups: half of the tile's columns, a row per thread.  Where pairs
+// share a tile's K (one tile a cluster then), each CTA leaves its sums in its shared
+// memory, in the ring's place, and takes a part of the rows (warps' quarters) to add
+// up in the order of the pairs and store.
+template <bool SPLIT>
+__device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePlace<SPLIT>& at, uint32_t tmem, uint32_t half, int quarter,
                                 int lane, volatile uint32_t* abort) {
   const uint32_t tiles = p.m_tiles * p.n_tiles;
   const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kAccCols;
   uint32_t pos = 0, chunk = 0;
-  for (uint32_t t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1) {
+  for (uint32_t t = at.first; t < tiles; t += at.step) {
     uint32_t mt, nt;
     tile_of(p, t, mt, nt);
-    const uint32_t m0 = (2 * mt + rank) * kTileM + quarter * 32, n0 = nt * kTileN + half * kAccCols;
+    const uint32_t m0 = (2 * mt + at.rank) * kTileM + quarter * 32, n0 = nt * kTileN + half * kAccCols;
     float acc[kAccCols];
 #pragma unroll
     for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
-    for (uint32_t kb = 0; kb < p.kblocks; ++kb, ++pos) {
-      const uint32_t buf = (pos & 1u) * 2 + half, at = kb % kScaleBlocks, cb = chunk & 1u;
-      if (at == 0 && !mbar_wait(smem_u32(&s.scale_full[cb]), (chunk >> 1) & 1u, abort)) return;
-      const float scale = s.x_scale[cb][at][quarter * 32 + lane] * s.w_scale[cb][half][at];
-      if (at == kScaleBlocks - 1 || kb + 1 == p.kblocks) {
+    bool alive = true;   // (SPLIT: all CTAs of the cluster meet below, whatever happens)
+    for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
+      const uint32_t buf = (pos & 1u) * 2 + half, in = (kb - at.kb0) % kScaleBlocks, cb = chunk & 1u;
+      if (in == 0 && !mbar_wait(smem_u32(&s.scale_full[cb]), (chunk >> 1) & 1u, abort)) {
+        if constexpr (!SPLIT) return;
+        alive = false;
+        break;
+      }
+      const float scale = s.x_scale[cb][in][quarter * 32 + lane] * s.w_scale[cb][half][in];
+      if (in == kScaleBlocks - 1 || kb + 1 == at.kb1) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[cb]));
         ++chunk;
       }
-      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) return;
+      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) {
+        if constexpr (!SPLIT) return;
+        alive = false;
+        break;
+      }
       tc_fence_after();
       const uint32_t col = taddr + (pos & 1u) * kTileN;
       uint32_t v[2][32];
@@ -302,16 +351,36 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, uint32_t tme
         for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(v[c & 1][e]), scale, acc[32 * c + e]);
       }
     }
+    if constexpr (SPLIT) {
+      // (The ring is idle: every copy into it has been multiplied.)
+      float* part = reinterpret_cast<float*>(s.x[0]) + (half * 4 + quarter) * (kAccCols * 32) + lane;
+      if (alive) {
+#pragma unroll
+        for (int e = 0; e < kAccCols; ++e) part[32 * e] = acc[e];
+      }
+      cluster_sync();
+      alive = alive && quarter * p.splits / 4 == at.pair;
+      if (alive) {
+#pragma unroll
+        for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
+        for (uint32_t i = 0; i < p.splits; ++i) {
+          const uint32_t from = map_shared(smem_u32(part), 2 * i + at.rank);
+#pragma unroll
+          for (int e = 0; e < kAccCols; ++e) acc[e] += ld_shared_cluster(from + 128 * e);
+        }
+      }
+      if (!alive) return;
+    }
     store_rows(p, s.stage[half * 4 + quarter], acc, m0, n0, lane);
   }
 }
 
-__global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
-    matmul_tile_kernel(const __grid_constant__ MatmulParams p) {
+template <bool SPLIT>
+__global__ void __launch_bounds__(kTileThreads, 1) matmul_tile_kernel(const __grid_constant__ MatmulParams p) {
   extern __shared__ uint8_t smem_raw[];
   TileSmem& s = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const TilePlace<SPLIT> at(p);
   volatile uint32_t* abort = &s.abort_flag;
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
@@ -342,13 +411,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t tmem = s.tmem_base;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0 && elect_one()) tile_producer(s, p, rank, abort);
-    if (warp == 1 && elect_one()) tile_mma(s, p, tmem, abort);
-    if (warp >= 2) tile_scales(s, p, rank, warp - 2, lane, abort);
+    if (warp == 0 && elect_one()) tile_producer(s, p, at, abort);
+    if (warp == 1 && elect_one()) tile_mma(s, p, at, tmem, abort);
+    if (warp >= 2) tile_scales(s, p, at, warp - 2, lane, abort);
     __syncwarp();
+    if constexpr (SPLIT) cluster_sync();   // with the one in tile_accumulate
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 128 x 88 + 256 x 208 = 384 x 168
-    tile_accumulate(s, p, tmem, rank, (warp - 4) >> 2, warp & 3, lane, abort);
+    tile_accumulate(s, p, at, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
     if (lane == 0) bulk_wait_group_all();   // the staging buffers outlive their stores
   }
   tc_fence_before();
@@ -567,6 +637,23 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
   if (threadIdx.x == 0 && s.abort_flag && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
 }
 
+template <typename Kernel, typename... Args>
+cudaError_t launch_cluster(Kernel kernel, uint32_t clusters, uint32_t size, uint32_t threads, int smem, cudaStream_t stream,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int MT>
 mla_status_t launch_thin(MatmulParams& p, int dev, int sms, int slot, cudaStream_t stream) {
   auto kernel = matmul_thin_kernel<MT>;
@@ -577,18 +664,7 @@ mla_status_t launch_thin(MatmulParams& p, int dev, int sms, int slot, cudaStream
   uint32_t splits = 1;
   while (splits < 8 && tiles * splits < static_cast<uint64_t>(sms) && p.kblocks >= 4 * splits) splits *= 2;
   if (tiles * splits > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<uint32_t>(tiles * splits));
-  cfg.blockDim = dim3(kThinThreads);
-  cfg.dynamicSmemBytes = kThinSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, splits);
+  const cudaError_t e = launch_cluster(kernel, static_cast<uint32_t>(tiles), splits, kThinThreads, kThinSmem, stream, p, splits);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
   return MLA_OK;
 }
@@ -669,15 +745,23 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;
-  // Whichever kernel is expected to end first, from what both measured (us, tile /
-  // thin): 200x8192x8192 33 / 38, 300x4096x4096 19 / 21, 1024x2048x2048 12 / 14,
-  // 256x16384x512 7.3 / 15, but 512x1024x8192 33 / 16, 1000x576x8192 33 / 23,
-  // 128x8192x8192 33 / 25.  The tile kernel takes 0.45 us a block of K for each
-  // round of its CTA pairs, the thin one 2.1 ns a block of 128 x 64 outputs and
-  // 1.3 us more at its ends.
-  const uint64_t rounds = (pairs * wide + sms / 2 - 1) / (sms / 2);
-  const uint64_t thin_blocks = static_cast<uint64_t>((M + 63) / 64) * ((N + 127) / 128) * kb;
-  if (M > 64 && 4500 * kb * rounds < 13000 + 21 * thin_blocks) {
+  // Whichever kernel is expected to end first; costs in 0.1 ns, from what both
+  // measured.  A block of K takes a tile 0.5 us, in each round of the CTA pairs; pairs
+  // that share a tile's K take 4 (two) or 6 to 8 us (four) longer to meet.  The few-token
+  // kernel takes 2 to 3 ns a block of 128 x 64 outputs over the whole GPU.  (us, tile / shared by
+  // two / by four / few-token: 256x576x512 7.4 / - / - / 8.6, 1000x1000x1024 9.3 / 11.3 / 26 /
+  // 11.4, 200x4096x7168 33 / 23.4 / 38 / 23.0, 2000x576x7168 33 / 23.6 / 39 / 34,
+  // 256x7168x16384 71 / 43 / 60 / 63, 700x1000x16384 68 / 41 / 29.8 / 41.)
+  const uint64_t tiles = pairs * wide, thin_blocks = static_cast<uint64_t>((M + 63) / 64) * ((N + 127) / 128) * kb;
+  uint64_t best = 55000 + 5000 * kb * ((tiles + sms / 2 - 1) / (sms / 2));
+  uint32_t splits = 1;
+  for (uint32_t sp = 2; sp <= 4 && sp <= kb; sp *= 2) {
+    // Clusters at a time: 36 of four CTAs; of eight, 12 fit and 16 do not.
+    if (tiles > static_cast<uint64_t>(sp == 2 ? sms / 4 - 2 : sms / 12)) break;
+    const uint64_t cost = 5000 * ((kb + sp - 1) / sp) + (sp == 2 ? 93000 : 115000);
+    if (cost < best) best = cost, splits = sp;
+  }
+  if (M > 64 && best < 85000 + 22 * thin_blocks) {
     if (pairs * wide > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
     if ((st = encode_codes(&p.tm_x, x, kTileM, "x")) != MLA_OK) return st;
     if ((st = encode_codes(&p.tm_w, w, kTileN / 2, "w")) != MLA_OK) return st;
@@ -694,11 +778,14 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
     p.m_tiles = static_cast<uint32_t>(pairs);
     p.n_tiles = static_cast<uint32_t>(wide);
     const int smem = static_cast<int>(sizeof(TileSmem) + 1024);
-    if ((st = set_max_dynamic_smem(reinterpret_cast<const void*>(matmul_tile_kernel), smem, dev, 8)) != MLA_OK) return st;
-    if ((st = check_registers(reinterpret_cast<const void*>(matmul_tile_kernel), kTileRegs, dev, 8)) != MLA_OK) return st;
-    const uint32_t clusters = static_cast<uint32_t>(std::min<uint64_t>(pairs * wide, static_cast<uint64_t>(sms) / 2));
-    matmul_tile_kernel<<<2 * clusters, kTileThreads, smem, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const auto kernel = splits > 1 ? matmul_tile_kernel<true> : matmul_tile_kernel<false>;
+    const int slot = splits > 1 ? 12 : 8;
+    if ((st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev, slot)) != MLA_OK) return st;
+    if ((st = check_registers(reinterpret_cast<const void*>(kernel), kTileRegs, dev, slot)) != MLA_OK) return st;
+    p.splits = splits;
+    // Split tiles have a cluster each; the others' clusters walk the tiles.
+    const uint32_t clusters = static_cast<uint32_t>(splits > 1 ? tiles : std::min<uint64_t>(tiles, static_cast<uint64_t>(sms) / 2));
+    cudaError_t e = launch_cluster(kernel, clusters, 2 * splits, kTileThreads, smem, s, p);
     if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
     return MLA_OK;
   }

@@ -195,6 +195,25 @@ def test_matmul_strides(lib, m, n, k, dtype):
     assert (buf == 3).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(700, 2048, 4112), (129, 8200, 6000), (760, 1000, 10000), (65, 1100, 40960)])
+@pytest.mark.parametrize("dtype,pad", [(torch.bfloat16, 8), (torch.float32, 5)])
+def test_matmul_few_tiles_of_a_long_k(lib, m, n, k, dtype, pad):
+    """Few output tiles, whose K is shared by several CTA pairs in unequal parts; outputs stored in
+    both ways, the same in every run."""
+    from mla_ragged_paged_gb300 import binding
+    x, xs, w, ws = _matmul_case(m, n, k, 5)
+    buf = torch.full((m + 1, n + pad), 3.0, dtype=dtype, device="cuda")
+    out = buf[:m, :n]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.matmul_fp8(out, x, xs, w, ws, status)
+    first = out.clone()
+    _check_matmul(out, x, xs, w, ws)
+    out.fill_(3)
+    assert (buf == 3).all() and int(status) == 0
+    binding.matmul_fp8(out, x, xs, w, ws)
+    assert torch.equal(out, first)
+
+
 @pytest.mark.parametrize("dtype,pad", [(torch.bfloat16, 24), (torch.float32, 4), (torch.float32, 12)])
 def test_matmul_aligned_padded_rows(lib, dtype, pad):
     """Output rows that start 16-byte aligned and end inside a store's width:
