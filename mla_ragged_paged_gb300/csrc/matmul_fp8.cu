@@ -12,11 +12,11 @@
 // * matmul_tile_kernel, for products with many output tiles: persistent CTA
 //   pairs, each CTA one 128 x 256 output tile; the pair shares its weight tile by
 //   TMA multicast, because one SM's share of the L2 cannot feed 48 KB per 512
-//   tensor-core cycles.  Measured 8192^3 in 434 us = 2530 TFLOP/s;
+//   tensor-core cycles.  Measured 8192^3 in 430 us = 2560 TFLOP/s;
 //   without the sums in fp32 333 us, without the UMMAs as well 278 us.  What bounds it
-//   is how far the 32 768 fp32 products a block hide behind the tensor cores; more
-//   warps for them, scales read earlier and UMMAs over the CTA pair measured slower
-//   (450 .. 527 us).
+//   is a tile's chain of tensor memory reads and sums, 0.5 us a block however few SMs
+//   are busy; more warps for them, scales read earlier and UMMAs over the CTA pair
+//   measured slower (450 .. 527 us).
 //   Where tiles are few and K is long, two or four pairs share a tile's K as one
 //   cluster and add their sums through distributed shared memory
 //   (2000 x 576 x 16384: 69 -> 42 us).
@@ -747,7 +747,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;
   // Whichever kernel is expected to end first; costs in 0.1 ns, from what both
   // measured.  A block of K takes a tile 0.5 us, in each round of the CTA pairs; pairs
-  // that share a tile's K take 4 (two) or 6 to 8 us (four) longer to meet.  The few-token
+  // that share a tile's K take 4.5 (two) or 6 to 8 us (four) longer to meet.  The few-token
   // kernel takes 2 to 3 ns a block of 128 x 64 outputs over the whole GPU.  (us, tile / shared by
   // two / by four / few-token: 256x576x512 7.4 / - / - / 8.6, 1000x1000x1024 9.3 / 11.3 / 26 /
   // 11.4, 200x4096x7168 33 / 23.4 / 38 / 23.0, 2000x576x7168 33 / 23.6 / 39 / 34,
@@ -758,7 +758,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   for (uint32_t sp = 2; sp <= 4 && sp <= kb; sp *= 2) {
     // Clusters at a time: 36 of four CTAs; of eight, 12 fit and 16 do not.
     if (tiles > static_cast<uint64_t>(sp == 2 ? sms / 4 - 2 : sms / 12)) break;
-    const uint64_t cost = 5000 * ((kb + sp - 1) / sp) + (sp == 2 ? 93000 : 115000);
+    const uint64_t cost = 5000 * ((kb + sp - 1) / sp) + (sp == 2 ? 100000 : 115000);
     if (cost < best) best = cost, splits = sp;
   }
   if (M > 64 && best < 85000 + 22 * thin_blocks) {
