@@ -790,6 +790,18 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       }
     }
     named_bar_sync(bar, 128);
+    // Whole row tiles: neighbouring lanes trade values, so that an even lane stores
+    // two dims of the even rows and an odd lane two of the odd ones.
+    const uint32_t odd = lane & 1;
+    uint16_t* to[N / 2] = {};
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        const uint32_t r = first_row + r0 + 2 * k + odd, tok = r / p.H;
+        if (r < g.s.rows)
+          to[k] = p.out + (g.s.q0 + static_cast<long long>(tok)) * p.o_tok + (r - tok * p.H) * p.o_head + (key - odd);
+      }
+    }
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[N];
@@ -798,15 +810,20 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
       tmem_ld_wait();
       const uint32_t dim = c * 128 + key;
       if (whole) {
-        uint32_t tok = (first_row + r0) / p.H, head = first_row + r0 - tok * p.H;
+        float w[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (first_row + r0 + i < g.s.rows) {
-            const float v = s.row_val[group][i];
-            p.out[(g.s.q0 + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + dim] =
-                static_cast<uint16_t>(pack_bf16x2(v != 0.f ? __uint_as_float(o[i]) * v : 0.f, 0.f));
-          }
-          if (++head == p.H) head = 0, ++tok;
+        for (int i = 0; i < N; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
+          w[i] = f.x != 0.f ? __uint_as_float(o[i]) * f.x : 0.f;
+          w[i + 1] = f.y != 0.f ? __uint_as_float(o[i + 1]) * f.y : 0.f;
+          w[i + 2] = f.z != 0.f ? __uint_as_float(o[i + 2]) * f.z : 0.f;
+          w[i + 3] = f.w != 0.f ? __uint_as_float(o[i + 3]) * f.w : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? w[2 * k] : w[2 * k + 1], 1);
+          const uint32_t pair = odd ? pack_bf16x2(got, w[2 * k + 1]) : pack_bf16x2(w[2 * k], got);
+          if (to[k]) *reinterpret_cast<uint32_t*>(to[k] + c * 128) = pair;
         }
       } else {
         float* dst = p.part_o + (static_cast<size_t>(slot) * kMaxRows + r0) * kLatent + dim;
