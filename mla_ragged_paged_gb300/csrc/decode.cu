@@ -181,12 +181,12 @@ __device__ __forceinline__ Seq sequence(const DecodeParams& p, const RawSeq& r) 
 }
 
 // What is left of a CTA's share: `left` steps from step `at` of row tile rt of
-// sequence b, whose lengths have been read ahead.  A row tile's steps are
+// sequence b.  (Its lengths are read again for every row tile: the prologue has brought
+// them close.)  A row tile's steps are
 // kStartSteps that stand for what beginning it costs, then one for each key tile.
 struct Share {
   unsigned long long left;
   uint32_t b, rt, at;
-  RawSeq raw;
 };
 struct Segment {
   Seq s;
@@ -195,9 +195,9 @@ struct Segment {
 template <int NR>
 __device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, Segment& g) {
   while (sh.left && sh.b < p.B) {
-    const Seq s = sequence<NR>(p, sh.raw);
+    const Seq s = sequence<NR>(p, load_raw(p, sh.b));
     if (!s.row_tiles || !s.key_tiles) {
-      sh.raw = load_raw(p, ++sh.b);
+      ++sh.b;
       continue;
     }
     g.s = s;
@@ -213,7 +213,7 @@ __device__ __forceinline__ bool next_segment(const DecodeParams& p, Share& sh, S
       sh.at = 0;
       if (++sh.rt == s.row_tiles) {
         sh.rt = 0;
-        sh.raw = load_raw(p, ++sh.b);
+        ++sh.b;
       }
     }
     if (g.kt0 == g.kt1) continue;   // the share ends before the row tile's first key tile
@@ -940,7 +940,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
         pro.start.b = b;
         pro.start.rt = static_cast<uint32_t>((u0 - start) / each);
         pro.start.at = static_cast<uint32_t>((u0 - start) % each);
-        pro.start.raw = raw;
         break;
       }
       start += here;
