@@ -218,7 +218,7 @@ __device__ void tile_scales(TileSmem& s, const MatmulParams& p, const TilePlace<
     fetch(at.kb0 + block);
     for (uint32_t kb = at.kb0; kb < at.kb1; kb += kScaleBlocks, ++pos) {
       const uint32_t buf = pos & 1u;
-      if (!mbar_wait(smem_u32(&s.scale_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort)) return;
+      mbar_wait(smem_u32(&s.scale_empty[buf]), ((pos >> 1) & 1u) ^ 1u, abort);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s.x_scale[buf][block][half * 64 + sub + 4 * i] = x[i];
       if (sub == 0) s.w_scale[buf][half][block] = w;
@@ -299,7 +299,9 @@ __device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* stage
 // One of two warpgroups: half of the tile's columns, a row per thread.  Where pairs
 // share a tile's K (one tile a cluster then), each CTA leaves its sums in its shared
 // memory, in the ring's place, and takes a part of the rows (warps' quarters) to add
-// up in the order of the pairs and store.
+// up in the order of the pairs and store.  (A warp never leaves early: after a wait that
+// gave up it goes on with values that mean nothing, so that its lanes stay together
+// and the cluster meets.  So do the scales' warps.)
 template <bool SPLIT>
 __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePlace<SPLIT>& at, uint32_t tmem, uint32_t half, int quarter,
                                 int lane, volatile uint32_t* abort) {
@@ -313,25 +315,16 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePl
     float acc[kAccCols];
 #pragma unroll
     for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
-    bool alive = true;   // (SPLIT: all CTAs of the cluster meet below, whatever happens)
     for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
       const uint32_t buf = (pos & 1u) * 2 + half, in = (kb - at.kb0) % kScaleBlocks, cb = chunk & 1u;
-      if (in == 0 && !mbar_wait(smem_u32(&s.scale_full[cb]), (chunk >> 1) & 1u, abort)) {
-        if constexpr (!SPLIT) return;
-        alive = false;
-        break;
-      }
+      if (in == 0) mbar_wait(smem_u32(&s.scale_full[cb]), (chunk >> 1) & 1u, abort);
       const float scale = s.x_scale[cb][in][quarter * 32 + lane] * s.w_scale[cb][half][in];
       if (in == kScaleBlocks - 1 || kb + 1 == at.kb1) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.scale_empty[cb]));
         ++chunk;
       }
-      if (!mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort)) {
-        if constexpr (!SPLIT) return;
-        alive = false;
-        break;
-      }
+      mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort);
       tc_fence_after();
       const uint32_t col = taddr + (pos & 1u) * kTileN;
       uint32_t v[2][32];
@@ -354,22 +347,17 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePl
     if constexpr (SPLIT) {
       // (The ring is idle: every copy into it has been multiplied.)
       float* part = reinterpret_cast<float*>(s.x[0]) + (half * 4 + quarter) * (kAccCols * 32) + lane;
-      if (alive) {
 #pragma unroll
-        for (int e = 0; e < kAccCols; ++e) part[32 * e] = acc[e];
-      }
+      for (int e = 0; e < kAccCols; ++e) part[32 * e] = acc[e];
       cluster_sync();
-      alive = alive && quarter * p.splits / 4 == at.pair;
-      if (alive) {
+      if (quarter * p.splits / 4 != at.pair) return;
 #pragma unroll
-        for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
-        for (uint32_t i = 0; i < p.splits; ++i) {
-          const uint32_t from = map_shared(smem_u32(part), 2 * i + at.rank);
+      for (int e = 0; e < kAccCols; ++e) acc[e] = 0.f;
+      for (uint32_t i = 0; i < p.splits; ++i) {
+        const uint32_t from = map_shared(smem_u32(part), 2 * i + at.rank);
 #pragma unroll
-          for (int e = 0; e < kAccCols; ++e) acc[e] += ld_shared_cluster(from + 128 * e);
-        }
+        for (int e = 0; e < kAccCols; ++e) acc[e] += ld_shared_cluster(from + 128 * e);
       }
-      if (!alive) return;
     }
     store_rows(p, s.stage[half * 4 + quarter], acc, m0, n0, lane);
   }
