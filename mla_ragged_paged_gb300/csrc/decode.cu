@@ -22,8 +22,9 @@
 //   O^T [4 x 128 dims, rows] += codes^T (512 dims) . P^T
 // Both products are of 8-bit operands, so q and the softmax weights are split
 // into two terms, a value and what its rounding left.  q, scaled by a power of
-// two per row, is reproduced exactly: a bf16 value has eight significant bits,
-// each e4m3 term four; its terms are stacked as 2 x rows columns of one product.
+// two per row, is reproduced exactly down to 2^-9 of the row's largest value (a bf16
+// value has eight significant bits, each e4m3 term four) and to 2^-17 of it below;
+// its terms are stacked as 2 x rows columns of one product.
 // A weight is e4m3 + e5m2 (seven significant bits, down to 2^-17), two products
 // into one O, and the sum that divides O is of the weights as the products see
 // them, so that a row which hangs on one key is exact.  (lse takes the unrounded
