@@ -652,7 +652,10 @@ size_t mla_decode_latent_workspace_size(void);
  *                aligned; its contents before the call do not matter.  Calls
  *                that may overlap on the GPU need distinct workspaces.
  * Sums and softmax statistics are 32-bit; the weights that multiply the cached
- * codes carry seven significant bits and are normalised by their own sum.
+ * codes carry seven significant bits and are normalised by their own sum.  A
+ * query's elements are taken exactly down to 2^-9 of its largest one, smaller
+ * ones to 2^-17 of that: next to an element 2^10 times larger they keep seven
+ * bits, next to one 2^14 times larger three.
  * Slots past a sequence's context may hold anything.  A query all of whose
  * keys are masked gets 0 and lse -inf.  Rows outside [row_offsets[0],
  * row_offsets[B]) are not written.

@@ -423,6 +423,26 @@ def test_decode_value_ranges(lib, q_std, spread, sink):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("large", [2.0 ** 8, 2.0 ** 10, 2.0 ** 14])
+def test_decode_query_elements_next_to_a_large_one(lib, large):
+    """One element far above the others, in a dim that the cache leaves at zero: the others must
+    keep what is documented."""
+    d = Decode([1, 2], [700, 40], 20, 64, seed=77, q_std=1.0)
+    d.q.clamp_(-2, 2)
+    d.q[:, :, 7] = large
+    d.codes.view(torch.uint8)[..., 7] = 0
+    out, lse = _run_decode(d)
+    # The two terms: the row's largest element is scaled into [128, 256).
+    q = d.q.float()
+    up = 2.0 ** (7 - torch.floor(torch.log2(q.abs().amax(-1, keepdim=True))))
+    first = (q * up).to(E4M3).float()
+    taken = (first + (q * up - first).to(E4M3).float()) / up
+    assert ((taken - q).abs() <= 2.0 ** -17 * large).all()
+    assert torch.equal(taken[q.abs() >= 2.0 ** -9 * large], q[q.abs() >= 2.0 ** -9 * large])
+    d.q = taken
+    _check_decode(d, out, lse)
+
+
 def test_decode_tail_behind_a_sink(lib):
     """One key takes e^12 times the weight of each of 40 000 others, which
     together outweigh it in the first 512 columns: weights rounded to steps of
