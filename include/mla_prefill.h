@@ -692,8 +692,9 @@ mla_status_t mla_test_inject_stall(uint32_t enable);
  * Test hook for the pipeline's ordering (no counterpart on the pages).  While
  * nonzero (process-wide), the softmax warps of the second query tile of every
  * attention work item wait `nanoseconds` (at most 100000) before loading each
- * score tile, so that tile runs far behind the first one; results must be
- * bit-identical to an undelayed launch, only slower.  0 turns it off.  Never
+ * score tile, so that tile runs far behind the first one; likewise the warps
+ * that add up the second half of a tile's columns in mla_matmul_fp8, where a tile's K is
+ * shared, before each block of K.  Results must be bit-identical to an undelayed launch, only slower.  0 turns it off.  Never
  * set it outside tests.
  */
 mla_status_t mla_test_delay_softmax(uint32_t nanoseconds);

@@ -753,7 +753,7 @@ def test_inject_stall(enable):
 
 def test_delay_softmax(nanoseconds):
     """mla_test_delay_softmax: delay the second query tile's softmax before
-    every score-tile load (tests of the pipeline's ordering only)."""
+    every score-tile load, and the second half of a tile's columns in matmul_fp8 (tests of the pipeline's ordering only)."""
     _check(load().mla_test_delay_softmax(int(nanoseconds)))
 
 

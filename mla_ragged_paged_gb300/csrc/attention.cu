@@ -1584,7 +1584,6 @@ mla_status_t launch_attention(AttnParams& prm, int dev, int sms, const uint32_t*
 }
 
 std::atomic<uint32_t> g_test_stall{0};
-std::atomic<uint32_t> g_test_delay_ns{0};
 
 // Full-context call (buffer_row_offsets == NULL) or one buffer row of a
 // chunked call (with lse).
@@ -1827,7 +1826,7 @@ mla_status_t prefill(const mla_tensor_t* out, const mla_tensor_t* lse, const mla
   prm.H = static_cast<uint32_t>(H);
   prm.causal = mask == MLA_MASK_CAUSAL;
   prm.test_stall = g_test_stall.load(std::memory_order_relaxed);
-  prm.test_delay_ns = g_test_delay_ns.load(std::memory_order_relaxed);
+  prm.test_delay_ns = test_delay_ns();
   prm.sl2 = scale * 1.4426950408889634f;
   prm.ws = static_cast<uint8_t*>(workspace);
   prm.q_base = static_cast<const uint8_t*>(q->data);
@@ -1897,12 +1896,6 @@ extern "C" mla_status_t mla_prefill_ragged(const mla_tensor_t* out, const mla_te
 
 extern "C" mla_status_t mla_test_inject_stall(uint32_t enable) {
   mla::g_test_stall.store(enable ? 1u : 0u, std::memory_order_relaxed);
-  return MLA_OK;
-}
-
-extern "C" mla_status_t mla_test_delay_softmax(uint32_t nanoseconds) {
-  if (nanoseconds > 100000u) return mla::fail(MLA_ERR_INVALID_ARG, "delay above 100 us");
-  mla::g_test_delay_ns.store(nanoseconds, std::memory_order_relaxed);
   return MLA_OK;
 }
 

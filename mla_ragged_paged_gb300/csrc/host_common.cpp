@@ -16,6 +16,8 @@ std::atomic<int> g_num_sms[kMaxDevices];  // 0 = unknown, -1 = unsupported devic
 std::atomic<int> g_smem_set[kMaxDevices][kSmemSlots];
 std::atomic<int> g_regs_ok[kMaxDevices][kSmemSlots];
 
+std::atomic<uint32_t> g_test_delay_ns{0};
+
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
@@ -119,7 +121,15 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
   return MLA_OK;
 }
 
+uint32_t test_delay_ns() { return g_test_delay_ns.load(std::memory_order_relaxed); }
+
 }  // namespace mla
+
+extern "C" mla_status_t mla_test_delay_softmax(uint32_t nanoseconds) {
+  if (nanoseconds > 100000u) return mla::fail(MLA_ERR_INVALID_ARG, "delay above 100 us");
+  mla::g_test_delay_ns.store(nanoseconds, std::memory_order_relaxed);
+  return MLA_OK;
+}
 
 extern "C" const char* mla_last_error_string(void) { return mla::g_error; }
 

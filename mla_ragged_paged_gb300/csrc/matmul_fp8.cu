@@ -52,6 +52,7 @@ struct MatmulParams {
   uint32_t tma;                 // every output row starts 16-byte aligned
   uint32_t m_tiles, n_tiles;    // tile kernel: m_tiles counts pairs of 128 rows
   uint32_t splits;              // tile kernel: CTA pairs that share a tile's K, a cluster
+  uint32_t test_delay_ns;       // test hook, where pairs share K: how long the second accumulating warpgroup waits before each block
   uint32_t* status;
 };
 
@@ -325,6 +326,14 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePl
         ++chunk;
       }
       mbar_wait(smem_u32(&s.acc_full[buf]), (pos >> 1) & 1u, abort);
+      if constexpr (SPLIT) {
+        if (half == 1 && p.test_delay_ns) {
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < p.test_delay_ns) {
+          }
+          __syncwarp();
+        }
+      }
       tc_fence_after();
       const uint32_t col = taddr + (pos & 1u) * kTileN;
       uint32_t v[2][32];
@@ -345,7 +354,11 @@ __device__ void tile_accumulate(TileSmem& s, const MatmulParams& p, const TilePl
       }
     }
     if constexpr (SPLIT) {
-      // (The ring is idle: every copy into it has been multiplied.)
+      // The sums take the ring's place.  A warpgroup has only seen its own half of
+      // the last block multiplied, and the other half's UMMAs, which wait for the other
+      // warpgroup to free their accumulator, read the same x: only where both
+      // warpgroups have their last accumulator is every copy in the ring multiplied.
+      named_bar_sync(1, 32 * kAccWarps);
       float* part = reinterpret_cast<float*>(s.x[0]) + (half * 4 + quarter) * (kAccCols * 32) + lane;
 #pragma unroll
       for (int e = 0; e < kAccCols; ++e) part[32 * e] = acc[e];
@@ -730,6 +743,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   p.kblocks = static_cast<uint32_t>(kb);
   p.out_f32 = out->dtype == MLA_DTYPE_F32;
   p.status = status;
+  p.test_delay_ns = test_delay_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;

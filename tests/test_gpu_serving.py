@@ -214,6 +214,26 @@ def test_matmul_few_tiles_of_a_long_k(lib, m, n, k, dtype, pad):
     assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("m,n,k", [(700, 2048, 4112), (760, 1000, 10000), (129, 8200, 6000)])
+def test_matmul_delayed_second_half_keeps_results(lib, m, n, k):
+    """One half of a tile's columns added up far behind the other where K is shared: the first
+    half's sums must not take the place of operands that the second half still needs."""
+    from mla_ragged_paged_gb300 import binding
+    x, xs, w, ws = _matmul_case(m, n, k, 6)
+    ref, out = (torch.empty(m, n, device="cuda") for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.matmul_fp8(ref, x, xs, w, ws, status)
+    _check_matmul(ref, x, xs, w, ws)
+    binding.test_delay_softmax(5000)
+    try:
+        for _ in range(5):
+            out.fill_(float("nan"))
+            binding.matmul_fp8(out, x, xs, w, ws, status)
+            assert torch.equal(out, ref) and int(status) == 0
+    finally:
+        binding.test_delay_softmax(0)
+
+
 @pytest.mark.parametrize("dtype,pad", [(torch.bfloat16, 24), (torch.float32, 4), (torch.float32, 12)])
 def test_matmul_aligned_padded_rows(lib, dtype, pad):
     """Output rows that start 16-byte aligned and end inside a store's width:
