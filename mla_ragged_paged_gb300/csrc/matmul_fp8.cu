@@ -9,17 +9,17 @@
 // tensor memory.  No sum ever passes through fewer than 32 bits.
 //
 // Two kernels (the host's rule compares their expected times):
-// * matmul_tile_kernel, for products with many output tiles: persistent CTA
-//   pairs, each CTA one 128 x 256 output tile; the pair shares its weight tile by
-//   TMA multicast, because one SM's share of the L2 cannot feed 48 KB per 512
-//   tensor-core cycles.  Measured 8192^3 in 430 us = 2560 TFLOP/s;
-//   without the sums in fp32 333 us, without the UMMAs as well 278 us.  What bounds it
-//   is a tile's chain of tensor memory reads and sums, 0.5 us a block however few SMs
-//   are busy; more warps for them, scales read earlier and UMMAs over the CTA pair
-//   measured slower (450 .. 527 us).
-//   Where tiles are few and K is long, two or four pairs share a tile's K as one
+// * matmul_tile_kernel, for products with many output tiles: persistent CTAs of
+//   one 128 x 256 output tile; two neighbouring CTAs take the same columns, so that
+//   the second one finds the weight tile in L2.  Measured 8192^3 in 458 us = 2400
+//   TFLOP/s.  What bounds it is a tile's chain of tensor memory reads and sums, 0.44 us
+//   a block with few SMs busy and 0.5 with all (a quarter of it goes without the sums in
+//   fp32), and, where rows of x and w do not start at whole 128-byte lines, what an SM
+//   draws from L2, 48 KB a block in two lines a row (5001 x 8200, fp32 output: K = 4112
+//   201 us, with rows padded to 4224 bytes 171 us, K = 4096 163 us = 2060 TFLOP/s).
+//   Where tiles are few and K is long, two or four such pairs share a tile's K as one
 //   cluster and add their sums through distributed shared memory
-//   (2000 x 576 x 16384: 69 -> 42 us).
+//   (2000 x 576 x 16384: 69 -> 43 us).
 // * matmul_thin_kernel, for few tokens: bound by HBM (w), 4.8 TB/s at
 //   64 x 8192 x 16384 (28 us).  The weights are the 128-row operand and the tokens the
 //   narrow one, so few rows waste no tensor time, and K is split over a cluster of
@@ -93,18 +93,17 @@ __device__ __forceinline__ void tile_of(const MatmulParams& p, uint32_t t, uint3
   m = band * kBand + (r - n * rows);
 }
 
-// A CTA's place: which tiles its cluster walks, which blocks of K its pair takes
-// (SPLIT: of the p.splits pairs of a cluster; else the cluster is one pair).
+// A CTA's place: which tiles its pair (SPLIT: its cluster of p.splits pairs) walks,
+// which blocks of K its pair takes.
 template <bool SPLIT>
 struct TilePlace {
   uint32_t rank, pair;          // in the pair, in the cluster
   uint32_t first, step;         // tiles
   uint32_t kb0, kb1;
   __device__ __forceinline__ explicit TilePlace(const MatmulParams& p) {
-    const uint32_t r = cluster_rank();
-    rank = r & 1u;
+    rank = blockIdx.x & 1u;
     if constexpr (SPLIT) {
-      pair = r >> 1;
+      pair = cluster_rank() >> 1;
       first = blockIdx.x / (2 * p.splits);
       step = gridDim.x / (2 * p.splits);
       kb0 = p.kblocks * pair / p.splits;
@@ -128,7 +127,7 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, const TilePlac
     uint32_t m, n;
     tile_of(p, t, m, n);
     const int32_t mr = static_cast<int32_t>((2 * m + rank) * kTileM);
-    const int32_t nr = static_cast<int32_t>(n * kTileN + rank * (kTileN / 2));
+    const int32_t nr = static_cast<int32_t>(n * kTileN);
     for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
       const uint32_t st = pos % kStages;
       if (!(alive = mbar_wait(smem_u32(&s.empty[st]), ((pos / kStages) & 1u) ^ 1u, abort))) break;
@@ -136,15 +135,8 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, const TilePlac
       mbar_arrive_expect_tx(bar, kXBytes + kWBytes);
       const int32_t k = static_cast<int32_t>(kb * kKB);
       tma_load_2d(smem_u32(s.x[st]), &p.tm_x, bar, k, mr);
-      // Half of the pair's weight tile, into both CTAs.
-      tma_load_2d_multicast(smem_u32(s.w[st]) + rank * (kWBytes / 2), &p.tm_w, bar, k, nr,
-                            static_cast<uint16_t>(3u << (2 * at.pair)));
+      tma_load_2d(smem_u32(s.w[st]), &p.tm_w, bar, k, nr);
     }
-  }
-  // Both CTAs' UMMA threads have arrived on every slot before this CTA exits.
-  for (uint32_t i = pos < kStages ? pos : kStages; i >= 1 && !*abort; --i) {
-    const uint32_t q = pos - i;
-    mbar_wait(smem_u32(&s.empty[q % kStages]), (q / kStages) & 1u, abort);
   }
   if (*abort) {
     // Let the copies still in flight land before the CTA exits.
@@ -183,7 +175,7 @@ __device__ void tile_mma(TileSmem& s, const MatmulParams& p, const TilePlace<SPL
         umma_commit(smem_u32(&s.acc_full[buf]));
       }
       if (!alive) break;
-      umma_commit_multicast(smem_u32(&s.empty[st]), static_cast<uint16_t>(3u << (2 * at.pair)));
+      umma_commit(smem_u32(&s.empty[st]));
     }
   }
   // No UMMA may still be in flight when tensor memory is released.
@@ -387,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul_tile_kernel(const __gr
     s.abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), 2);   // both CTAs' UMMA threads: a slot is filled for both at once
+      mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s.acc_full[i]), 1);
@@ -407,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul_tile_kernel(const __gr
     tmem_relinquish();
   }
   tc_fence_before();
-  cluster_sync();   // both CTAs' barriers are ready before either copies into the other
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   if (warp < 4) {
@@ -423,7 +415,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul_tile_kernel(const __gr
     if (lane == 0) bulk_wait_group_all();   // the staging buffers outlive their stores
   }
   tc_fence_before();
-  cluster_sync();   // the other CTA no longer copies into this one or arrives on its barriers
+  if constexpr (SPLIT) cluster_sync();   // no CTA leaves while another reads its sums
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -748,25 +741,27 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;
   // Whichever kernel is expected to end first; costs in 0.1 ns, from what both
-  // measured.  A block of K takes a tile 0.5 us, in each round of the CTA pairs; pairs
-  // that share a tile's K take 4.5 (two) or 6 to 8 us (four) longer to meet.  The few-token
+  // measured; the output is left out.  A
+  // block of K takes a tile 0.44 us, in each round of the CTA pairs, and 0.55 us where pairs
+  // share its K, which take 4 (two) or 7 us (four) longer to meet.  The few-token
   // kernel takes 2 to 3 ns a block of 128 x 64 outputs over the whole GPU.  (us, tile / shared by
-  // two / by four / few-token: 256x576x512 7.4 / - / - / 8.6, 1000x1000x1024 9.3 / 11.3 / 26 /
-  // 11.4, 200x4096x7168 33 / 23.4 / 38 / 23.0, 2000x576x7168 33 / 23.6 / 39 / 34,
-  // 256x7168x16384 71 / 43 / 60 / 63, 700x1000x16384 68 / 41 / 29.8 / 41.)
+  // two / by four / few-token: 256x576x512 5.9 / 9.3 / 12.2 / 8.2, 1000x1000x1024 8.1 / 10.7 / - /
+  // 10.8, 300x4096x4096 18.4 / 17.8 / - / 21.5, 200x4096x7168 29.0 / 23.6 / - / 22.7,
+  // 512x1024x8192 31.8 / 25.4 / 20.6 / 15.9, 2000x576x7168 29.1 / 23.6 / - / 33.5,
+  // 256x7168x16384 61.5 / 44.5 / - / 69.6, 700x1000x16384 60.5 / 42.4 / 29.8 / 40.1.)
   const uint64_t tiles = pairs * wide, thin_blocks = static_cast<uint64_t>((M + 63) / 64) * ((N + 127) / 128) * kb;
-  uint64_t best = 55000 + 5000 * kb * ((tiles + sms / 2 - 1) / (sms / 2));
+  uint64_t best = 41000 + 4400 * kb * ((tiles + sms / 2 - 1) / (sms / 2));
   uint32_t splits = 1;
   for (uint32_t sp = 2; sp <= 4 && sp <= kb; sp *= 2) {
     // Clusters at a time: 36 of four CTAs; of eight, 12 fit and 16 do not.
     if (tiles > static_cast<uint64_t>(sp == 2 ? sms / 4 - 2 : sms / 12)) break;
-    const uint64_t cost = 5000 * ((kb + sp - 1) / sp) + (sp == 2 ? 100000 : 115000);
+    const uint64_t cost = 5500 * ((kb + sp - 1) / sp) + (sp == 2 ? 81000 : 114000);
     if (cost < best) best = cost, splits = sp;
   }
   if (M > 64 && best < 85000 + 22 * thin_blocks) {
     if (pairs * wide > 0x7FFFFFFFull) return fail(MLA_ERR_INVALID_ARG, "too many output tiles");
     if ((st = encode_codes(&p.tm_x, x, kTileM, "x")) != MLA_OK) return st;
-    if ((st = encode_codes(&p.tm_w, w, kTileN / 2, "w")) != MLA_OK) return st;
+    if ((st = encode_codes(&p.tm_w, w, kTileN, "w")) != MLA_OK) return st;
     const uint64_t es = p.out_f32 ? 4 : 2;
     p.tma = aligned16(out->data) && (static_cast<uint64_t>(out->stride[0]) * es) % 16 == 0 && out->stride[0] < (1ll << 38);
     if (p.tma) {
@@ -785,9 +780,10 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
     if ((st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev, slot)) != MLA_OK) return st;
     if ((st = check_registers(reinterpret_cast<const void*>(kernel), kTileRegs, dev, slot)) != MLA_OK) return st;
     p.splits = splits;
-    // Split tiles have a cluster each; the others' clusters walk the tiles.
-    const uint32_t clusters = static_cast<uint32_t>(splits > 1 ? tiles : std::min<uint64_t>(tiles, static_cast<uint64_t>(sms) / 2));
-    cudaError_t e = launch_cluster(kernel, clusters, 2 * splits, kTileThreads, smem, s, p);
+    // Split tiles have a cluster each; the others' pairs of CTAs walk the tiles.
+    const uint32_t pairs_of_ctas = static_cast<uint32_t>(splits > 1 ? tiles * splits : std::min<uint64_t>(tiles, static_cast<uint64_t>(sms) / 2));
+    const uint32_t size = splits > 1 ? 2 * splits : 1;
+    cudaError_t e = launch_cluster(kernel, 2 * pairs_of_ctas / size, size, kTileThreads, smem, s, p);
     if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "matmul launch: %s", cudaGetErrorString(e));
     return MLA_OK;
   }

@@ -1,6 +1,7 @@
 """Refusals of the serving-step entry points (norm, block-scaled product,
 latent append, latent decode): host checks, no GPU needed."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -178,6 +179,14 @@ def test_good_arguments_reach_the_device_check(lib):
         pytest.skip("would launch on made-up addresses")
     for call in (_norm, _matmul, _append, _decode):
         assert call(lib) in (binding.MLA_ERR_UNSUPPORTED, binding.MLA_ERR_CUDA)
+
+
+def test_no_kernel_copies_by_multicast():
+    """Ranks of multi-GPU jobs load the library: every copy lands in the CTA that issued it."""
+    csrc = os.path.join(os.path.dirname(pkg.__file__), "csrc")
+    for name in os.listdir(csrc):
+        with open(os.path.join(csrc, name)) as f:
+            assert "multicast" not in f.read(), name
 
 
 def test_packed_descriptors_have_the_structs_layout():
