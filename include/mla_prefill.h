@@ -639,7 +639,9 @@ size_t mla_decode_latent_workspace_size(void);
  *   cache        device e4m3 [num_pages, P, 576], pages contiguous (page
  *                stride = P x token stride), token stride a multiple of 16
  *                bytes; positive scales, per token ([num_pages * P] floats) or
- *                one for all.  Pages of a multiple of 8 tokens are read in boxes,
+ *                one for all, from 2^-120 on and those of a sequence within
+ *                2^110 of each other (mla_append_latent's smallest, of a row
+ *                of zeros, is 2^-108.4).  Pages of a multiple of 8 tokens are read in boxes,
  *                others row by row (up to twice as slow)
  *   page_table   device uint32 [B, max_pages], B <= 16384
  *   row_offsets, cache_lens, scale, mask  as in mla_prefill_ragged
@@ -651,8 +653,13 @@ size_t mla_decode_latent_workspace_size(void);
  *   workspace    device, mla_decode_latent_workspace_size() bytes, 256-byte
  *                aligned; its contents before the call do not matter.  Calls
  *                that may overlap on the GPU need distinct workspaces.
- * Sums and softmax statistics are 32-bit; the weights that multiply the cached
- * codes carry seven significant bits and are normalised by their own sum.  A
+ * Sums and softmax statistics are 32-bit.  What multiplies the cached codes, a
+ * key's softmax weight times its scale, is rounded within 2^-8 of itself down to
+ * 2^-10 of the row's largest such product, and below that within 2^-18 of the
+ * largest: random errors of a long tail of small ones cancel, but n keys of one and the
+ * same small weight can together be off by n * 2^-18 of the largest key's part, and
+ * those below 2^-21 of it may drop out of the output.  The sum that normalises
+ * the output counts every key; lse is of unrounded weights.  A
  * query's elements are taken exactly down to 2^-9 of its largest one, smaller
  * ones to 2^-17 of that: next to an element 2^10 times larger they keep seven
  * bits, next to one 2^14 times larger three.

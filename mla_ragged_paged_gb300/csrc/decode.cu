@@ -25,21 +25,25 @@
 // two per row, is reproduced exactly down to 2^-9 of the row's largest value (a bf16
 // value has eight significant bits, each e4m3 term four) and to 2^-17 of it below;
 // its terms are stacked as 2 x rows columns of one product.
-// A weight is e4m3 + e5m2 (seven significant bits, down to 2^-17), two products
-// into one O, and the sum that divides O is of the weights as the products see
-// them, so that a row which hangs on one key is exact.  (lse takes the unrounded
-// sum.)  Sums are fp32, in tensor memory.
+// A weight w is e4m3 + e5m2, two products into one O: within 2^-8 of w where it is
+// at least 2^-6, within 2^-14 below, and nothing from 2^-17 down.  The sum that
+// divides O takes weights from 2^-6 on as the products see them, so that a row which
+// hangs on one key is exact, and smaller ones unrounded: a key with a small scale s_j
+// has a small w and adds little to O, but what it adds to the sum, w / s_j, may
+// be the most of all (a row of zeros is cached with the scale 1e-30 / 448).  (lse takes
+// the sum of all weights unrounded.)  Sums are fp32, in tensor memory.
 //
 // Softmax.  A thread owns one key and a quarter of the rows of the tile, so the key's
 // scale is a scalar of the thread: with y = x + log2(s_j) (log2 units) the weight
 // that multiplies the codes is w_j = 2^(y_j - mu + 7) <= 2^8.5 and the one that
 // is summed is w_j / s_j.  The reference mu of a row rises when a key passes
 // mu + 1.5, to 2 above the tile's maximum, so that random maxima seldom pass
-// again; O is then rescaled in tensor memory.  A weight's error is at most
-// 2^-17, which is 2^-22 of the largest weight or less: 131 072 keys of that size
-// together move a row by less than a part in 32, and when all keys of a tile
-// are below mu - 12 (behind a first token far above the rest, say) mu falls to
-// them.  Whether some key passes is one vote of the warpgroup; the maxima
+// again; O is then rescaled in tensor memory.  The largest weight is 2^4.5 or more
+// when mu is set for it, so a small weight's error of at most 2^-14 is 2^-18 of the
+// largest weight or less.  Those errors cancel in a sum over many keys unless they have
+// one sign, as for keys of equal weight; and when all keys of a tile whose maxima are
+// formed are below mu - 12 (behind a first token far above the rest, say) mu
+// falls to them.  Whether some key passes is one vote of the warpgroup; the maxima
 // themselves (transposed through the warps) are only formed in the first two
 // tiles, in every eighth one and after a change.
 //
@@ -77,6 +81,7 @@ constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
 constexpr float kShift = 7.f;                 // w = 2^(y - mu + kShift)
+constexpr float kSmall = 0x1p-6f;             // weights below it (e4m3's normal numbers end there) are summed unrounded
 constexpr float kRaise = 1.5f;                // mu rises when a key is that far above it,
 constexpr float kDrop = 12.f;                 // and falls when a tile's maximum is that far below it,
 constexpr float kMargin = 2.f;                // in both cases to that far above the maximum
@@ -111,7 +116,7 @@ struct DecodeParams {
   const uint32_t* lens;
   uint32_t* status;
   PartHeader* headers;             // [2 * kMaxCtas]
-  float* part_ml;                  // [slots][3][kMaxRows]: mu, the sum of the weights, and as the products see them
+  float* part_ml;                  // [slots][3][kMaxRows]: mu, the sum of the weights, and the sum that divides O
   float* part_o;                   // [slots][kMaxRows][512]
   float sl2;                       // scale * log2(e)
   uint32_t step_col, step_off;     // kKeys = step_col * P + step_off
@@ -689,10 +694,10 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
         float q0, q1, q2, q3;
         weight_terms(w0, w1, a0, b0, q0, q1);
         weight_terms(w2, w3, a1, b1, q2, q3);
-        lq[i] = fmaf(q0, to_sum, lq[i]);
-        lq[i + 1] = fmaf(q1, to_sum, lq[i + 1]);
-        lq[i + 2] = fmaf(q2, to_sum, lq[i + 2]);
-        lq[i + 3] = fmaf(q3, to_sum, lq[i + 3]);
+        lq[i] = fmaf(w0 >= kSmall ? q0 : w0, to_sum, lq[i]);
+        lq[i + 1] = fmaf(w1 >= kSmall ? q1 : w1, to_sum, lq[i + 1]);
+        lq[i + 2] = fmaf(w2 >= kSmall ? q2 : w2, to_sum, lq[i + 2]);
+        lq[i + 3] = fmaf(w3 >= kSmall ? q3 : w3, to_sum, lq[i + 3]);
         t1[i / 4] = a0 | a1 << 16;
         t2[i / 4] = b0 | b1 << 16;
       }

@@ -443,6 +443,43 @@ def test_decode_value_ranges(lib, q_std, spread, sink):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("spread", [12.0, 20.0, 40.0])
+@pytest.mark.parametrize("n,prior", [([1, 2], [1500, 300]), ([1], [9000]), ([1] * 170, [100] * 170)])
+def test_decode_scales_far_apart(lib, n, prior, spread):
+    """Keys of similar softmax weight whose scales differ by up to 2^80: those with small scales add
+    little to the numerator and all of their weight to the denominator, in row tiles that one CTA takes
+    whole and in joined ones."""
+    d = Decode(n, prior, 20, 64, seed=41, spread=spread, q_std=2.0 ** -spread)
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
+@pytest.mark.parametrize("q_std", [0.0, 1.0])
+@pytest.mark.parametrize("lengths,zeros", [
+    ([2], "late"), ([2], "early"), ([300], "early"), ([300], "late"), ([300], "odd"), ([5000], "odd"), ([5000], "early"),
+    ([5000], "all but one"), ([200] * 160, "odd"), ([200] * 160, "early"), ([70], "all")])
+def test_decode_rows_of_zeros(lib, lengths, zeros, q_std):
+    """Rows of zeros, as the append caches them, among ordinary ones: in an opening key tile that holds
+    nothing else, in later ones, in every one."""
+    from mla_ragged_paged_gb300 import binding
+    d = Decode([1] * len(lengths), [n - 1 for n in lengths], 16, 16, seed=42, q_std=q_std)
+    g = torch.Generator().manual_seed(43)
+    rows = []
+    for n in lengths:
+        x = torch.randn(n, WIDTH, generator=g)
+        zero = {"early": slice(0, (n + 1) // 2), "late": slice(n // 2, n), "odd": slice(1, n, 2), "all": slice(0, n),
+                "all but one": slice(1, n)}[zeros]
+        x[zero] = 0
+        rows.append(x)
+    cache, scales = d.codes.cuda(), d.scales.cuda()
+    ro = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
+    binding.append_latent(cache, scales, torch.cat(rows).to(torch.bfloat16).cuda(), d.table.cuda(), ro,
+                          torch.zeros(len(lengths), dtype=torch.int32, device="cuda"))
+    d.codes, d.scales = cache.cpu(), scales.cpu()
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
 @pytest.mark.parametrize("large", [2.0 ** 8, 2.0 ** 10, 2.0 ** 14])
 def test_decode_query_elements_next_to_a_large_one(lib, large):
     """One element far above the others, in a dim that the cache leaves at zero: the others must
