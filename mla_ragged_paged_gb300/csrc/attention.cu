@@ -1583,8 +1583,6 @@ mla_status_t launch_attention(AttnParams& prm, int dev, int sms, const uint32_t*
   return MLA_OK;
 }
 
-std::atomic<uint32_t> g_test_stall{0};
-
 // Full-context call (buffer_row_offsets == NULL) or one buffer row of a
 // chunked call (with lse).
 // page_table == NULL: K_rope is contiguous, k_rope_pages is [Sk, 64] with row
@@ -1825,7 +1823,7 @@ mla_status_t prefill(const mla_tensor_t* out, const mla_tensor_t* lse, const mla
   prm.page_size = static_cast<uint32_t>(P);
   prm.H = static_cast<uint32_t>(H);
   prm.causal = mask == MLA_MASK_CAUSAL;
-  prm.test_stall = g_test_stall.load(std::memory_order_relaxed);
+  prm.test_stall = test_stall();
   prm.test_delay_ns = test_delay_ns();
   prm.sl2 = scale * 1.4426950408889634f;
   prm.ws = static_cast<uint8_t*>(workspace);
@@ -1892,11 +1890,6 @@ extern "C" mla_status_t mla_prefill_ragged(const mla_tensor_t* out, const mla_te
   if (!page_table) return mla::fail(MLA_ERR_INVALID_ARG, "page_table descriptor is NULL");
   return mla::prefill(out, nullptr, q, nullptr, k_nope, v, k_rope_pages, page_table, 0, row_offsets, cache_lens,
                       nullptr, nullptr, scale, mask, 0u, workspace, workspace_bytes, stream);
-}
-
-extern "C" mla_status_t mla_test_inject_stall(uint32_t enable) {
-  mla::g_test_stall.store(enable ? 1u : 0u, std::memory_order_relaxed);
-  return MLA_OK;
 }
 
 extern "C" mla_status_t mla_prefill_ragged_split(

@@ -123,6 +123,7 @@ struct DecodeParams {
   uint32_t box_rows;               // power of two that divides P, up to 128; 1: row gathers
   uint32_t ctas;                   // of the decode kernel's launch
   uint32_t per_token, causal, Tq, H, B, P, num_pages, max_pages, max_keys;
+  uint32_t test_stall;             // test hook: each CTA's first chunk is never loaded
 };
 
 template <int NR>
@@ -263,6 +264,7 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   const bool boxed = p.box_rows > 1;
   const uint32_t boxes = kKeys / p.box_rows;
   uint32_t tile = 0, bad = 0;
+  uint32_t chunks = 0, ropes = 0;    // copied so far: positions in the two rings
   bool alive = true;
   Segment g;
   while (alive && next_segment<NR>(p, sh, g)) {
@@ -313,7 +315,11 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
         uint64_t* full = c < 4 ? &s.full[at_c.slot] : &s.rope_full[rs];
         uint64_t* empty = c < 4 ? &s.empty[at_c.slot] : &s.rope_empty[rs];
         const uint32_t phase = c < 4 ? at_c.phase : (tile / R::kRopeSlots) & 1u;
-        if (!(alive = mbar_wait(smem_u32(empty), phase ^ 1u, abort))) break;
+        // (The warp goes on or gives up as one: what follows needs all lanes.)
+        if (!(alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty), phase ^ 1u, abort)))) break;
+        if (c < 4) chunks = tile * 4 + c + 1;
+        else ropes = tile + 1;
+        if (p.test_stall && chunks == 1) continue;   // nothing arms this chunk's barrier
         const uint32_t bar = smem_u32(full);
         if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
         __syncwarp();
@@ -332,17 +338,15 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
   if (*abort) {
     // Let the copies still in flight land before the CTA exits.
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 0; i < 3 && i <= tile; ++i)
-      for (uint32_t c = 0; c < 4; ++c) {
-        const Place<NR> at_c(tile - i, c);
-        while (!mbar_try_wait(smem_u32(&s.full[at_c.slot]), at_c.phase))
+    auto landed = [&](uint64_t* full, uint32_t slots, uint32_t copies) {
+      for (uint32_t i = 1; i <= min(slots, copies); ++i) {
+        const uint32_t q = copies - i;
+        while (!mbar_try_wait(smem_u32(&full[q % slots]), (q / slots) & 1u))
           if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
       }
-    for (uint32_t i = 0; i < R::kRopeSlots && i <= tile; ++i) {
-      const uint32_t q = tile - i;
-      while (!mbar_try_wait(smem_u32(&s.rope_full[q % R::kRopeSlots]), (q / R::kRopeSlots) & 1u))
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
-    }
+    };
+    landed(s.full, R::kSlots, chunks);
+    landed(s.rope_full, R::kRopeSlots, ropes);
   }
 }
 
@@ -1198,6 +1202,7 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   p.ro = row_offsets;
   p.lens = cache_lens;
   p.status = status;
+  p.test_stall = test_stall();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.headers = reinterpret_cast<PartHeader*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);

@@ -16,6 +16,7 @@ std::atomic<int> g_num_sms[kMaxDevices];  // 0 = unknown, -1 = unsupported devic
 std::atomic<int> g_smem_set[kMaxDevices][kSmemSlots];
 std::atomic<int> g_regs_ok[kMaxDevices][kSmemSlots];
 
+std::atomic<uint32_t> g_test_stall{0};
 std::atomic<uint32_t> g_test_delay_ns{0};
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -121,9 +122,15 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
   return MLA_OK;
 }
 
+uint32_t test_stall() { return g_test_stall.load(std::memory_order_relaxed); }
 uint32_t test_delay_ns() { return g_test_delay_ns.load(std::memory_order_relaxed); }
 
 }  // namespace mla
+
+extern "C" mla_status_t mla_test_inject_stall(uint32_t enable) {
+  mla::g_test_stall.store(enable ? 1u : 0u, std::memory_order_relaxed);
+  return MLA_OK;
+}
 
 extern "C" mla_status_t mla_test_delay_softmax(uint32_t nanoseconds) {
   if (nanoseconds > 100000u) return mla::fail(MLA_ERR_INVALID_ARG, "delay above 100 us");

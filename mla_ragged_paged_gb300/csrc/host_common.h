@@ -46,7 +46,8 @@ mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int s
 // built with exactly `regs` registers per thread; cached per (device, slot).
 mla_status_t check_registers(const void* func, int regs, int device, int slot);
 
-// What the test hook mla_test_delay_softmax asks of launches.
+// What the test hooks mla_test_inject_stall and mla_test_delay_softmax ask of launches.
+uint32_t test_stall();
 uint32_t test_delay_ns();
 
 }  // namespace mla

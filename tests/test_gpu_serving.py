@@ -677,6 +677,26 @@ def test_decode_impossible_lengths_and_offsets(lib):
             _within(_f64(out)[0], ref[0], tol[0], "out")
 
 
+@pytest.mark.parametrize("heads,P", [(64, 16), (16, 12)])
+def test_decode_wait_timeout_sets_status_and_context_survives(lib, heads, P):
+    """A copy that never comes: the call ends, says so, and the next one is right (64- and 32-row tiles,
+    boxes and row gathers; several tiles a CTA, so that the producer is stopped in mid-ring)."""
+    from mla_ragged_paged_gb300 import binding
+    d = Decode([1] * 60, [3000] * 60, heads, P, seed=66)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.test_inject_stall(True)
+    try:
+        _run_decode(d, status=status)
+        assert int(status) == 0x8
+    finally:
+        binding.test_inject_stall(False)
+    status.zero_()
+    d2 = Decode([1, 1], [700, 40], heads, P, seed=67)
+    out, lse = _run_decode(d2, status=status)
+    assert int(status) == 0
+    _check_decode(d2, out, lse)
+
+
 def test_decode_many_heads(lib):
     d = Decode([1, 2], [70, 300], 1024, 64, seed=65)
     out, lse = _run_decode(d)
