@@ -687,8 +687,8 @@ mla_status_t mla_read_device_status(const void* workspace, uint32_t* status_out,
 /*
  * Test hook for the timeout path (no counterpart on the pages).  While
  * enabled (process-wide), every attention launch leaves the first K group of
- * each CTA's first work item unloaded, and every mla_decode_latent launch the
- * first piece of each CTA's first tile: the UMMA issuers' bounded wait for it
+ * each CTA's first work item unloaded, and every mla_decode_latent and
+ * mla_matmul_fp8 launch the first piece of each CTA's first tile: the UMMA issuers' bounded wait for it
  * runs out (after a few seconds), the kernel winds down every role, waits for
  * its copies in flight, frees tensor memory and sets
  * MLA_DEVICE_STATUS_TIMEOUT in the status word; the output is then incomplete.  The CUDA context

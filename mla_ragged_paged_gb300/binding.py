@@ -746,8 +746,8 @@ def prefill_ragged_noalloc(out, q, k_nope, v, k_rope_pages, page_table, row_offs
 
 
 def test_inject_stall(enable):
-    """mla_test_inject_stall: make attention and latent decode launches run into their wait
-    timeout (tests of the timeout path only)."""
+    """mla_test_inject_stall: make attention, latent decode and fp8 product launches run into their
+    wait timeout (tests of the timeout path only)."""
     _check(load().mla_test_inject_stall(1 if enable else 0))
 
 

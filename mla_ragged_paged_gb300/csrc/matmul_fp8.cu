@@ -54,6 +54,7 @@ struct MatmulParams {
   uint32_t splits;              // tile kernel: CTA pairs that share a tile's K, a cluster
   uint32_t test_delay_ns;       // test hook, where pairs share K: how long the second accumulating warpgroup waits before each block
   uint32_t* status;
+  uint32_t test_stall;          // test hook: each CTA's first blocks are never loaded
 };
 
 // ---------------------------------------------------------------- many tiles
@@ -131,6 +132,7 @@ __device__ void tile_producer(TileSmem& s, const MatmulParams& p, const TilePlac
     for (uint32_t kb = at.kb0; kb < at.kb1; ++kb, ++pos) {
       const uint32_t st = pos % kStages;
       if (!(alive = mbar_wait(smem_u32(&s.empty[st]), ((pos / kStages) & 1u) ^ 1u, abort))) break;
+      if (p.test_stall && pos == 0) continue;   // nothing arms this slot's barrier
       const uint32_t bar = smem_u32(&s.full[st]);
       mbar_arrive_expect_tx(bar, kXBytes + kWBytes);
       const int32_t k = static_cast<int32_t>(kb * kKB);
@@ -494,6 +496,7 @@ __global__ void __launch_bounds__(kThinThreads, 2) matmul_thin_kernel(const __gr
       for (uint32_t kb = kb0; kb < kb1; kb += splits, ++pos) {
         const uint32_t st = pos % kRing;
         if (!mbar_wait(smem_u32(&s.empty[st]), ((pos / kRing) & 1u) ^ 1u, abort)) break;
+        if (p.test_stall && pos == 0) continue;   // nothing arms this slot's barrier
         const uint32_t bar = smem_u32(&s.full[st]);
         mbar_arrive_expect_tx(bar, (128 + MT) * kKB);
         tma_load_2d(smem_u32(s.w[st]), &p.tm_w, bar, static_cast<int32_t>(kb * kKB), static_cast<int32_t>(nt * 128));
@@ -737,6 +740,7 @@ extern "C" mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor
   p.out_f32 = out->dtype == MLA_DTYPE_F32;
   p.status = status;
   p.test_delay_ns = test_delay_ns();
+  p.test_stall = test_stall();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t pairs = (static_cast<uint64_t>(M) + 2 * kTileM - 1) / (2 * kTileM);
   const uint64_t wide = (static_cast<uint64_t>(N) + kTileN - 1) / kTileN;

@@ -277,6 +277,26 @@ def test_matmul_nan_and_infinite_scale_stay_in_their_row(lib, m):
     _check_matmul(out[keep], x[keep], xs[keep], w, ws)
 
 
+@pytest.mark.parametrize("m,n,k", [(48, 640, 8192), (700, 2304, 768), (700, 2048, 4112)])
+def test_matmul_wait_timeout_sets_status_and_context_survives(lib, m, n, k):
+    """A copy that never comes: the call ends, says so, and the next one is right (few tokens, many, and
+    a tile's K shared by a cluster)."""
+    from mla_ragged_paged_gb300 import binding
+    x, xs, w, ws = _matmul_case(m, n, k, 11)
+    out = torch.empty(m, n, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.test_inject_stall(True)
+    try:
+        binding.matmul_fp8(out, x, xs, w, ws, status)
+        assert int(status) == 0x8
+    finally:
+        binding.test_inject_stall(False)
+    status.zero_()
+    binding.matmul_fp8(out, x, xs, w, ws, status)
+    _check_matmul(out, x, xs, w, ws)
+    assert int(status) == 0
+
+
 def test_matmul_no_rows(lib):
     from mla_ragged_paged_gb300 import binding
     x, xs, w, ws = _matmul_case(4, 64, 128, 1)
