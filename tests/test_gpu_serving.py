@@ -297,6 +297,19 @@ def test_matmul_wait_timeout_sets_status_and_context_survives(lib, m, n, k):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 300, 384), (200, 300, 384), (700, 2048, 4112)])
+def test_matmul_infinite_and_nan_scales_stay_in_their_rows(lib, m, n, k):
+    """A row's scale that is infinite or NaN, in each kernel, makes that row not finite and no other."""
+    from mla_ragged_paged_gb300 import binding
+    x, xs, w, ws = _matmul_case(m, n, k, 10)
+    xs[1, 2], xs[2, 0] = float("inf"), float("nan")
+    out = torch.empty(m, n, device="cuda")
+    binding.matmul_fp8(out, x, xs, w, ws)
+    assert not torch.isfinite(out[1]).any() and torch.isnan(out[2]).all()
+    keep = [0] + list(range(3, m))
+    _check_matmul(out[keep], x[keep], xs[keep], w, ws)
+
+
 def test_matmul_no_rows(lib):
     from mla_ragged_paged_gb300 import binding
     x, xs, w, ws = _matmul_case(4, 64, 128, 1)
