@@ -552,7 +552,8 @@ mla_status_t mla_gather_up_project(const mla_tensor_t* k_out, const mla_tensor_t
  *   out = bf16(y);  out_scales[r, g] = max(amax over columns 128 g .. 128 g +
  *   127 of |y|, 1e-30) / 448,  out_fp8 = e4m3(y / out_scales)
  * h, its mean square and y are 32-bit: y does not pass through the rounding
- * of residual_out.  A row with a NaN gives NaN scales and codes.
+ * of residual_out.  A row with a NaN gives NaN scales and codes; a finite one
+ * whose sum of squares exceeds float32 gives zeros.
  *   x             device bf16 [rows, D], 1 <= D <= 32768
  *   residual      device bf16 [rows, D] or NULL
  *   residual_out  device bf16 [rows, D] (written) or NULL; needs residual
@@ -584,8 +585,10 @@ mla_status_t mla_rms_norm(const mla_tensor_t* out, const mla_tensor_t* out_fp8,
  *   w_scales  device float32 [ceil(N / 128), ceil(K / 128)], any strides >= 0
  *   status    device uint32 or NULL: MLA_DEVICE_STATUS_TIMEOUT is ORed in if a
  *             pipeline wait of the kernel gives up
- * Rows of x and w start 16-byte aligned.  Every sum is 32-bit; one rounding,
- * of the output.  The result does not depend on timing (no atomics).
+ * Rows of x and w start 16-byte aligned (products of many tokens are faster where
+ * they start 128-byte aligned).  Every sum is 32-bit; one rounding, of the output.
+ * A block's two scales are multiplied first, in float32: their product should be
+ * a normal number.  The result does not depend on timing (no atomics).
  */
 mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor_t* x,
                             const mla_tensor_t* x_scales, const mla_tensor_t* w,
@@ -612,8 +615,9 @@ mla_status_t mla_matmul_fp8(const mla_tensor_t* out, const mla_tensor_t* x,
  *                _BAD_COLUMN into *status
  * Slots no new token lands on keep their contents.  Two tokens of one call
  * must not land on the same slot (sequences that share a page they both append
- * to); which one stays would be undefined.  The rope columns and the scales
- * are what the fp8 prefill calls take as a paged K_rope.  One launch.
+ * to): the slot would hold pieces of both, with the scale of either.  The rope
+ * columns and the scales are what the fp8 prefill calls take as a paged K_rope.  One
+ * launch.
  */
 mla_status_t mla_append_latent(const mla_tensor_t* cache, const mla_tensor_t* rows,
                                const mla_tensor_t* page_table, const uint32_t* row_offsets,

@@ -19,7 +19,9 @@
 // (no barrier); wider rows, and few rows of more than 256 columns, a block each, which
 // walks the rows and, where the registers allow, reads the next one while it finishes
 // the current one.  Measured, residual and codes: 16384 x 8192 in 160 us = 5.9 TB/s,
-// 100000 x 1024 in 116 us = 6.2 TB/s (HBM); 1 x 8192 in 3.0 us (launch).
+// 100000 x 1024 in 116 us = 6.2 TB/s (HBM); 1 x 8192 in 3.0 us (launch).  By
+// single elements: 16384 x 8191 in 360 us = 2.6 TB/s, 16384 x 1023 in 44 us = 2.7 TB/s,
+// 1 x 8191 in 4.6 us (one or two bytes an access: HBM at 31 %, issue slots at 49 %).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -69,7 +71,8 @@ __device__ __forceinline__ void widen(float (&v)[8], uint4 u) {
 // bounds to what lets two blocks in: they read the weights anew for every row (they
 // stay in L1) and, but for one form, no row ahead.  (16384 rows, us with one block an
 // SM / two: 4608 columns 124 / 92, 6144 138 / 129, 8192 164 / 160, 10240 262 / 193,
-// 12288 286 / 220, 16384 338 / 295, 20480 533 / 383.)  From 24577 columns on a second
+// 12288 286 / 220, 16384 338 / 295, 20480 533 / 383, although threads of four chunks
+// spill up to 192 bytes for it.)  From 24577 columns on a second
 // block has no registers left.
 __host__ __device__ constexpr bool two_blocks(int ch, int threads) {
   return threads != 32 && threads <= 768 && (ch > 1 || threads > 512);

@@ -135,6 +135,19 @@ def test_norm_in_place_zero_and_nan_rows(lib, dim):
     assert torch.isnan(scales[2]).all() and torch.isnan(codes[2].float()).all() and torch.isnan(x[2]).all()
 
 
+@pytest.mark.parametrize("dim", [256, 3000, 3001])
+def test_norm_sum_of_squares_past_float32_gives_zeros(lib, dim):
+    from mla_ragged_paged_gb300 import binding
+    x, r, w = _norm_case(3, dim, 6)
+    x[1, 5] = 1e20
+    out = torch.empty_like(r)
+    codes = torch.empty(3, dim, dtype=E4M3, device="cuda")
+    scales = torch.empty(3, -(-dim // 128), device="cuda")
+    binding.rms_norm(x, w, 1e-6, out=out, out_fp8=codes, out_scales=scales)
+    assert (out[1].float() == 0).all() and (codes[1].float() == 0).all() and (scales[1] > 0).all()
+    _check_norm(x[::2], None, w, 1e-6, out[::2], codes[::2], scales[::2], None)
+
+
 def test_norm_no_rows(lib):
     from mla_ragged_paged_gb300 import binding
     x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
