@@ -53,6 +53,7 @@ typedef enum {
   MLA_DTYPE_FP8_E4M3 = 1, /* float8_e4m3fn: no infinities, 0x7F/0xFF are NaN */
   MLA_DTYPE_U32 = 2,
   MLA_DTYPE_F32 = 3,
+  MLA_DTYPE_BYTES = 4, /* rows of a 4-bit latent cache, see mla_append_latent_fp4 */
 } mla_dtype_t;
 
 typedef enum {
@@ -676,6 +677,127 @@ mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse,
                                const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
                                mla_mask_t mask, uint32_t* status, void* workspace,
                                size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * ---- The 4-bit latent cache, and what comes before it ----
+ * (No counterpart on the reference pages.)  As the 8-bit serving step with half
+ * the cache: mla_norm_rope of the queries' rope dims and of the new latent rows,
+ * mla_append_latent_fp4, then mla_decode_latent_fp4 for new tokens or, for a
+ * prompt over cached contexts, mla_gather_latent_fp4 to e4m3 rows with a scale
+ * each, mla_matmul_fp8 with the up-projection weights and the prefill calls
+ * with a contiguous K_rope.
+ *
+ * A cached row of W elements (W a multiple of 64, up to 1024) is
+ * mla_latent_fp4_row_bytes(W) bytes:
+ *   [0, W / 2)          e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5,
+ *                       1, 1.5, 2, 3, 4, 6), element 2 i in the low half of byte i
+ *   W / 2               E, the row's exponent; 255: every element is NaN
+ *   [W / 2 + 1, + W / 64)  the shifts of its blocks of 32 elements, 0 .. 14, block
+ *                       2 i in the low half of byte i
+ *   the rest            zeros, up to a multiple of 16 bytes (304 for W = 576)
+ * Element k is e2m1(code_k) * 2^(E - 127 - shift[k / 32]).  Every step of the
+ * format is a power of two, so all conversions below are exact but the one to
+ * e2m1.  A cache is a tensor [num_pages, P, row bytes] of dtype MLA_DTYPE_BYTES;
+ * it starts 16-byte aligned and its strides are multiples of 16 bytes.
+ */
+
+/* Bytes of a cached row: W / 2 + W / 64 + 1 rounded up to 16; 0 where W is not
+ * a multiple of 64 from 64 to 1024. */
+size_t mla_latent_fp4_row_bytes(uint32_t width);
+
+/*
+ * Norm and position rotation of each head's queries and keys, in one pass.
+ * For every row x [D] (a token t and a head) of q, and likewise of k:
+ *   y[0:Dn] = x[0:Dn] * weight / sqrt(mean of x[0:Dn]^2 + eps),  y[Dn:D] = x[Dn:D]
+ *   out[0 : D - R] = y[0 : D - R], and of the last R = 2 * len(inv_freq) columns
+ *   pair i, (u, v) of y with a = positions[t] * inv_freq[i], becomes
+ *   rope_scale * (u cos a - v sin a, u sin a + v cos a)
+ * Pair i is columns D - R + 2 i and the one after it; with MLA_ROPE_HALVES columns
+ * D - R + i and D - R / 2 + i.  Dn is the weight's length, R inv_freq's twice: MLA's latent
+ * row [c_kv 512 | k_rope 64] has Dn = 512 and R = 64, whole heads Dn = D, rope
+ * dims alone (a view of the columns, no weight) R = D = 64.
+ *   q, q_out   device bf16 [T, Hq, D], 1 <= D <= 1024, or both NULL
+ *   k, k_out   device bf16 [T, Hk, Dk], or both NULL (not both pairs)
+ *   q_weight, k_weight  device bf16 or float32 [Dn], 1 <= Dn <= D, or NULL: no norm
+ *   eps        finite, >= 0
+ *   positions  device uint32 [T], any value; NULL without inv_freq
+ *   inv_freq   device float32 [R / 2], 0 < R <= D and Dk, or NULL: no rotation (then
+ *              q and k need weights)
+ *   rope_scale finite (an attention factor of the frequencies' scaling, else 1)
+ *   flags      0 or MLA_ROPE_HALVES
+ * Norms, angles and rotations are 32-bit with one rounding, of the output; an
+ * angle's part beyond whole turns is exact to 2^-24 of a turn at any position, for
+ * inv_freq as given and up to 256 in magnitude (an infinity or NaN gives NaNs).  A row
+ * whose sum of squares exceeds float32 gives zeros in [0, Dn).
+ * Inputs may have any strides, outputs any under which no two of their elements share memory; rows
+ * that all start 16-byte aligned, with D, Dn and R multiples of 8 (16 for R with
+ * MLA_ROPE_HALVES), take wide accesses.  An output may be the same view as its
+ * input (in place).  One launch.
+ */
+#define MLA_ROPE_HALVES 0x1u
+mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tensor_t* q, const mla_tensor_t* q_weight,
+                           const mla_tensor_t* k_out, const mla_tensor_t* k, const mla_tensor_t* k_weight,
+                           float eps, const uint32_t* positions, const mla_tensor_t* inv_freq, float rope_scale,
+                           uint32_t flags, mla_stream_t stream);
+
+/*
+ * Append of new latent rows to a paged 4-bit cache.  Row row_offsets[b] + i of
+ * `rows` becomes context token a = cache_lens[b] + i of sequence b, at
+ * cache[page_table[b, a / P], a % P, :].  With amax_j the largest magnitude of
+ * block j and e_j the least integer with amax_j <= 7 * 2^e_j:
+ *   E - 127 = max over j of e_j, held to -100 .. 125
+ *   shift_j = E - 127 - e_j, held to 0 .. 14
+ *   code_k  = e2m1(row_k / 2^(E - 127 - shift)), to nearest, ties to even, at most 6
+ * (a negative value that rounds to 0 keeps its sign).  So a block holds its values to
+ * within a sixth of the largest or better, unless the block is 2^14 below the
+ * row's largest.  A row with a NaN or an infinity becomes E = 255 and zeros.
+ *   cache        device bytes [num_pages, P, mla_latent_fp4_row_bytes(W)] (written)
+ *   rows         device bf16 [Tq, W], 16-byte aligned rows
+ *   page_table   device uint32 [B, max_pages]
+ *   row_offsets, cache_lens, status  as in mla_append_latent
+ * Slots no new token lands on keep their contents.  Two tokens of one call
+ * must not land on the same slot.  One launch.
+ */
+mla_status_t mla_append_latent_fp4(const mla_tensor_t* cache, const mla_tensor_t* rows,
+                                   const mla_tensor_t* page_table, const uint32_t* row_offsets,
+                                   const uint32_t* cache_lens, uint32_t* status, mla_stream_t stream);
+
+/*
+ * Rows of a paged 4-bit cache read back into a contiguous buffer, as
+ * mla_gather_rows: for every sequence b and 0 <= i < buffer_row_offsets[b+1] -
+ * buffer_row_offsets[b], with a = cache_offsets[b] + i, buffer row
+ * buffer_row_offsets[b] + i receives cache[page_table[b, a / P], a % P].
+ *   dst    device bf16 [rows, W]: the elements' values (exact); or
+ *          device e4m3 [rows, W] with one scale a row (scale_gran
+ *          MLA_SCALE_PER_TOKEN, [rows] floats, written although the
+ *          descriptor's pointer is const): codes e2m1 * 2^(6 - shift) and the scale
+ *          2^(E - 133), exact; what mla_matmul_fp8 (column stride 0 of x_scales)
+ *          and the fp8 prefill calls' contiguous K_rope take.  A row with E = 255
+ *          gets NaN codes and a NaN scale.
+ *          16-byte aligned rows; written for positions < min(rows,
+ *          buffer_row_offsets[B]) only, from buffer_row_offsets[0] on
+ *   cache  device bytes [num_pages, P, mla_latent_fp4_row_bytes(W)]
+ *   page_table, buffer_row_offsets, cache_offsets, status  as in mla_gather_rows
+ * One launch.
+ */
+mla_status_t mla_gather_latent_fp4(const mla_tensor_t* dst, const mla_tensor_t* cache,
+                                   const mla_tensor_t* page_table, const uint32_t* buffer_row_offsets,
+                                   const uint32_t* cache_offsets, uint32_t* status, mla_stream_t stream);
+
+/*
+ * mla_decode_latent over a paged 4-bit cache: c_j is the row that
+ * mla_gather_latent_fp4 reads back.
+ *   cache        device bytes [num_pages, P, 304]; any strides under which no rows
+ *                overlap.  Rows as mla_append_latent_fp4 writes them, those of
+ *                a sequence with exponents E within 110 of each other
+ *   workspace    device, mla_decode_latent_workspace_size() bytes
+ * Everything else, the precision included, as in mla_decode_latent.
+ */
+mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                                   const mla_tensor_t* cache, const mla_tensor_t* page_table,
+                                   const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
+                                   mla_mask_t mask, uint32_t* status, void* workspace,
+                                   size_t workspace_bytes, mla_stream_t stream);
 
 /* Device status bits written into the workspace's first uint32. */
 #define MLA_DEVICE_STATUS_BAD_PAGE 0x1u    /* page id >= num_pages */

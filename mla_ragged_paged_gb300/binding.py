@@ -14,11 +14,12 @@ import torch
 from .buildlib import LIB_PATH
 
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA = 0, 1, 2, 3
-MLA_DTYPE_BF16, MLA_DTYPE_FP8_E4M3, MLA_DTYPE_U32, MLA_DTYPE_F32 = 0, 1, 2, 3
+MLA_DTYPE_BF16, MLA_DTYPE_FP8_E4M3, MLA_DTYPE_U32, MLA_DTYPE_F32, MLA_DTYPE_BYTES = 0, 1, 2, 3, 4
 MLA_MASK_CAUSAL, MLA_MASK_NULL = 0, 1
 MLA_SCALE_NONE, MLA_SCALE_PER_TENSOR, MLA_SCALE_PER_TOKEN = 0, 1, 2
 MLA_CHUNK_ACCUMULATE = 0x1
 MLA_FP8_PRECISE = 0x2
+MLA_ROPE_HALVES = 0x1
 STATUS_BITS = {0x1: "BAD_PAGE", 0x2: "BAD_COLUMN", 0x4: "BAD_OFFSETS", 0x8: "TIMEOUT"}
 
 # Names exported by the C ABI (kept in step with include/mla_prefill.h).
@@ -30,7 +31,8 @@ EXPORTS = ["mla_prefill_plan", "mla_prefill_plan_max_rows", "mla_prefill_ragged_
            "mla_prefill_ragged_chunk_contiguous", "mla_gather_rows", "mla_up_project",
            "mla_gather_up_project",
            "mla_prefill_ragged_split", "mla_rms_norm", "mla_matmul_fp8", "mla_append_latent",
-           "mla_decode_latent_workspace_size", "mla_decode_latent", "mla_test_inject_stall", "mla_test_delay_softmax",
+           "mla_decode_latent_workspace_size", "mla_decode_latent", "mla_latent_fp4_row_bytes", "mla_norm_rope",
+           "mla_append_latent_fp4", "mla_gather_latent_fp4", "mla_decode_latent_fp4", "mla_test_inject_stall", "mla_test_delay_softmax",
            "mla_read_device_status",
            "mla_last_error_string"]
 
@@ -117,6 +119,17 @@ def load(path=LIB_PATH):
     lib.mla_decode_latent.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, ctypes.c_int, vp, vp,
                                       ctypes.c_size_t, vp]
     lib.mla_decode_latent.restype = ctypes.c_int
+    lib.mla_latent_fp4_row_bytes.argtypes = [u32]
+    lib.mla_latent_fp4_row_bytes.restype = ctypes.c_size_t
+    lib.mla_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, ctypes.c_float, u32, vp]
+    lib.mla_norm_rope.restype = ctypes.c_int
+    lib.mla_append_latent_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.mla_append_latent_fp4.restype = ctypes.c_int
+    lib.mla_gather_latent_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.mla_gather_latent_fp4.restype = ctypes.c_int
+    lib.mla_decode_latent_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, ctypes.c_int, vp, vp,
+                                          ctypes.c_size_t, vp]
+    lib.mla_decode_latent_fp4.restype = ctypes.c_int
     lib.mla_read_device_status.argtypes = [vp, ctypes.POINTER(u32), vp]
     lib.mla_read_device_status.restype = ctypes.c_int
     lib.mla_last_error_string.argtypes = []
@@ -524,6 +537,7 @@ _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
+_BYTES = (torch.uint8,)
 _INDEX = (torch.int32, torch.uint32)
 
 
@@ -647,6 +661,16 @@ def alloc_decode_workspace(device="cuda"):
     return torch.empty(decode_workspace_size(), dtype=torch.uint8, device=device)
 
 
+def _decode_workspace(workspace, device, stream):
+    if workspace is None:
+        # From the launch stream's pool: its memory is not reused before the call is done.
+        with torch.cuda.stream(stream):
+            return alloc_decode_workspace(device)
+    if not workspace.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
+    return workspace
+
+
 def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, scale,
                   mask=MLA_MASK_CAUSAL, workspace=None, lse=None, status=None, stream=None):
     """mla_decode_latent: attention of new tokens (q [Tq, H, 576], absorbed
@@ -654,12 +678,7 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
     scales ([num_pages, P], or one float); out [Tq, H, 512] stays in the latent
     space, lse [Tq, H] is optional."""
     dev = _device_of(out, q, cache, cache_scales, page_table, row_offsets, cache_lens, workspace, lse, status)
-    if workspace is None:
-        # From the launch stream's pool: its memory is not reused before the call is done.
-        with torch.cuda.stream(stream):
-            workspace = alloc_decode_workspace(q.device)
-    elif not workspace.is_contiguous():
-        raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
+    workspace = _decode_workspace(workspace, q.device, stream)
     B = page_table.shape[0]
     _check(load().mla_decode_latent(_operand(out, "out", _BF16, MLA_DTYPE_BF16), _operand(lse, "lse", _F32, MLA_DTYPE_F32),
                                     _operand(q, "q", _BF16, MLA_DTYPE_BF16), _latent_cache(cache, cache_scales, True),
@@ -668,6 +687,91 @@ def decode_latent(out, q, cache, cache_scales, page_table, row_offsets, cache_le
                                     _indices(cache_lens, "cache_lens", B), scale, int(mask), _status_word(status),
                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                     _raw_stream(stream, dev)))
+    return out
+
+
+def norm_rope(positions, inv_freq, q=None, q_out=None, q_weight=None, k=None, k_out=None, k_weight=None, eps=1e-6,
+              rope_scale=1.0, interleaved=True, stream=None):
+    """mla_norm_rope: per head RMS norm of the first len(weight) columns of q
+    [T, Hq, D] and k [T, Hk, Dk] (bf16; no weight: no norm) and rotation of the last
+    2 * len(inv_freq) columns by positions[t] * inv_freq[i], as neighbouring pairs or,
+    with interleaved=False, as halves.  positions and inv_freq may both be None (norm
+    alone); an output may be its input.  Returns the outputs given."""
+    dev = _device_of(q, q_out, q_weight, k, k_out, k_weight, positions, inv_freq)
+    tokens = q if q is not None else k
+    if tokens is None or tokens.dim() != 3:
+        raise MlaError(MLA_ERR_INVALID_ARG, "q and k must be [T, H, D], one of them at least")
+    at = None if positions is None else _indices(positions, "positions", tokens.shape[0])
+    _check(load().mla_norm_rope(_operand(q_out, "q_out", _BF16, MLA_DTYPE_BF16), _operand(q, "q", _BF16, MLA_DTYPE_BF16),
+                                None if q_weight is None else _operand(q_weight, "q_weight", _BF16_F32, _bf16_or_f32(q_weight)),
+                                _operand(k_out, "k_out", _BF16, MLA_DTYPE_BF16), _operand(k, "k", _BF16, MLA_DTYPE_BF16),
+                                None if k_weight is None else _operand(k_weight, "k_weight", _BF16_F32, _bf16_or_f32(k_weight)),
+                                eps, at, _operand(inv_freq, "inv_freq", _F32, MLA_DTYPE_F32), rope_scale,
+                                0 if interleaved else MLA_ROPE_HALVES, _raw_stream(stream, dev)))
+    return tuple(t for t in (q_out, k_out) if t is not None)
+
+
+def latent_fp4_row_bytes(width):
+    """Bytes of a 4-bit cached row of `width` elements."""
+    n = int(load().mla_latent_fp4_row_bytes(int(width))) if 0 < width < 1 << 32 else 0
+    if not n:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"row width must be a multiple of 64 up to 1024 (got {width})")
+    return n
+
+
+def append_latent_fp4(cache, rows, page_table, row_offsets, cache_lens, status=None, stream=None):
+    """mla_append_latent_fp4: bf16 rows [Tq, W] quantised into the paged 4-bit cache
+    [num_pages, P, latent_fp4_row_bytes(W)] (uint8), at context positions
+    cache_lens[b] + i."""
+    dev = _device_of(cache, rows, page_table, row_offsets, cache_lens, status)
+    B = page_table.shape[0]
+    _check(load().mla_append_latent_fp4(_operand(cache, "cache", _BYTES, MLA_DTYPE_BYTES),
+                                        _operand(rows, "rows", _BF16, MLA_DTYPE_BF16),
+                                        _operand(page_table, "page_table", _INDEX, MLA_DTYPE_U32),
+                                        _indices(row_offsets, "row_offsets", B + 1),
+                                        _indices(cache_lens, "cache_lens", B), _status_word(status),
+                                        _raw_stream(stream, dev)))
+    return cache
+
+
+def gather_latent_fp4(dst, cache, page_table, buffer_row_offsets, cache_offsets, dst_scales=None, status=None,
+                      stream=None):
+    """mla_gather_latent_fp4: dst[bro[b] + i] = 4-bit cache row of context token co[b] + i of
+    sequence b, as bf16 values [rows, W] or as e4m3 codes with one float a row in
+    dst_scales [rows]."""
+    dev = _device_of(dst, cache, page_table, buffer_row_offsets, cache_offsets, dst_scales, status)
+    B = page_table.shape[0]
+    if dst_scales is None:
+        d_dst = _operand(dst, "dst (without dst_scales)", _BF16, MLA_DTYPE_BF16)
+    else:
+        _typed(dst, "dst (with dst_scales)", *_FP8)
+        _typed(dst_scales, "dst_scales", torch.float32)
+        if dst_scales.numel() != dst.shape[0] or not dst_scales.is_contiguous():
+            raise MlaError(MLA_ERR_INVALID_ARG, "dst_scales must be a packed [rows]")
+        d_dst = _pack(dst, MLA_DTYPE_FP8_E4M3, dst_scales.data_ptr(), MLA_SCALE_PER_TOKEN)
+    _check(load().mla_gather_latent_fp4(d_dst, _operand(cache, "cache", _BYTES, MLA_DTYPE_BYTES),
+                                        _operand(page_table, "page_table", _INDEX, MLA_DTYPE_U32),
+                                        _indices(buffer_row_offsets, "buffer_row_offsets", B + 1),
+                                        _indices(cache_offsets, "cache_offsets", B), _status_word(status),
+                                        _raw_stream(stream, dev)))
+    return dst
+
+
+def decode_latent_fp4(out, q, cache, page_table, row_offsets, cache_lens, scale, mask=MLA_MASK_CAUSAL, workspace=None,
+                      lse=None, status=None, stream=None):
+    """mla_decode_latent_fp4: decode_latent over the paged 4-bit latent cache
+    [num_pages, P, 304] (uint8) that append_latent_fp4 writes."""
+    dev = _device_of(out, q, cache, page_table, row_offsets, cache_lens, workspace, lse, status)
+    workspace = _decode_workspace(workspace, q.device, stream)
+    B = page_table.shape[0]
+    _check(load().mla_decode_latent_fp4(_operand(out, "out", _BF16, MLA_DTYPE_BF16), _operand(lse, "lse", _F32, MLA_DTYPE_F32),
+                                        _operand(q, "q", _BF16, MLA_DTYPE_BF16),
+                                        _operand(cache, "cache", _BYTES, MLA_DTYPE_BYTES),
+                                        _operand(page_table, "page_table", _INDEX, MLA_DTYPE_U32),
+                                        _indices(row_offsets, "row_offsets", B + 1),
+                                        _indices(cache_lens, "cache_lens", B), scale, int(mask), _status_word(status),
+                                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                        _raw_stream(stream, dev)))
     return out
 
 

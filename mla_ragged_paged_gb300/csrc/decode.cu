@@ -1107,42 +1107,25 @@ mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStre
 }
 
 }  // namespace
-}  // namespace mla
 
-extern "C" size_t mla_decode_latent_workspace_size(void) { return mla::kWorkspace; }
-
-extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
-                                          const mla_tensor_t* cache, const mla_tensor_t* page_table,
-                                          const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
-                                          mla_mask_t mask, uint32_t* status, void* workspace,
-                                          size_t workspace_bytes, mla_stream_t stream) {
-  using namespace mla;
+mla_status_t check_decode_operands(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                                   const mla_tensor_t* page_table, const uint32_t* row_offsets, const uint32_t* cache_lens,
+                                   float scale, mla_mask_t mask, const uint32_t* status, const void* workspace,
+                                   size_t workspace_bytes) {
   mla_status_t st;
   if ((st = check_tensor(out, "out", 3, MLA_DTYPE_BF16, true)) != MLA_OK) return st;
   if ((st = check_tensor(q, "q", 3, MLA_DTYPE_BF16, true)) != MLA_OK) return st;
-  if ((st = check_tensor(cache, "cache", 3, MLA_DTYPE_FP8_E4M3)) != MLA_OK) return st;
   if ((st = check_tensor(page_table, "page_table", 2, MLA_DTYPE_U32)) != MLA_OK) return st;
   if (!row_offsets || !cache_lens) return fail(MLA_ERR_INVALID_ARG, "row_offsets / cache_lens is NULL");
   if (!aligned4(page_table->data) || !aligned4(row_offsets) || !aligned4(cache_lens) || !aligned4(status))
     return fail(MLA_ERR_INVALID_ARG, "page_table, row_offsets, cache_lens and status must be 4-byte aligned");
   const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
-  const int64_t NP = cache->shape[0], P = cache->shape[1];
   if (q->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "q must be [Tq, H, %d]", kWidth);
   if (out->shape[0] != Tq || out->shape[1] != H || out->shape[2] != kLatent)
     return fail(MLA_ERR_INVALID_ARG, "out must be [Tq, H, %d] matching q", kLatent);
-  if (cache->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "cache must be [num_pages, P, %d]", kWidth);
-  if (!cache->scale || (cache->scale_gran != MLA_SCALE_PER_TOKEN && cache->scale_gran != MLA_SCALE_PER_TENSOR))
-    return fail(MLA_ERR_INVALID_ARG, "cache needs per-token or per-tensor scales");
-  if (!aligned4(cache->scale)) return fail(MLA_ERR_INVALID_ARG, "cache scales must be 4-byte aligned");
   if (Tq * H > 0x7FFFFFFFll) return fail(MLA_ERR_INVALID_ARG, "q exceeds 2^31 rows");
   if (H < 1 || H > 1024) return fail(MLA_ERR_INVALID_ARG, "heads must be 1..1024");
   if (B < 1 || B > 16384 || page_table->shape[1] < 1) return fail(MLA_ERR_INVALID_ARG, "batch must be 1..16384 with a page-table column");
-  if (NP < 1 || P < 1) return fail(MLA_ERR_INVALID_ARG, "empty cache");
-  if (NP * P > 0x7FFFFFFFll) return fail(MLA_ERR_INVALID_ARG, "cache exceeds 2^31 rows");
-  if (cache->stride[0] != P * cache->stride[1] && NP > 1)
-    return fail(MLA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = P x token stride)");
-  if (!aligned16(cache->data) || cache->stride[1] % 16 != 0 || cache->stride[1] < kWidth || cache->stride[1] >= (1ll << 40))
-    return fail(MLA_ERR_INVALID_ARG, "cache must start 16-byte aligned with a 16-byte-multiple token stride >= %d", kWidth);
   if (!aligned16(q->data) || (q->stride[0] * 2) % 16 != 0 || (q->stride[1] * 2) % 16 != 0)
     return fail(MLA_ERR_INVALID_ARG, "q must start 16-byte aligned with 16-byte-multiple strides");
   if (!aligned16(out->data) || (out->stride[0] * 2) % 16 != 0 || (out->stride[1] * 2) % 16 != 0)
@@ -1167,6 +1150,36 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
   if (workspace_bytes < mla_decode_latent_workspace_size())
     return fail(MLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, %zu needed", workspace_bytes,
                 mla_decode_latent_workspace_size());
+  return MLA_OK;
+}
+
+}  // namespace mla
+
+extern "C" size_t mla_decode_latent_workspace_size(void) { return mla::kWorkspace; }
+
+extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                                          const mla_tensor_t* cache, const mla_tensor_t* page_table,
+                                          const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
+                                          mla_mask_t mask, uint32_t* status, void* workspace,
+                                          size_t workspace_bytes, mla_stream_t stream) {
+  using namespace mla;
+  mla_status_t st;
+  if ((st = check_tensor(cache, "cache", 3, MLA_DTYPE_FP8_E4M3)) != MLA_OK) return st;
+  if ((st = check_decode_operands(out, lse, q, page_table, row_offsets, cache_lens, scale, mask, status, workspace,
+                                  workspace_bytes)) != MLA_OK)
+    return st;
+  const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
+  const int64_t NP = cache->shape[0], P = cache->shape[1];
+  if (cache->shape[2] != kWidth) return fail(MLA_ERR_INVALID_ARG, "cache must be [num_pages, P, %d]", kWidth);
+  if (!cache->scale || (cache->scale_gran != MLA_SCALE_PER_TOKEN && cache->scale_gran != MLA_SCALE_PER_TENSOR))
+    return fail(MLA_ERR_INVALID_ARG, "cache needs per-token or per-tensor scales");
+  if (!aligned4(cache->scale)) return fail(MLA_ERR_INVALID_ARG, "cache scales must be 4-byte aligned");
+  if (NP < 1 || P < 1) return fail(MLA_ERR_INVALID_ARG, "empty cache");
+  if (NP * P > 0x7FFFFFFFll) return fail(MLA_ERR_INVALID_ARG, "cache exceeds 2^31 rows");
+  if (cache->stride[0] != P * cache->stride[1] && NP > 1)
+    return fail(MLA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = P x token stride)");
+  if (!aligned16(cache->data) || cache->stride[1] % 16 != 0 || cache->stride[1] < kWidth || cache->stride[1] >= (1ll << 40))
+    return fail(MLA_ERR_INVALID_ARG, "cache must start 16-byte aligned with a 16-byte-multiple token stride >= %d", kWidth);
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   if (Tq == 0) return MLA_OK;

@@ -38,13 +38,23 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
 // (device, slot): each kernel needs a slot of its own (0 plan, 1 scheduler,
 // 2 / 3 / 4 attention bf16 / fp8 / fp8 with per-token K scales, 6 / 7 the last
 // two with two-term precision, 5 up-projection, 8 / 12 fp8 product, 9 .. 11 its
-// form for few tokens, 13 / 14 latent decode).
+// form for few tokens, 13 / 14 latent decode, 15 norm
+// and rotation).
 constexpr int kSmemSlots = 16;
 mla_status_t set_max_dynamic_smem(const void* func, int bytes, int device, int slot);
 
 // A kernel that moves registers between its warps (setmaxnreg) may only run as
 // built with exactly `regs` registers per thread; cached per (device, slot).
 mla_status_t check_registers(const void* func, int regs, int device, int slot);
+
+// What a 4-bit cache [num_pages, P, row bytes] has to keep: alignment, and rows apart.
+mla_status_t check_fp4_cache(const mla_tensor_t* cache);
+
+// What mla_decode_latent and mla_decode_latent_fp4 ask of everything but their caches.
+mla_status_t check_decode_operands(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                                   const mla_tensor_t* page_table, const uint32_t* row_offsets, const uint32_t* cache_lens,
+                                   float scale, mla_mask_t mask, const uint32_t* status, const void* workspace,
+                                   size_t workspace_bytes);
 
 // What the test hooks mla_test_inject_stall and mla_test_delay_softmax ask of launches.
 uint32_t test_stall();
