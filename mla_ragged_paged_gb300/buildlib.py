@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["host_common.cpp", "plan.cu", "attention.cu", "merge.cu", "gather.cu", "upproj.cu",
-           "norm.cu", "append.cu", "matmul_fp8.cu", "decode.cu", "latent_fp4.cu", "norm_rope.cu", "decode_fp4.cu"]
+           "norm.cu", "append.cu", "matmul_fp8.cu", "decode.cu", "latent_fp4.cu", "norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
          "-diag-suppress", "177"]

@@ -61,8 +61,10 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "host_common.h"
+#include "latent_fp4.cuh"
 #include "sm103.cuh"
 
 namespace mla {
@@ -77,6 +79,10 @@ constexpr int kGroups = 4;                    // softmax warpgroups
 constexpr int kSoftmaxWarps = 4 * kGroups;
 constexpr int kDecThreads = 128 + 128 * kGroups;  // producer and three UMMA issuers before them
 constexpr int kDecRegs = 96;
+// 4-bit cache: eight warps more, which turn its rows into e4m3 codes.
+constexpr int kDequantWarps = 8;
+constexpr int kDec4Threads = kDecThreads + 32 * kDequantWarps;
+constexpr int kDec4Regs = 72;
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
@@ -110,6 +116,8 @@ struct DecodeParams {
   const uint16_t* q;
   long long q_tok, q_head;
   const float* scales;
+  const uint8_t* rows4;            // 4-bit cache: its rows, read without tensor maps
+  long long page_bytes, tok_bytes;
   const uint32_t* page_table;
   long long pt_stride;
   const uint32_t* ro;
@@ -155,6 +163,16 @@ struct __align__(1024) DecodeSmem {
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
+// 4-bit cache: the keys' exponents, and the e4m3 forms of a block's codes.
+constexpr uint32_t kExponentSlots = 3;
+constexpr uint8_t kNoKey = 254;               // in the place of an exponent: past the context, or on a bad page
+template <int NR>
+struct DecodeSmem4 : DecodeSmem<NR> {
+  uint2 table[16];
+  uint8_t key_e[kExponentSlots][kKeys];
+};
+static_assert(sizeof(DecodeSmem4<64>) <= 232448, "decode shared memory");
+static_assert(sizeof(DecodeSmem4<32>) <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem<64>) + 1024 <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem<32>) + 1024 <= 232448, "decode shared memory");
 
@@ -549,8 +567,8 @@ __device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& first
       : "r"(seen));
 }
 
-template <int NR>
-__device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
+template <int NR, bool FP4>
+__device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem<NR>>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
   using R = Rows<NR>;
   constexpr int N = R::kCols;
@@ -577,21 +595,26 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
     // The key's scale is two dependent reads away (page table, scale): the page
     // is read two tiles ahead and the scale one tile ahead, so that neither is
     // waited for.
+    // (4-bit cache: the warps that make the codes leave the exponent.)
     KeyWalk walk(p, g.kt0 * kKeys + key);
     auto scale_of = [&](uint32_t page, uint32_t off, float& sc) {
       const bool ok = page < p.num_pages;
       sc = ok ? __ldg(p.scales + (p.per_token ? page * p.P + off : 0u)) : 1.f;
       return ok;
     };
-    const uint32_t page_first = walk.page(p, g.b, g.kt0 * kKeys + key < end), off_first = walk.off;
-    walk.next(p);
-    uint32_t page_after = walk.page(p, g.b, (g.kt0 + 1) * kKeys + key < end), off_after = walk.off;   // (a tile past kt1 is read, not used)
-    walk.next(p);
+    uint32_t page_first = 0, off_first = 0, page_after = 0, off_after = 0;
+    if constexpr (!FP4) {
+      page_first = walk.page(p, g.b, g.kt0 * kKeys + key < end), off_first = walk.off;
+      walk.next(p);
+      page_after = walk.page(p, g.b, (g.kt0 + 1) * kKeys + key < end), off_after = walk.off;   // (a tile past kt1 is read, not used)
+      walk.next(p);
+    }
     // ---- queries.  The previous segment's products with the old ones are
     // done: this warp has seen its last score tile.
     load_queries<NR>(s, p, g, tid);
-    float sc_next;
-    bool ok_next = scale_of(page_first, off_first, sc_next);
+    float sc_next = 1.f;
+    bool ok_next = true;
+    if constexpr (!FP4) ok_next = scale_of(page_first, off_first, sc_next);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
@@ -602,17 +625,28 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = lq[i] = 0.f;
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
-      const float sc = sc_next;
-      const bool ok = ok_next;
-      ok_next = scale_of(page_after, off_after, sc_next);
-      page_after = walk.page(p, g.b, (kt + 2) * kKeys + key < end);
-      off_after = walk.off;
-      walk.next(p);
+      float sc = sc_next, ls;
+      bool ok = ok_next;
       const uint32_t j = kt * kKeys + key;
-      const float ls = __log2f(fmaxf(sc, 0x1p-120f));    // NaN and 0 give finite factors; the score carries the NaN
-      const float to_sum = ex2_approx(-kShift - kSumShift - ls);
+      if constexpr (!FP4) {
+        ok_next = scale_of(page_after, off_after, sc_next);
+        page_after = walk.page(p, g.b, (kt + 2) * kKeys + key < end);
+        off_after = walk.off;
+        walk.next(p);
+        ls = __log2f(fmaxf(sc, 0x1p-120f));              // NaN and 0 give finite factors; the score carries the NaN
+      }
       // ---- scores
       softmax_wait(smem_u32(&s.s_full[tile & 1]), (tile >> 1) & 1u, abort);
+      if constexpr (FP4) {
+        const Place<NR> at(tile, 0);                     // (complete long ago: orders this thread after its exponent)
+        softmax_wait(smem_u32(&s.full[at.slot]), at.phase, abort);
+        const uint32_t e = s.key_e[tile % kExponentSlots][key];
+        ok = e != kNoKey;
+        // The codes are in units of 2^(E - 133).
+        sc = e == kFp4NanE ? __uint_as_float(0x7FC00000u) : __uint_as_float((max(e, 13u) - 6u) << 23);
+        ls = static_cast<float>(static_cast<int>(max(e, 13u)) - 133);
+      }
+      const float to_sum = ex2_approx(-kShift - kSumShift - ls);
       tc_fence_after();
       float y[N];
       {
@@ -735,7 +769,7 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
           *reinterpret_cast<uint4*>(row + R::kPTerm + ((group ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
         }
       }
-      if (group == 0 && (!ok || partial)) {
+      if (!FP4 && group == 0 && (!ok || partial)) {
         // A weight of 0 times a NaN code would be NaN: a key no row sees, or one
         // some rows do not see and that holds a NaN, becomes zeros.  (Rows that
         // see the NaN have NaN weights already: the scores read the same codes.)
@@ -861,27 +895,173 @@ __device__ void decode_softmax(DecodeSmem<NR>& s, const DecodeParams& p, Share s
   }
 }
 
+// ------------------------------------------------------------ 4-bit rows to codes
+// The rows of a CTA's tiles, one key of each tile: a page-table entry is read two
+// tiles before the row itself.
+struct RowWalk {
+  Share sh;
+  Segment g;
+  uint32_t kt, key;
+  KeyWalk walk;
+  uint32_t page, off;      // of the tile that the last step came to; kNoPage: no such key
+  __device__ __forceinline__ RowWalk(const DecodeParams& p, const Share& share, uint32_t key_)
+      : sh(share), kt(0), key(key_), walk(p, 0), page(kNoPage), off(0) {
+    g.kt1 = 0;
+  }
+  template <int NR>
+  __device__ __forceinline__ bool step(const DecodeParams& p) {
+    if (kt == g.kt1) {
+      if (!next_segment<NR>(p, sh, g)) return false;
+      kt = g.kt0;
+      walk = KeyWalk(p, kt * kKeys + key);
+    }
+    page = walk.page(p, g.b, kt * kKeys + key < g.s.keys);
+    off = walk.off;
+    walk.next(p);
+    ++kt;
+    return true;
+  }
+};
+
+// Warp w takes keys 16 w .. 16 w + 15 of a tile, chunk by chunk (128 dims, four
+// blocks): lane l block l % 4 of keys 16 w + l / 4 and 8 further, so that eight lanes'
+// 16-byte stores fall into different banks.  A block's 32 codes are 16 bytes and become 32.
+// What a chunk holds of the next tile is loaded as soon as its registers are free.
 template <int NR>
-__global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+__device__ void dequantise(DecodeSmem4<NR>& s, const DecodeParams& p, const Share& sh, uint32_t w, uint32_t lane,
+                           volatile uint32_t* abort) {
   using R = Rows<NR>;
-  extern __shared__ uint8_t smem_raw[];
-  DecodeSmem<NR>& s = *reinterpret_cast<DecodeSmem<NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t j = lane & 3u, near = w * 16 + (lane >> 2);   // keys near, near + 8
+  const uint32_t mine = j & 1u;                                // which of them this lane walks
+  RowWalk it(p, sh, near + 8 * mine);
+  uint32_t bad = 0;
+  auto address = [&]() -> const uint8_t* {
+    if (it.page == kNoPage) return nullptr;
+    if (it.page >= p.num_pages) {
+      bad = MLA_DEVICE_STATUS_BAD_PAGE;
+      return nullptr;
+    }
+    return p.rows4 + it.page * p.page_bytes + it.off * p.tok_bytes;
+  };
+  struct Rows2 {
+    const uint8_t* at[2];
+  };
+  auto both = [&](const uint8_t* own) {
+    const uint8_t* other = reinterpret_cast<const uint8_t*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own), 1));
+    Rows2 r;
+    r.at[0] = mine ? other : own;
+    r.at[1] = mine ? own : other;
+    return r;
+  };
+  auto load16 = [](const uint8_t* at) { return at ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0u, 0u, 0u, 0u); };
+  constexpr uint32_t kNone = 0x01010101u * kNoKey;
+  uint4 raw[4][2], raw_rope, meta[2];
+  auto load_chunk = [&](const Rows2& r, int c) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) raw[c][e] = load16(r.at[e] ? r.at[e] + c * 64 + j * 16 : nullptr);
+  };
+  auto load_rope = [&](const Rows2& r) {
+    const uint8_t* at = j >> 1 ? r.at[1] : r.at[0];
+    raw_rope = load16(at ? at + kLatent / 2 + (j & 1u) * 16 : nullptr);
+  };
+  auto load_meta = [&](const Rows2& r) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) meta[e] = r.at[e] ? __ldg(reinterpret_cast<const uint4*>(r.at[e] + kWidth / 2)) : make_uint4(kNone, 0u, 0u, 0u);
+  };
+  bool alive = it.template step<NR>(p);
+  if (!alive) return;
+  Rows2 rows = both(address());
+  bool more = it.template step<NR>(p);
+  load_meta(rows);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) load_chunk(rows, c);
+  load_rope(rows);
+  for (uint32_t tile = 0; alive; ++tile) {
+    // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
+    uint32_t lo[2], hi[2], e_byte[2], rope_shift;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t from = 8 + 4 * j;
+      lo[e] = __funnelshift_r(meta[e].x, meta[e].y, from);
+      hi[e] = __funnelshift_r(meta[e].y, meta[e].z, from);
+      e_byte[e] = meta[e].x & 255u;
+    }
+    rope_shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
+    // The next tile's rows (their page was read a tile ago), and the page of the one behind it.
+    const bool next = more;
+    if (next) {
+      rows = both(address());
+      more = it.template step<NR>(p);
+      load_meta(rows);
+    }
+#pragma unroll
+    for (int c = 0; c < 5; ++c) {
+      const Place<NR> at_c(tile, c);
+      const uint32_t rs = tile % R::kRopeSlots;
+      uint64_t* full = c < 4 ? &s.full[at_c.slot] : &s.rope_full[rs];
+      uint64_t* empty = c < 4 ? &s.empty[at_c.slot] : &s.rope_empty[rs];
+      const uint32_t phase = c < 4 ? at_c.phase : (tile / R::kRopeSlots) & 1u;
+      if (!(alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty), phase ^ 1u, abort)))) break;
+      if (c == 0 && j < 2) {
+        s.key_e[tile % kExponentSlots][near + 8 * j] = static_cast<uint8_t>(j ? e_byte[1] : e_byte[0]);
+      }
+      auto convert = [&](const uint4& v, uint32_t shift, uint8_t* row, uint32_t col, uint32_t swz) {
+        const uint2 t = s.table[shift];
+        const Fp4Table tab = {t.x, t.y};
+        const uint2 a = fp4_to_e4m3(v.x, tab), b = fp4_to_e4m3(v.y, tab), d = fp4_to_e4m3(v.z, tab), f = fp4_to_e4m3(v.w, tab);
+        *reinterpret_cast<uint4*>(row + ((col ^ swz) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(row + (((col + 1) ^ swz) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+      };
+      if (c < 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t key = near + 8 * e, shift = (c < 2 ? lo[e] : hi[e]) >> (16 * (c & 1)) & 15u;
+          convert(raw[c & 3][e], shift, s.chunk[at_c.slot] + key * 128, 2 * j, key & 7u);
+        }
+        if (next) load_chunk(rows, c & 3);
+      } else {
+        const uint32_t key = near + 8 * (j >> 1);
+        convert(raw_rope, rope_shift, s.rope[rs] + key * 64, 2 * (j & 1u), (key >> 1) & 3u);
+        if (next) load_rope(rows);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (p.test_stall && tile == 0 && c == 0) continue;   // nothing completes this chunk's barrier
+      if (lane == 0) mbar_arrive(smem_u32(full));
+    }
+    alive = alive && next;
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 0 && bad && p.status) atomicOr(p.status, bad);
+}
+
+template <int NR, bool FP4>
+__global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+  using R = Rows<NR>;
+  using Smem = std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem<NR>>;
+  constexpr int kThreads = FP4 ? kDec4Threads : kDecThreads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (FP4 && (smem_u32(smem_raw) & 1023u)) {  // (no room is left to round up)
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile uint32_t* abort = &s.abort_flag;
   // Scratch of the prologue, in the place of the queries.
   struct Prologue {
-    unsigned long long warp_sum[kDecThreads / 32];
+    unsigned long long warp_sum[kThreads / 32];
     Share start;
   };
   Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (uint32_t i = 0; i < R::kSlots; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.full[i]), FP4 ? kDequantWarps : 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (uint32_t i = 0; i < R::kRopeSlots; ++i) {
-      mbar_init(smem_u32(&s.rope_full[i]), 1);
+      mbar_init(smem_u32(&s.rope_full[i]), FP4 ? kDequantWarps : 1);
       mbar_init(smem_u32(&s.rope_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -893,15 +1073,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
     mbar_init(smem_u32(&s.pv_done), 2);        // both output issuers
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     fence_barrier_init();
-    tma_prefetch_desc(&p.tm_latent);
-    tma_prefetch_desc(&p.tm_rope);
+    if constexpr (!FP4) {
+      tma_prefetch_desc(&p.tm_latent);
+      tma_prefetch_desc(&p.tm_rope);
+    }
+  }
+  if constexpr (FP4) {
+    if (threadIdx.x >= 32 && threadIdx.x < 48) {
+      const Fp4Table t = fp4_table(threadIdx.x - 32);
+      s.table[threadIdx.x - 32] = make_uint2(t.lo, t.hi);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&s.tmem_base), 512);
     tmem_relinquish();
   }
   // ---- this CTA's share: prefix sums of the sequences' steps
-  const uint32_t per = (p.B + kDecThreads - 1) / kDecThreads;
+  const uint32_t per = (p.B + kThreads - 1) / kThreads;
   const uint32_t b0 = min(p.B, threadIdx.x * per), b1 = min(p.B, b0 + per);
   auto steps_of = [](const Seq& q) {
     return q.key_tiles ? static_cast<unsigned long long>(q.row_tiles) * (kStartSteps + q.key_tiles) : 0ull;
@@ -928,7 +1116,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   unsigned long long before = 0, steps = 0;
-  for (int w = 0; w < kDecThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += pro.warp_sum[w];
     steps += pro.warp_sum[w];
   }
@@ -959,18 +1147,32 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   Share sh = {};
   if (u0 < u1) sh = pro.start;
   __syncthreads();     // the scratch becomes query space
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
+  auto issue = [&] {
     if (warp > 0 && elect_one()) {
       if (warp == 1) issue_scores<NR>(s, p, sh, tmem, abort);
       else issue_output<NR>(s, p, sh, tmem, 2 * (warp - 2), abort);
       drain_umma(&s.drain[warp - 1]);
     }
     __syncwarp();
+  };
+  if constexpr (FP4) {
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+      issue();
+    } else if (warp < 4 + kSoftmaxWarps) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");  // 128 x 40 + 512 x 88 + 256 x 56 = 896 x 72
+      decode_softmax<NR, true>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      dequantise<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
+    }
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
+    issue();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");  // 128 x 64 + 512 x 104 = 640 x 96
-    decode_softmax<NR>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+    decode_softmax<NR, false>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   }
   tc_fence_before();
   __syncthreads();
@@ -1083,16 +1285,16 @@ constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 25
 constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 3 * kMaxRows;
 constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * kLatent;
 
-template <int NR>
+template <int NR, bool FP4>
 mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStream_t stream) {
-  const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR>);
-  const int smem = static_cast<int>(sizeof(DecodeSmem<NR>) + 1024);
+  const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR, FP4>);
+  const int smem = static_cast<int>(FP4 ? sizeof(DecodeSmem4<NR>) : sizeof(DecodeSmem<NR>) + 1024);
   mla_status_t st;
-  if ((st = check_registers(kernel, kDecRegs, dev, slot)) != MLA_OK) return st;
+  if ((st = check_registers(kernel, FP4 ? kDec4Regs : kDecRegs, dev, slot)) != MLA_OK) return st;
   if ((st = set_max_dynamic_smem(kernel, smem, dev, slot)) != MLA_OK) return st;
   const uint32_t ctas = std::min<uint32_t>(static_cast<uint32_t>(sms), kMaxCtas);
   p.ctas = ctas;
-  decode_kernel<NR><<<ctas, kDecThreads, smem, stream>>>(p);
+  decode_kernel<NR, FP4><<<ctas, FP4 ? kDec4Threads : kDecThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
   // Row tiles: each sequence's last one may be partial.  (us with a block / a warp per
@@ -1104,6 +1306,42 @@ mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStre
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
   return MLA_OK;
+}
+
+// The parameters that do not depend on the cache's form.
+void fill_params(DecodeParams& p, const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                 const mla_tensor_t* cache, const mla_tensor_t* page_table, const uint32_t* row_offsets,
+                 const uint32_t* cache_lens, float scale, mla_mask_t mask, uint32_t* status, void* workspace) {
+  p.out = static_cast<uint16_t*>(out->data);
+  p.o_tok = out->stride[0];
+  p.o_head = out->stride[1];
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.l_tok = lse ? lse->stride[0] : 0;
+  p.l_head = lse ? lse->stride[1] : 0;
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.q_tok = q->stride[0];
+  p.q_head = q->stride[1];
+  p.page_table = static_cast<const uint32_t*>(page_table->data);
+  p.pt_stride = page_table->stride[0];
+  p.ro = row_offsets;
+  p.lens = cache_lens;
+  p.status = status;
+  p.test_stall = test_stall();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.headers = reinterpret_cast<PartHeader*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + kMlBytes);
+  p.sl2 = scale * 1.4426950408889634f;
+  p.causal = mask == MLA_MASK_CAUSAL;
+  p.Tq = static_cast<uint32_t>(q->shape[0]);
+  p.H = static_cast<uint32_t>(q->shape[1]);
+  p.B = static_cast<uint32_t>(page_table->shape[0]);
+  p.P = static_cast<uint32_t>(cache->shape[1]);
+  p.num_pages = static_cast<uint32_t>(cache->shape[0]);
+  p.max_pages = static_cast<uint32_t>(page_table->shape[1]);
+  p.max_keys = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(p.P) * p.max_pages, 0x7FFFFF00ull));
+  p.step_col = kKeys / p.P;
+  p.step_off = kKeys % p.P;
 }
 
 }  // namespace
@@ -1199,46 +1437,46 @@ extern "C" mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_ten
                            CU_TENSOR_MAP_SWIZZLE_64B, "cache")) != MLA_OK)
       return st;
   }
-  p.out = static_cast<uint16_t*>(out->data);
-  p.o_tok = out->stride[0];
-  p.o_head = out->stride[1];
-  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
-  p.l_tok = lse ? lse->stride[0] : 0;
-  p.l_head = lse ? lse->stride[1] : 0;
-  p.q = static_cast<const uint16_t*>(q->data);
-  p.q_tok = q->stride[0];
-  p.q_head = q->stride[1];
+  fill_params(p, out, lse, q, cache, page_table, row_offsets, cache_lens, scale, mask, status, workspace);
   p.scales = cache->scale;
   p.per_token = cache->scale_gran == MLA_SCALE_PER_TOKEN;
-  p.page_table = static_cast<const uint32_t*>(page_table->data);
-  p.pt_stride = page_table->stride[0];
-  p.ro = row_offsets;
-  p.lens = cache_lens;
-  p.status = status;
-  p.test_stall = test_stall();
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.headers = reinterpret_cast<PartHeader*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
-  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + kMlBytes);
-  p.sl2 = scale * 1.4426950408889634f;
-  p.causal = mask == MLA_MASK_CAUSAL;
-  p.Tq = static_cast<uint32_t>(Tq);
-  p.H = static_cast<uint32_t>(H);
-  p.B = static_cast<uint32_t>(B);
-  p.P = static_cast<uint32_t>(P);
-  p.num_pages = static_cast<uint32_t>(NP);
-  p.max_pages = static_cast<uint32_t>(page_table->shape[1]);
-  p.max_keys = static_cast<uint32_t>(std::min<uint64_t>(static_cast<uint64_t>(P) * p.max_pages, 0x7FFFFF00ull));
   // One box of as many rows as divide a page; pages without a multiple of the
   // swizzle's eight rows take row gathers (measured, 64 sequences of
   // 4500 with 64 heads: 62 us in boxes, 128 us in gathers).
-  p.step_col = kKeys / p.P;
-  p.step_off = kKeys % p.P;
   p.box_rows = static_cast<uint32_t>(box_rows);
   // 32-row tiles where an average sequence's queries fit one (us in tiles of 32 / 64,
   // 64 sequences of 4500 with 16 heads 49 / 61, 32 heads 50 / 62, 40 heads 78 / 62,
   // 128 heads 141 / 108).
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return rows <= 32 ? launch_decode<32>(p, dev, sms, 13, s) : launch_decode<64>(p, dev, sms, 14, s);
+  return rows <= 32 ? launch_decode<32, false>(p, dev, sms, 13, s) : launch_decode<64, false>(p, dev, sms, 14, s);
+}
+
+extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla_tensor_t* lse, const mla_tensor_t* q,
+                                              const mla_tensor_t* cache, const mla_tensor_t* page_table,
+                                              const uint32_t* row_offsets, const uint32_t* cache_lens, float scale,
+                                              mla_mask_t mask, uint32_t* status, void* workspace,
+                                              size_t workspace_bytes, mla_stream_t stream) {
+  using namespace mla;
+  mla_status_t st;
+  if ((st = check_tensor(cache, "cache", 3, MLA_DTYPE_BYTES)) != MLA_OK) return st;
+  if (cache->shape[2] != fp4_row_bytes(kWidth))
+    return fail(MLA_ERR_INVALID_ARG, "cache must be [num_pages, P, %u] bytes", fp4_row_bytes(kWidth));
+  if ((st = check_fp4_cache(cache)) != MLA_OK) return st;
+  if ((st = check_decode_operands(out, lse, q, page_table, row_offsets, cache_lens, scale, mask, status, workspace,
+                                  workspace_bytes)) != MLA_OK)
+    return st;
+  int dev = 0, sms = 0;
+  if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
+  const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
+  if (Tq == 0) return MLA_OK;
+  DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  fill_params(p, out, lse, q, cache, page_table, row_offsets, cache_lens, scale, mask, status, workspace);
+  p.rows4 = static_cast<const uint8_t*>(cache->data);
+  p.page_bytes = cache->stride[0];
+  p.tok_bytes = cache->stride[1];
+  const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return rows <= 32 ? launch_decode<32, true>(p, dev, sms, 16, s) : launch_decode<64, true>(p, dev, sms, 17, s);
 }
