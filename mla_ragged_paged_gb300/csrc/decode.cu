@@ -108,7 +108,9 @@ struct PartHeader {
 };
 
 struct DecodeParams {
-  CUtensorMap tm_latent, tm_rope;  // cache rows [slots, 576]; boxes 128 x box_rows and 64 x box_rows
+  // Cache rows [slots, 576]; boxes 128 x box_rows and 64 x box_rows.  4-bit: rows of 304 bytes, boxes of a chunk's
+  // codes and of what is behind the last (the rope dims', the exponent, the shifts), 64 bytes each.
+  CUtensorMap tm_latent, tm_rope;
   uint16_t* out;
   long long o_tok, o_head;
   float* lse;
@@ -116,8 +118,6 @@ struct DecodeParams {
   const uint16_t* q;
   long long q_tok, q_head;
   const float* scales;
-  const uint8_t* rows4;            // 4-bit cache: its rows, read without tensor maps
-  long long page_bytes, tok_bytes;
   const uint32_t* page_table;
   long long pt_stride;
   const uint32_t* ro;
@@ -134,7 +134,7 @@ struct DecodeParams {
   uint32_t test_stall;             // test hook: each CTA's first chunk is never loaded
 };
 
-template <int NR>
+template <int NR, bool FP4>
 struct Rows {
   static constexpr int kCols = NR / kGroups;      // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
@@ -143,12 +143,15 @@ struct Rows {
   static constexpr uint32_t kPBytes = kKeys * 2 * NR;
   static constexpr uint32_t kPTerm = NR == 64 ? kKeys * 64 : 32;  // bytes from the first term to the second
   // What fits: 8 latent chunks are two tiles.
-  static constexpr uint32_t kSlots = NR <= 32 ? 10 : 8, kRopeSlots = NR <= 32 ? 2 : 1;
+  static constexpr uint32_t kSlots = FP4 ? (NR <= 32 ? 8 : 6) : NR <= 32 ? 10 : 8;
+  static constexpr uint32_t kRopeSlots = !FP4 && NR <= 32 ? 2 : 1;
+  // 4-bit cache: chunks of codes as they are cached, and the tiles' rope codes and shifts.
+  static constexpr uint32_t kRawSlots = NR <= 32 ? 4 : 3, kRawTails = 1;
 };
 
 template <int NR>
-struct __align__(1024) DecodeSmem {
-  using R = Rows<NR>;
+struct __align__(1024) DecodeSmem8 {
+  using R = Rows<NR, false>;
   uint8_t chunk[R::kSlots][kChunk];
   uint8_t rope[R::kRopeSlots][kRopeBytes];
   uint8_t q[4][R::kQChunk];
@@ -163,18 +166,41 @@ struct __align__(1024) DecodeSmem {
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
-// 4-bit cache: the keys' exponents, and the e4m3 forms of a block's codes.
-constexpr uint32_t kExponentSlots = 3;
+// 4-bit cache.
+constexpr uint32_t kRow4Bytes = fp4_row_bytes(kWidth);
+// A tile's chunk of cached codes, and its rows' tails: 48 bytes and 16 past the row, which arrive as zeros (copies
+// of four rows have to begin 128-byte aligned).
+constexpr uint32_t kTailRow = 64, kRawChunk = kKeys * 64, kRawTail = kKeys * kTailRow;
 constexpr uint8_t kNoKey = 254;               // in the place of an exponent: past the context, or on a bad page
 template <int NR>
-struct DecodeSmem4 : DecodeSmem<NR> {
-  uint2 table[16];
-  uint8_t key_e[kExponentSlots][kKeys];
+struct __align__(1024) DecodeSmem4 {
+  using R = Rows<NR, true>;
+  uint8_t chunk[R::kSlots][kChunk];
+  uint8_t rope[R::kRopeSlots][kRopeBytes];
+  uint8_t q[4][R::kQChunk];
+  uint8_t q_rope[2 * NR * 64];
+  uint8_t p[R::kPBytes];
+  uint8_t raw[R::kRawSlots][kRawChunk];
+  uint8_t raw_tail[R::kRawTails][kRawTail];
+  float warp_red[kGroups][4][R::kCols];
+  float row_val[kGroups][R::kCols];
+  float col_factor[NR];
+  uint2 table[16];                            // the e4m3 forms of a block's codes, by its shift
+  uint8_t key_e[2][kKeys];                    // the keys' exponents
+  uint64_t full[R::kSlots], empty[R::kSlots];
+  uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
+  uint64_t raw_full[R::kRawSlots], raw_empty[R::kRawSlots];
+  uint64_t tail_full[R::kRawTails], tail_empty[R::kRawTails];
+  uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain[3];
+  uint32_t tmem_base;
+  uint32_t abort_flag;
 };
+template <int NR, bool FP4>
+using DecodeSmem = std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem8<NR>>;
 static_assert(sizeof(DecodeSmem4<64>) <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem4<32>) <= 232448, "decode shared memory");
-static_assert(sizeof(DecodeSmem<64>) + 1024 <= 232448, "decode shared memory");
-static_assert(sizeof(DecodeSmem<32>) + 1024 <= 232448, "decode shared memory");
+static_assert(sizeof(DecodeSmem8<64>) + 1024 <= 232448, "decode shared memory");
+static_assert(sizeof(DecodeSmem8<32>) + 1024 <= 232448, "decode shared memory");
 
 // ------------------------------------------------------------ the work's order
 struct RawSeq {
@@ -265,20 +291,24 @@ struct KeyWalk {
 };
 
 // Ring place of latent chunk c of a tile.
-template <int NR>
+template <int NR, bool FP4>
 struct Place {
   uint32_t slot, phase;
   __device__ __forceinline__ Place(uint32_t tile, uint32_t c) {
     const uint32_t pos = tile * 4 + c;
-    slot = pos % Rows<NR>::kSlots;
-    phase = (pos / Rows<NR>::kSlots) & 1u;
+    slot = pos % Rows<NR, FP4>::kSlots;
+    phase = (pos / Rows<NR, FP4>::kSlots) & 1u;
   }
 };
 
 // ------------------------------------------------------------ producer
-template <int NR>
-__device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
-  using R = Rows<NR>;
+// 8-bit: chunks and rope dims of the codes that the tensor cores read.  4-bit: first the tile's
+// tails (rope codes, exponents, shifts), then its chunks, all as they are cached.
+template <int NR, bool FP4>
+__device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
+  using R = Rows<NR, FP4>;
+  constexpr uint32_t kBodyBytes = FP4 ? kRawChunk : kChunk, kTailBytes = FP4 ? kRawTail : kRopeBytes;
+  constexpr uint32_t kBodyStep = FP4 ? 64 : 128, kBodySlots = FP4 ? R::kRawSlots : R::kSlots, kTailSlots = FP4 ? R::kRawTails : R::kRopeSlots;
   const bool boxed = p.box_rows > 1;
   const uint32_t boxes = kKeys / p.box_rows;
   uint32_t tile = 0, bad = 0;
@@ -324,30 +354,41 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
         // from now; into L2 the rows can come at once (measured: 118 -> 108 us
         // for 152 sequences x 4500 x 64 heads).
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, rows[0]);
-        tma_prefetch_2d(&p.tm_rope, kLatent, rows[0]);
+        for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * kBodyStep, rows[0]);
+        tma_prefetch_2d(&p.tm_rope, 4 * kBodyStep, rows[0]);
       }
-      for (int c = 0; c < 5 && alive; ++c) {
-        const Place<NR> at_c(tile, c);
-        const uint32_t rs = tile % R::kRopeSlots;
-        uint64_t* full = c < 4 ? &s.full[at_c.slot] : &s.rope_full[rs];
-        uint64_t* empty = c < 4 ? &s.empty[at_c.slot] : &s.rope_empty[rs];
-        const uint32_t phase = c < 4 ? at_c.phase : (tile / R::kRopeSlots) & 1u;
+      for (int i = 0; i < 5 && alive; ++i) {
+        const int c = FP4 ? (i + 4) % 5 : i;   // 4: the tail
+        const uint32_t pos = c < 4 ? tile * 4 + c : tile, ring = c < 4 ? kBodySlots : kTailSlots;
+        const uint32_t slot = pos % ring, phase = (pos / ring) & 1u;
+        uint64_t *full, *empty;
+        uint32_t dst;
+        if constexpr (FP4) {
+          full = c < 4 ? &s.raw_full[slot] : &s.tail_full[slot];
+          empty = c < 4 ? &s.raw_empty[slot] : &s.tail_empty[slot];
+          dst = c < 4 ? smem_u32(s.raw[slot]) : smem_u32(s.raw_tail[slot]);
+        } else {
+          full = c < 4 ? &s.full[slot] : &s.rope_full[slot];
+          empty = c < 4 ? &s.empty[slot] : &s.rope_empty[slot];
+          dst = c < 4 ? smem_u32(s.chunk[slot]) : smem_u32(s.rope[slot]);
+        }
         // (The warp goes on or gives up as one: what follows needs all lanes.)
         if (!(alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty), phase ^ 1u, abort)))) break;
-        if (c < 4) chunks = tile * 4 + c + 1;
-        else ropes = tile + 1;
-        if (p.test_stall && chunks == 1) continue;   // nothing arms this chunk's barrier
+        if (p.test_stall && tile == 0 && c == 0) {   // nothing arms this chunk's barrier
+          chunks = 1;
+          continue;
+        }
+        if (c < 4) chunks = pos + 1;
+        else ropes = pos + 1;
         const uint32_t bar = smem_u32(full);
-        if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kChunk : kRopeBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kBodyBytes : kTailBytes);
         __syncwarp();
-        const uint32_t dst = c < 4 ? smem_u32(s.chunk[at_c.slot]) : smem_u32(s.rope[rs]);
-        const uint32_t row_bytes = c < 4 ? 128u : 64u;
+        const uint32_t row_bytes = c < 4 ? kBodyBytes / kKeys : kTailBytes / kKeys;
         const CUtensorMap* map = c < 4 ? &p.tm_latent : &p.tm_rope;
         if (!boxed)
-          tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
+          tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * kBodyStep, rows[0], rows[1], rows[2], rows[3]);
         else if (lane < boxes)
-          tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * 128, rows[0]);
+          tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * kBodyStep, rows[0]);
       }
     }
   }
@@ -363,8 +404,13 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
           if (global_timer_ns() - t0 > kWaitTimeoutNs) break;
       }
     };
-    landed(s.full, R::kSlots, chunks);
-    landed(s.rope_full, R::kRopeSlots, ropes);
+    if constexpr (FP4) {
+      landed(s.raw_full, kBodySlots, chunks);
+      landed(s.tail_full, kTailSlots, ropes);
+    } else {
+      landed(s.full, kBodySlots, chunks);
+      landed(s.rope_full, kTailSlots, ropes);
+    }
   }
 }
 
@@ -373,9 +419,9 @@ __device__ void decode_producer(DecodeSmem<NR>& s, const DecodeParams& p, Share 
 // dims.  One UMMA takes its thread about 50 cycles to issue, and twice that
 // beside two softmax warps on the same scheduler, against 48 to 64 cycles of
 // tensor time: one thread could keep the tensor cores half busy.
-template <int NR>
-__device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
-  using R = Rows<NR>;
+template <int NR, bool FP4>
+__device__ void issue_scores(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, uint32_t tmem, volatile uint32_t* abort) {
+  using R = Rows<NR, FP4>;
   const uint32_t id_s = make_idesc(128, 2 * NR, 0, false);
   const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0])), q_desc = sw128_desc_at(smem_u32(s.q[0]));
   uint32_t tile = 0, segs = 0;
@@ -387,22 +433,29 @@ __device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
       const uint32_t par = tile & 1, phase = (tile >> 1) & 1u;
       if (!mbar_wait(smem_u32(&s.s_empty[par]), phase ^ 1u, abort)) return;
       const uint32_t d = tmem + kColS + par * (2 * NR);
+      auto rope_part = [&] {
+        const uint32_t st = tile % R::kRopeSlots;
+        if (!mbar_wait(smem_u32(&s.rope_full[st]), (tile / R::kRopeSlots) & 1u, abort)) return false;
+        if constexpr (FP4) fence_proxy_async_smem();   // for the warps that wrote the codes
+        tc_fence_after();
+        const uint64_t kd = sw64_desc_at(smem_u32(s.rope[st])), qd = sw64_desc_at(smem_u32(s.q_rope));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, FP4 ? k != 0 : 1u);
+        umma_commit(smem_u32(&s.rope_empty[st]));
+        return true;
+      };
+      if (FP4 && !rope_part()) return;                 // (the 4-bit rows' tails come first)
 #pragma unroll 1
       for (uint32_t c = 0; c < 4; ++c) {
-        const Place<NR> at(tile, c);
+        const Place<NR, FP4> at(tile, c);
         if (!mbar_wait(smem_u32(&s.full[at.slot]), at.phase, abort)) return;
+        if constexpr (FP4) fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t kd = chunk_desc + at.slot * (kChunk >> 4), qd = q_desc + c * (R::kQChunk >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, (c | k) != 0);
+        for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, FP4 || (c | k) != 0);
       }
-      const uint32_t st = tile % R::kRopeSlots;
-      if (!mbar_wait(smem_u32(&s.rope_full[st]), (tile / R::kRopeSlots) & 1u, abort)) return;
-      tc_fence_after();
-      const uint64_t kd = sw64_desc_at(smem_u32(s.rope[st])), qd = sw64_desc_at(smem_u32(s.q_rope));
-#pragma unroll
-      for (int k = 0; k < 2; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, 1u);
-      umma_commit(smem_u32(&s.rope_empty[st]));
+      if (!FP4 && !rope_part()) return;
       umma_commit(smem_u32(&s.s_full[par]));
     }
   }
@@ -410,10 +463,10 @@ __device__ void issue_scores(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
 
 // Chunks [c0, c0 + 2) of the output: A = codes^T (dims contiguous: MN-major), B =
 // P^T (rows contiguous: MN-major); the weights' second term is e5m2 (format 1 of B).
-template <int NR>
-__device__ void issue_output(DecodeSmem<NR>& s, const DecodeParams& p, Share sh, uint32_t tmem, uint32_t c0,
+template <int NR, bool FP4>
+__device__ void issue_output(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, uint32_t tmem, uint32_t c0,
                              volatile uint32_t* abort) {
-  using R = Rows<NR>;
+  using R = Rows<NR, FP4>;
   const uint32_t id_o = make_idesc(128, NR, 0, true) | (1u << 15);
   const uint64_t chunk_desc = sw128_desc_at(smem_u32(s.chunk[0])), p_desc = sw64_desc_at(smem_u32(s.p));
   uint32_t tile = 0;
@@ -421,11 +474,12 @@ __device__ void issue_output(DecodeSmem<NR>& s, const DecodeParams& p, Share sh,
   while (next_segment<NR>(p, sh, g)) {
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
       if (!mbar_wait(smem_u32(&s.p_full), tile & 1u, abort)) return;
+      if constexpr (FP4) fence_proxy_async_smem();
       tc_fence_after();
       const uint32_t more = kt != g.kt0;
 #pragma unroll 1
       for (uint32_t c = 0; c < 2; ++c) {
-        const Place<NR> at(tile, c0 + c);
+        const Place<NR, FP4> at(tile, c0 + c);
         const uint64_t vd = chunk_desc + at.slot * (kChunk >> 4);
         const uint32_t d = tmem + (c0 + c) * NR;
 #pragma unroll
@@ -479,8 +533,8 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 }
 // The queries of a row tile as two e4m3 terms, rows t1 at r and t2 at NR + r of
 // the K-major operand; col_factor[r] takes the row's power of two back.
-template <int NR>
-__device__ void load_queries(DecodeSmem<NR>& s, const DecodeParams& p, const Segment& g, int tid) {
+template <int NR, typename Smem>
+__device__ void load_queries(Smem& s, const DecodeParams& p, const Segment& g, int tid) {
   constexpr int kPer = 128 * kGroups / NR;        // threads per row
   constexpr int kPieces = (36 + kPer - 1) / kPer;  // of 16 dims
   const uint32_t r = tid / kPer, part = tid % kPer;
@@ -568,9 +622,9 @@ __device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& first
 }
 
 template <int NR, bool FP4>
-__device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem<NR>>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
+__device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
-  using R = Rows<NR>;
+  using R = Rows<NR, FP4>;
   constexpr int N = R::kCols;
   const int tid = group * 128 + quarter * 32 + lane;
   const uint32_t key = quarter * 32 + lane;              // this thread's key of a tile
@@ -638,9 +692,9 @@ __device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSm
       // ---- scores
       softmax_wait(smem_u32(&s.s_full[tile & 1]), (tile >> 1) & 1u, abort);
       if constexpr (FP4) {
-        const Place<NR> at(tile, 0);                     // (complete long ago: orders this thread after its exponent)
+        const Place<NR, FP4> at(tile, 0);                     // (complete long ago: orders this thread after its exponent)
         softmax_wait(smem_u32(&s.full[at.slot]), at.phase, abort);
-        const uint32_t e = s.key_e[tile % kExponentSlots][key];
+        const uint32_t e = s.key_e[tile & 1][key];
         ok = e != kNoKey;
         // The codes are in units of 2^(E - 133).
         sc = e == kFp4NanE ? __uint_as_float(0x7FC00000u) : __uint_as_float((max(e, 13u) - 6u) << 23);
@@ -775,12 +829,12 @@ __device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSm
         // see the NaN have NaN weights already: the scores read the same codes.)
         uint32_t nan = !ok;
         for (int c = 0; c < 4; ++c) {  // (complete long ago: orders this thread after the copies)
-          const Place<NR> at(tile, c);
+          const Place<NR, FP4> at(tile, c);
           softmax_wait(smem_u32(&s.full[at.slot]), at.phase, abort);
         }
 #pragma unroll 1
         for (int c = 0; c < 4 && !nan; ++c) {
-          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[Place<NR>(tile, c).slot] + key * 128);
+          const uint4* row = reinterpret_cast<const uint4*>(s.chunk[Place<NR, FP4>(tile, c).slot] + key * 128);
           for (int i = 0; i < 8; ++i) {
             const uint4 v = row[i];
             nan |= (((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -790,7 +844,7 @@ __device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSm
         if (nan) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint4* row = reinterpret_cast<uint4*>(s.chunk[Place<NR>(tile, c).slot] + key * 128);
+            uint4* row = reinterpret_cast<uint4*>(s.chunk[Place<NR, FP4>(tile, c).slot] + key * 128);
             for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -896,149 +950,79 @@ __device__ void decode_softmax(std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSm
 }
 
 // ------------------------------------------------------------ 4-bit rows to codes
-// The rows of a CTA's tiles, one key of each tile: a page-table entry is read two
-// tiles before the row itself.
-struct RowWalk {
-  Share sh;
-  Segment g;
-  uint32_t kt, key;
-  KeyWalk walk;
-  uint32_t page, off;      // of the tile that the last step came to; kNoPage: no such key
-  __device__ __forceinline__ RowWalk(const DecodeParams& p, const Share& share, uint32_t key_)
-      : sh(share), kt(0), key(key_), walk(p, 0), page(kNoPage), off(0) {
-    g.kt1 = 0;
-  }
-  template <int NR>
-  __device__ __forceinline__ bool step(const DecodeParams& p) {
-    if (kt == g.kt1) {
-      if (!next_segment<NR>(p, sh, g)) return false;
-      kt = g.kt0;
-      walk = KeyWalk(p, kt * kKeys + key);
-    }
-    page = walk.page(p, g.b, kt * kKeys + key < g.s.keys);
-    off = walk.off;
-    walk.next(p);
-    ++kt;
-    return true;
-  }
-};
-
 // Warp w takes keys 16 w .. 16 w + 15 of a tile, chunk by chunk (128 dims, four
 // blocks): lane l block l % 4 of keys 16 w + l / 4 and 8 further, so that eight lanes'
-// 16-byte stores fall into different banks.  A block's 32 codes are 16 bytes and become 32.
-// What a chunk holds of the next tile is loaded as soon as its registers are free.
+// 16-byte loads and stores fall into different banks.  A block's 32 codes are 16 bytes and
+// become 32.  The fence between these warps' stores and the tensor cores' reads is the
+// issuers', behind their wait.
 template <int NR>
-__device__ void dequantise(DecodeSmem4<NR>& s, const DecodeParams& p, const Share& sh, uint32_t w, uint32_t lane,
-                           volatile uint32_t* abort) {
-  using R = Rows<NR>;
+__device__ void dequantise(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, uint32_t w, uint32_t lane, volatile uint32_t* abort) {
+  using R = Rows<NR, true>;
   const uint32_t j = lane & 3u, near = w * 16 + (lane >> 2);   // keys near, near + 8
-  const uint32_t mine = j & 1u;                                // which of them this lane walks
-  RowWalk it(p, sh, near + 8 * mine);
-  uint32_t bad = 0;
-  auto address = [&]() -> const uint8_t* {
-    if (it.page == kNoPage) return nullptr;
-    if (it.page >= p.num_pages) {
-      bad = MLA_DEVICE_STATUS_BAD_PAGE;
-      return nullptr;
-    }
-    return p.rows4 + it.page * p.page_bytes + it.off * p.tok_bytes;
+  auto wait = [&](uint64_t& bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1u, abort)); };
+  auto arrive = [&](uint64_t& bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
-  struct Rows2 {
-    const uint8_t* at[2];
+  auto convert = [&](const uint4& v, uint32_t shift, uint8_t* row, uint32_t col, uint32_t swz) {
+    const uint2 t = s.table[shift];
+    const Fp4Table tab = {t.x, t.y};
+    const uint2 a = fp4_to_e4m3(v.x, tab), b = fp4_to_e4m3(v.y, tab), d = fp4_to_e4m3(v.z, tab), f = fp4_to_e4m3(v.w, tab);
+    *reinterpret_cast<uint4*>(row + ((col ^ swz) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(row + (((col + 1) ^ swz) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
   };
-  auto both = [&](const uint8_t* own) {
-    const uint8_t* other = reinterpret_cast<const uint8_t*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own), 1));
-    Rows2 r;
-    r.at[0] = mine ? other : own;
-    r.at[1] = mine ? own : other;
-    return r;
-  };
-  auto load16 = [](const uint8_t* at) { return at ? __ldg(reinterpret_cast<const uint4*>(at)) : make_uint4(0u, 0u, 0u, 0u); };
-  constexpr uint32_t kNone = 0x01010101u * kNoKey;
-  uint4 raw[4][2], raw_rope, meta[2];
-  auto load_chunk = [&](const Rows2& r, int c) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) raw[c][e] = load16(r.at[e] ? r.at[e] + c * 64 + j * 16 : nullptr);
-  };
-  auto load_rope = [&](const Rows2& r) {
-    const uint8_t* at = j >> 1 ? r.at[1] : r.at[0];
-    raw_rope = load16(at ? at + kLatent / 2 + (j & 1u) * 16 : nullptr);
-  };
-  auto load_meta = [&](const Rows2& r) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) meta[e] = r.at[e] ? __ldg(reinterpret_cast<const uint4*>(r.at[e] + kWidth / 2)) : make_uint4(kNone, 0u, 0u, 0u);
-  };
-  bool alive = it.template step<NR>(p);
-  if (!alive) return;
-  Rows2 rows = both(address());
-  bool more = it.template step<NR>(p);
-  load_meta(rows);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) load_chunk(rows, c);
-  load_rope(rows);
-  for (uint32_t tile = 0; alive; ++tile) {
-    // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
-    uint32_t lo[2], hi[2], e_byte[2], rope_shift;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t from = 8 + 4 * j;
-      lo[e] = __funnelshift_r(meta[e].x, meta[e].y, from);
-      hi[e] = __funnelshift_r(meta[e].y, meta[e].z, from);
-      e_byte[e] = meta[e].x & 255u;
-    }
-    rope_shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
-    // The next tile's rows (their page was read a tile ago), and the page of the one behind it.
-    const bool next = more;
-    if (next) {
-      rows = both(address());
-      more = it.template step<NR>(p);
-      load_meta(rows);
-    }
-#pragma unroll
-    for (int c = 0; c < 5; ++c) {
-      const Place<NR> at_c(tile, c);
-      const uint32_t rs = tile % R::kRopeSlots;
-      uint64_t* full = c < 4 ? &s.full[at_c.slot] : &s.rope_full[rs];
-      uint64_t* empty = c < 4 ? &s.empty[at_c.slot] : &s.rope_empty[rs];
-      const uint32_t phase = c < 4 ? at_c.phase : (tile / R::kRopeSlots) & 1u;
-      if (!(alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty), phase ^ 1u, abort)))) break;
-      if (c == 0 && j < 2) {
-        s.key_e[tile % kExponentSlots][near + 8 * j] = static_cast<uint8_t>(j ? e_byte[1] : e_byte[0]);
+  uint32_t tile = 0;
+  Segment g;
+  while (next_segment<NR>(p, sh, g)) {
+    // Bit e: key near + 8 e is looked up; what lies on bad pages or past the context is no key.
+    KeyWalk walk(p, g.kt0 * kKeys + near + 8 * (j & 1u));
+    for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
+      const uint32_t page = j < 2 ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
+      walk.next(p);
+      const uint32_t tail = tile % R::kRawTails, tail_phase = tile / R::kRawTails;
+      if (!wait(s.tail_full[tail], tail_phase)) return;
+      const uint8_t* from = s.raw_tail[tail] + near * kTailRow;
+      const uint4 meta[2] = {*reinterpret_cast<const uint4*>(from + kRope / 2), *reinterpret_cast<const uint4*>(from + 8 * kTailRow + kRope / 2)};
+      const uint4 rope = *reinterpret_cast<const uint4*>(from + (j >> 1) * 8 * kTailRow + (j & 1u) * 16);
+      arrive(s.tail_empty[tail]);
+      // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
+      const uint32_t by = 8 + 4 * j;
+      const uint32_t lo[2] = {__funnelshift_r(meta[0].x, meta[0].y, by), __funnelshift_r(meta[1].x, meta[1].y, by)};
+      const uint32_t hi[2] = {__funnelshift_r(meta[0].y, meta[0].z, by), __funnelshift_r(meta[1].y, meta[1].z, by)};
+      const uint32_t e = (j & 1u ? meta[1].x : meta[0].x) & 255u;
+      {
+        const uint32_t key = near + 8 * (j >> 1), shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
+        const uint32_t rs = tile % R::kRopeSlots;
+        if (!wait(s.rope_empty[rs], tile / R::kRopeSlots ^ 1u)) return;
+        convert(rope, shift, s.rope[rs] + key * 64, 2 * (j & 1u), (key >> 1) & 3u);
+        arrive(s.rope_full[rs]);
       }
-      auto convert = [&](const uint4& v, uint32_t shift, uint8_t* row, uint32_t col, uint32_t swz) {
-        const uint2 t = s.table[shift];
-        const Fp4Table tab = {t.x, t.y};
-        const uint2 a = fp4_to_e4m3(v.x, tab), b = fp4_to_e4m3(v.y, tab), d = fp4_to_e4m3(v.z, tab), f = fp4_to_e4m3(v.w, tab);
-        *reinterpret_cast<uint4*>(row + ((col ^ swz) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(row + (((col + 1) ^ swz) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
-      };
-      if (c < 4) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t key = near + 8 * e, shift = (c < 2 ? lo[e] : hi[e]) >> (16 * (c & 1)) & 15u;
-          convert(raw[c & 3][e], shift, s.chunk[at_c.slot] + key * 128, 2 * j, key & 7u);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t pos = tile * 4 + c, rs = pos % R::kRawSlots;
+        if (!wait(s.raw_full[rs], pos / R::kRawSlots)) return;
+        const uint8_t* src = s.raw[rs] + near * 64 + j * 16;
+        const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 8 * 64)};
+        arrive(s.raw_empty[rs]);
+        const Place<NR, true> at(tile, c);
+        if (!wait(s.empty[at.slot], at.phase ^ 1u)) return;
+        // (The chunk ring has room for this tile: two tiles ago all exponents were read.)
+        if (c == 0 && j < 2) s.key_e[tile & 1][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t key = near + 8 * k, shift = (c < 2 ? lo[k] : hi[k]) >> (16 * (c & 1)) & 15u;
+          convert(v[k], shift, s.chunk[at.slot] + key * 128, 2 * j, key & 7u);
         }
-        if (next) load_chunk(rows, c & 3);
-      } else {
-        const uint32_t key = near + 8 * (j >> 1);
-        convert(raw_rope, rope_shift, s.rope[rs] + key * 64, 2 * (j & 1u), (key >> 1) & 3u);
-        if (next) load_rope(rows);
+        arrive(s.full[at.slot]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (p.test_stall && tile == 0 && c == 0) continue;   // nothing completes this chunk's barrier
-      if (lane == 0) mbar_arrive(smem_u32(full));
     }
-    alive = alive && next;
   }
-  bad = __reduce_or_sync(0xffffffffu, bad);
-  if (lane == 0 && bad && p.status) atomicOr(p.status, bad);
 }
 
 template <int NR, bool FP4>
 __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
-  using R = Rows<NR>;
-  using Smem = std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem<NR>>;
+  using R = Rows<NR, FP4>;
+  using Smem = DecodeSmem<NR, FP4>;
   constexpr int kThreads = FP4 ? kDec4Threads : kDecThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1073,12 +1057,21 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
     mbar_init(smem_u32(&s.pv_done), 2);        // both output issuers
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     fence_barrier_init();
-    if constexpr (!FP4) {
-      tma_prefetch_desc(&p.tm_latent);
-      tma_prefetch_desc(&p.tm_rope);
-    }
+    tma_prefetch_desc(&p.tm_latent);
+    tma_prefetch_desc(&p.tm_rope);
   }
   if constexpr (FP4) {
+    if (threadIdx.x == 0) {
+      for (uint32_t i = 0; i < R::kRawSlots; ++i) {
+        mbar_init(smem_u32(&s.raw_full[i]), 1);
+        mbar_init(smem_u32(&s.raw_empty[i]), kDequantWarps);
+      }
+      for (uint32_t i = 0; i < R::kRawTails; ++i) {
+        mbar_init(smem_u32(&s.tail_full[i]), 1);
+        mbar_init(smem_u32(&s.tail_empty[i]), kDequantWarps);
+      }
+      fence_barrier_init();
+    }
     if (threadIdx.x >= 32 && threadIdx.x < 48) {
       const Fp4Table t = fp4_table(threadIdx.x - 32);
       s.table[threadIdx.x - 32] = make_uint2(t.lo, t.hi);
@@ -1149,30 +1142,29 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
   __syncthreads();     // the scratch becomes query space
   auto issue = [&] {
     if (warp > 0 && elect_one()) {
-      if (warp == 1) issue_scores<NR>(s, p, sh, tmem, abort);
-      else issue_output<NR>(s, p, sh, tmem, 2 * (warp - 2), abort);
+      if (warp == 1) issue_scores<NR, FP4>(s, p, sh, tmem, abort);
+      else issue_output<NR, FP4>(s, p, sh, tmem, 2 * (warp - 2), abort);
       drain_umma(&s.drain[warp - 1]);
     }
     __syncwarp();
   };
-  if constexpr (FP4) {
-    if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-      issue();
-    } else if (warp < 4 + kSoftmaxWarps) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");  // 128 x 40 + 512 x 88 + 256 x 56 = 896 x 72
-      decode_softmax<NR, true>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-      dequantise<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
+  if (warp < 4) {
+    if constexpr (FP4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) decode_producer<NR, FP4>(s, p, sh, lane, abort);
+    if (warp > 0 && elect_one()) {
+      if (warp == 1) issue_scores<NR, FP4>(s, p, sh, tmem, abort);
+      else issue_output<NR, FP4>(s, p, sh, tmem, 2 * (warp - 2), abort);
+      drain_umma(&s.drain[warp - 1]);
     }
-  } else if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0) decode_producer<NR>(s, p, sh, lane, abort);
-    issue();
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");  // 128 x 64 + 512 x 104 = 640 x 96
-    decode_softmax<NR, false>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+    __syncwarp();
+  } else if (!FP4 || warp < 4 + kSoftmaxWarps) {
+    if constexpr (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");  // 128 x 40 + 512 x 88 + 256 x 56 = 896 x 72
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");               // 128 x 64 + 512 x 104 = 640 x 96
+    decode_softmax<NR, FP4>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
+  } else if constexpr (FP4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    dequantise<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
   }
   tc_fence_before();
   __syncthreads();
@@ -1288,7 +1280,7 @@ constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMax
 template <int NR, bool FP4>
 mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR, FP4>);
-  const int smem = static_cast<int>(FP4 ? sizeof(DecodeSmem4<NR>) : sizeof(DecodeSmem<NR>) + 1024);
+  const int smem = static_cast<int>(FP4 ? sizeof(DecodeSmem4<NR>) : sizeof(DecodeSmem8<NR>) + 1024);
   mla_status_t st;
   if ((st = check_registers(kernel, FP4 ? kDec4Regs : kDecRegs, dev, slot)) != MLA_OK) return st;
   if ((st = set_max_dynamic_smem(kernel, smem, dev, slot)) != MLA_OK) return st;
@@ -1466,6 +1458,11 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   if ((st = check_decode_operands(out, lse, q, page_table, row_offsets, cache_lens, scale, mask, status, workspace,
                                   workspace_bytes)) != MLA_OK)
     return st;
+  const int64_t NP = cache->shape[0], P = cache->shape[1];
+  if (cache->stride[0] != P * cache->stride[1] && NP > 1)
+    return fail(MLA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = P x token stride)");
+  if (cache->stride[1] < kRow4Bytes || cache->stride[1] >= (1ll << 40))
+    return fail(MLA_ERR_INVALID_ARG, "cache needs a token stride >= %u bytes", kRow4Bytes);
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
@@ -1473,9 +1470,21 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   DecodeParams p;
   memset(&p, 0, sizeof(p));
   fill_params(p, out, lse, q, cache, page_table, row_offsets, cache_lens, scale, mask, status, workspace);
-  p.rows4 = static_cast<const uint8_t*>(cache->data);
-  p.page_bytes = cache->stride[0];
-  p.tok_bytes = cache->stride[1];
+  int64_t box_rows = 1;
+  while (box_rows < kKeys && P % (2 * box_rows) == 0) box_rows *= 2;
+  if (box_rows < 8) box_rows = 1;   // row gathers take a one-row box
+  {
+    const uint64_t dims[2] = {kRow4Bytes, static_cast<uint64_t>(NP * P)};
+    const uint64_t str[1] = {static_cast<uint64_t>(cache->stride[1])};
+    const uint32_t r = static_cast<uint32_t>(box_rows), box[2] = {64, r}, tail_box[2] = {kTailRow, r};
+    if ((st = encode_tiled(&p.tm_latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, box,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, "cache")) != MLA_OK)
+      return st;
+    if ((st = encode_tiled(&p.tm_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, tail_box,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, "cache")) != MLA_OK)
+      return st;
+  }
+  p.box_rows = static_cast<uint32_t>(box_rows);
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return rows <= 32 ? launch_decode<32, true>(p, dev, sms, 16, s) : launch_decode<64, true>(p, dev, sms, 17, s);

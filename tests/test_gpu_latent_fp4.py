@@ -529,9 +529,8 @@ def test_decode_tail_behind_a_sink(lib):
 
 
 @pytest.mark.parametrize("P", [16, 12])
-@pytest.mark.parametrize("slots_outside", [False, True])
-def test_decode_strides_and_rows_outside(lib, P, slots_outside):
-    """Padded queries, outputs and cache rows, slots outside pages in memory; rows before the first and
+def test_decode_strides_and_rows_outside(lib, P):
+    """Padded queries, outputs and cache rows; rows before the first and
     behind the last sequence stay as they were."""
     d = DecodeFp4([2, 1], [100, 300], 6, P, seed=14)
     tq = int(d.ro[-1])
@@ -541,10 +540,7 @@ def test_decode_strides_and_rows_outside(lib, P, slots_outside):
     buf = torch.full((tq + 5, 7, 520), 3.0, dtype=torch.bfloat16, device="cuda")
     out = buf[:, :6, :512]
     pages = d.raw.shape[0]
-    if slots_outside:
-        cache = torch.full((P, pages, 320), 0xFF, dtype=torch.uint8, device="cuda")[:, :, :304].transpose(0, 1)
-    else:
-        cache = torch.full((pages, P, 336), 0xFF, dtype=torch.uint8, device="cuda")[:, :, :304]
+    cache = torch.full((pages, P, 336), 0xFF, dtype=torch.uint8, device="cuda")[:, :, :304]
     cache.copy_(d.raw.cuda())
     ref_ro = d.ro.copy()
     d.ro = d.ro + 2

@@ -164,6 +164,7 @@ def _decode(lib, **over):
     dict(lse=_desc([6, 5], F32)), dict(lse=_desc([6, 4])), dict(lse=_desc([6, 4], F32, ptr=0x10002)),
     dict(lse=_desc([6, 4], F32, stride=[0, 1])), dict(pt=_desc([16385, 4], U32)),
     dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(mask=7),
+    dict(cache=_cache(stride=[17 * 304, 304, 1])), dict(cache=_cache(stride=[304, 8 * 304, 1])),
 ])
 def test_decode_refuses(lib, change):
     assert _decode(lib, **change) == binding.MLA_ERR_INVALID_ARG
@@ -176,8 +177,11 @@ def test_good_arguments_reach_the_device_check(lib):
     later = (binding.MLA_ERR_UNSUPPORTED, binding.MLA_ERR_CUDA)
     for call in (_append, _gather, _decode):
         assert call(lib) in later
-        assert call(lib, cache=_cache(stride=[17 * 320, 320, 1])) in later       # padded rows and pages
+        assert call(lib, cache=_cache(stride=[16 * 320, 320, 1])) in later       # padded rows
+    for call in (_append, _gather):
+        assert call(lib, cache=_cache(stride=[17 * 320, 320, 1])) in later       # padded pages too
         assert call(lib, cache=_cache(stride=[304, 8 * 304, 1])) in later        # slots outside, pages inside
+    for call in (_append, _gather, _decode):
         assert call(lib, cache=_cache((1, 1, 304), stride=[0, 0, 1])) in later
     assert _gather(lib, dst=_to8()) in later
     assert _gather(lib, dst=_desc([0, 576], ptr=0)) in later
