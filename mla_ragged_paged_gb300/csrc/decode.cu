@@ -75,14 +75,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kKeys = 128;               // keys per tile
 constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent dims
 constexpr uint32_t kRopeBytes = kKeys * 64;
-constexpr int kGroups = 4;                    // softmax warpgroups
-constexpr int kSoftmaxWarps = 4 * kGroups;
-constexpr int kDecThreads = 128 + 128 * kGroups;  // producer and three UMMA issuers before them
-constexpr int kDecRegs = 96;
-// 4-bit cache: eight warps more, which turn its rows into e4m3 codes.
-constexpr int kDequantWarps = 8;
-constexpr int kDec4Threads = kDecThreads + 32 * kDequantWarps;
-constexpr int kDec4Regs = 72;
+constexpr int kDequantWarps = 8;              // 4-bit cache: they turn its rows into e4m3 codes
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
@@ -108,8 +101,8 @@ struct PartHeader {
 };
 
 struct DecodeParams {
-  // Cache rows [slots, 576]; boxes 128 x box_rows and 64 x box_rows.  4-bit: rows of 304 bytes, boxes of a chunk's
-  // codes and of what is behind the last (the rope dims', the exponent, the shifts), 64 bytes each.
+  // Cache rows [slots, 576]; boxes 128 x box_rows and 64 x box_rows.  4-bit: rows of 304 bytes, boxes of two
+  // chunks' codes (128 bytes) and of the tails (64).
   CUtensorMap tm_latent, tm_rope;
   uint16_t* out;
   long long o_tok, o_head;
@@ -136,6 +129,11 @@ struct DecodeParams {
 
 template <int NR, bool FP4>
 struct Rows {
+  static constexpr int kGroups = FP4 && NR <= 32 ? 2 : 4;  // softmax warpgroups
+  static constexpr int kSoftmaxWarps = 4 * kGroups;
+  // Producer and three UMMA issuers, the softmax warps, the warps that make codes.
+  static constexpr int kThreads = 128 + 128 * kGroups + (FP4 ? 32 * kDequantWarps : 0);
+  static constexpr int kRegs = kThreads == 640 ? 96 : 72;
   static constexpr int kCols = NR / kGroups;      // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
   // P: a row of codes per key.  64 rows: an array of 64-byte rows per term; 32
@@ -143,10 +141,8 @@ struct Rows {
   static constexpr uint32_t kPBytes = kKeys * 2 * NR;
   static constexpr uint32_t kPTerm = NR == 64 ? kKeys * 64 : 32;  // bytes from the first term to the second
   // What fits: 8 latent chunks are two tiles.
-  static constexpr uint32_t kSlots = FP4 ? (NR <= 32 ? 8 : 6) : NR <= 32 ? 10 : 8;
-  static constexpr uint32_t kRopeSlots = !FP4 && NR <= 32 ? 2 : 1;
-  // 4-bit cache: chunks of codes as they are cached, and the tiles' rope codes and shifts.
-  static constexpr uint32_t kRawSlots = NR <= 32 ? 4 : 3, kRawTails = 1;
+  static constexpr uint32_t kSlots = NR <= 32 ? 10 : 8, kRopeSlots = NR <= 32 ? 2 : 1;
+  static constexpr uint32_t kHalves = kSlots / 2;  // 4-bit cache: two chunks come and go together
 };
 
 template <int NR>
@@ -157,8 +153,8 @@ struct __align__(1024) DecodeSmem8 {
   uint8_t q[4][R::kQChunk];
   uint8_t q_rope[2 * NR * 64];
   uint8_t p[R::kPBytes];
-  float warp_red[kGroups][4][R::kCols];
-  float row_val[kGroups][R::kCols];
+  float warp_red[R::kGroups][4][R::kCols];
+  float row_val[R::kGroups][R::kCols];
   float col_factor[NR];
   uint64_t full[R::kSlots], empty[R::kSlots];
   uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
@@ -166,11 +162,10 @@ struct __align__(1024) DecodeSmem8 {
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
-// 4-bit cache.
+// 4-bit cache.  Half a tile's codes (two chunks, 128 bytes a key) arrive in the place of the
+// second of the two chunks that they become, a key's where its row of that chunk will be; the rows' tails
+// (rope dims, exponent, shifts: 48 bytes and 16 past the row, which arrive as zeros) in the place of the rope dims.
 constexpr uint32_t kRow4Bytes = fp4_row_bytes(kWidth);
-// A tile's chunk of cached codes, and its rows' tails: 48 bytes and 16 past the row, which arrive as zeros (copies
-// of four rows have to begin 128-byte aligned).
-constexpr uint32_t kTailRow = 64, kRawChunk = kKeys * 64, kRawTail = kKeys * kTailRow;
 constexpr uint8_t kNoKey = 254;               // in the place of an exponent: past the context, or on a bad page
 template <int NR>
 struct __align__(1024) DecodeSmem4 {
@@ -180,17 +175,14 @@ struct __align__(1024) DecodeSmem4 {
   uint8_t q[4][R::kQChunk];
   uint8_t q_rope[2 * NR * 64];
   uint8_t p[R::kPBytes];
-  uint8_t raw[R::kRawSlots][kRawChunk];
-  uint8_t raw_tail[R::kRawTails][kRawTail];
-  float warp_red[kGroups][4][R::kCols];
-  float row_val[kGroups][R::kCols];
+  float warp_red[R::kGroups][4][R::kCols];
+  float row_val[R::kGroups][R::kCols];
   float col_factor[NR];
   uint2 table[16];                            // the e4m3 forms of a block's codes, by its shift
-  uint8_t key_e[2][kKeys];                    // the keys' exponents
-  uint64_t full[R::kSlots], empty[R::kSlots];
-  uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
-  uint64_t raw_full[R::kRawSlots], raw_empty[R::kRawSlots];
-  uint64_t tail_full[R::kRawTails], tail_empty[R::kRawTails];
+  static constexpr uint32_t kExponents = (R::kHalves + 1) / 2;
+  uint8_t key_e[kExponents][kKeys];           // the keys' exponents
+  uint64_t full[R::kHalves], empty[R::kHalves], raw_full[R::kHalves];
+  uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots], tail_full[R::kRopeSlots];
   uint64_t q_full, s_full[2], s_empty[2], p_full, pv_done, drain[3];
   uint32_t tmem_base;
   uint32_t abort_flag;
@@ -302,13 +294,14 @@ struct Place {
 };
 
 // ------------------------------------------------------------ producer
-// 8-bit: chunks and rope dims of the codes that the tensor cores read.  4-bit: first the tile's
-// tails (rope codes, exponents, shifts), then its chunks, all as they are cached.
+// 8-bit: chunks and rope dims, the codes that the tensor cores read.  4-bit: first the tile's tails,
+// then its halves, as they are cached.
 template <int NR, bool FP4>
 __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, int lane, volatile uint32_t* abort) {
   using R = Rows<NR, FP4>;
-  constexpr uint32_t kBodyBytes = FP4 ? kRawChunk : kChunk, kTailBytes = FP4 ? kRawTail : kRopeBytes;
-  constexpr uint32_t kBodyStep = FP4 ? 64 : 128, kBodySlots = FP4 ? R::kRawSlots : R::kSlots, kTailSlots = FP4 ? R::kRawTails : R::kRopeSlots;
+  // Bodies: chunks, or half tiles of 4-bit codes; 128 bytes a key either way.
+  constexpr int kBodies = FP4 ? 2 : 4;
+  constexpr uint32_t kBodySlots = R::kSlots * kBodies / 4;
   const bool boxed = p.box_rows > 1;
   const uint32_t boxes = kKeys / p.box_rows;
   uint32_t tile = 0, bad = 0;
@@ -354,41 +347,40 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
         // from now; into L2 the rows can come at once (measured: 118 -> 108 us
         // for 152 sequences x 4500 x 64 heads).
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tma_prefetch_2d(&p.tm_latent, c * kBodyStep, rows[0]);
-        tma_prefetch_2d(&p.tm_rope, 4 * kBodyStep, rows[0]);
+        for (int c = 0; c < kBodies; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, rows[0]);
+        tma_prefetch_2d(&p.tm_rope, kBodies * 128, rows[0]);
       }
-      for (int i = 0; i < 5 && alive; ++i) {
-        const int c = FP4 ? (i + 4) % 5 : i;   // 4: the tail
-        const uint32_t pos = c < 4 ? tile * 4 + c : tile, ring = c < 4 ? kBodySlots : kTailSlots;
+      for (int i = 0; i <= kBodies && alive; ++i) {
+        const int c = FP4 ? (i + kBodies) % (kBodies + 1) : i;   // kBodies: the tail
+        const bool body = c < kBodies;
+        const uint32_t pos = body ? tile * kBodies + c : tile, ring = body ? kBodySlots : R::kRopeSlots;
         const uint32_t slot = pos % ring, phase = (pos / ring) & 1u;
-        uint64_t *full, *empty;
-        uint32_t dst;
+        uint64_t *full, *empty = body ? &s.empty[slot] : &s.rope_empty[slot];
+        uint32_t dst = smem_u32(s.rope[body ? 0 : slot]);
         if constexpr (FP4) {
-          full = c < 4 ? &s.raw_full[slot] : &s.tail_full[slot];
-          empty = c < 4 ? &s.raw_empty[slot] : &s.tail_empty[slot];
-          dst = c < 4 ? smem_u32(s.raw[slot]) : smem_u32(s.raw_tail[slot]);
+          full = body ? &s.raw_full[slot] : &s.tail_full[slot];
+          if (body) dst = smem_u32(s.chunk[2 * slot + 1]);
         } else {
-          full = c < 4 ? &s.full[slot] : &s.rope_full[slot];
-          empty = c < 4 ? &s.empty[slot] : &s.rope_empty[slot];
-          dst = c < 4 ? smem_u32(s.chunk[slot]) : smem_u32(s.rope[slot]);
+          full = body ? &s.full[slot] : &s.rope_full[slot];
+          if (body) dst = smem_u32(s.chunk[slot]);
         }
         // (The warp goes on or gives up as one: what follows needs all lanes.)
         if (!(alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(empty), phase ^ 1u, abort)))) break;
-        if (p.test_stall && tile == 0 && c == 0) {   // nothing arms this chunk's barrier
+        if (p.test_stall && tile == 0 && c == 0) {   // nothing arms this barrier
           chunks = 1;
           continue;
         }
-        if (c < 4) chunks = pos + 1;
+        if (body) chunks = pos + 1;
         else ropes = pos + 1;
         const uint32_t bar = smem_u32(full);
-        if (lane == 0) mbar_arrive_expect_tx(bar, c < 4 ? kBodyBytes : kTailBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, body ? kChunk : kRopeBytes);
         __syncwarp();
-        const uint32_t row_bytes = c < 4 ? kBodyBytes / kKeys : kTailBytes / kKeys;
-        const CUtensorMap* map = c < 4 ? &p.tm_latent : &p.tm_rope;
+        const uint32_t row_bytes = body ? 128u : 64u;
+        const CUtensorMap* map = body ? &p.tm_latent : &p.tm_rope;
         if (!boxed)
-          tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * kBodyStep, rows[0], rows[1], rows[2], rows[3]);
+          tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
         else if (lane < boxes)
-          tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * kBodyStep, rows[0]);
+          tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * 128, rows[0]);
       }
     }
   }
@@ -406,10 +398,10 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
     };
     if constexpr (FP4) {
       landed(s.raw_full, kBodySlots, chunks);
-      landed(s.tail_full, kTailSlots, ropes);
+      landed(s.tail_full, R::kRopeSlots, ropes);
     } else {
       landed(s.full, kBodySlots, chunks);
-      landed(s.rope_full, kTailSlots, ropes);
+      landed(s.rope_full, R::kRopeSlots, ropes);
     }
   }
 }
@@ -448,9 +440,11 @@ __device__ void issue_scores(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Shar
 #pragma unroll 1
       for (uint32_t c = 0; c < 4; ++c) {
         const Place<NR, FP4> at(tile, c);
-        if (!mbar_wait(smem_u32(&s.full[at.slot]), at.phase, abort)) return;
-        if constexpr (FP4) fence_proxy_async_smem();
-        tc_fence_after();
+        if (!FP4 || c % 2 == 0) {
+          if (!mbar_wait(smem_u32(&s.full[FP4 ? at.slot / 2 : at.slot]), at.phase, abort)) return;
+          if constexpr (FP4) fence_proxy_async_smem();
+          tc_fence_after();
+        }
         const uint64_t kd = chunk_desc + at.slot * (kChunk >> 4), qd = q_desc + c * (R::kQChunk >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f8_ss(d, kd + 2 * k, qd + 2 * k, id_s, FP4 || (c | k) != 0);
@@ -488,7 +482,8 @@ __device__ void issue_output(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Shar
           for (int term = 0; term < 2; ++term)
             umma_f8_ss(d, vd + k * (32 * 128 >> 4), p_desc + term * (R::kPTerm >> 4) + k * (32 * 64 >> 4),
                        term ? id_o | 1u << 10 : id_o, term || k ? 1u : more);
-        umma_commit(smem_u32(&s.empty[at.slot]));
+        if (!FP4) umma_commit(smem_u32(&s.empty[at.slot]));
+        else if (c) umma_commit(smem_u32(&s.empty[at.slot / 2]));
       }
       umma_commit(smem_u32(&s.pv_done));
     }
@@ -535,7 +530,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
 // the K-major operand; col_factor[r] takes the row's power of two back.
 template <int NR, typename Smem>
 __device__ void load_queries(Smem& s, const DecodeParams& p, const Segment& g, int tid) {
-  constexpr int kPer = 128 * kGroups / NR;        // threads per row
+  constexpr int kPer = 128 * Smem::R::kGroups / NR;  // threads per row
   constexpr int kPieces = (36 + kPer - 1) / kPer;  // of 16 dims
   const uint32_t r = tid / kPer, part = tid % kPer;
   const uint32_t row = g.rt * NR + r, tok = row / p.H, head = row - tok * p.H;
@@ -625,7 +620,7 @@ template <int NR, bool FP4>
 __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, unsigned long long steps, uint32_t ctas,
                                uint32_t tmem, int group, int quarter, int lane, volatile uint32_t* abort) {
   using R = Rows<NR, FP4>;
-  constexpr int N = R::kCols;
+  constexpr int N = R::kCols, kGroups = R::kGroups;
   const int tid = group * 128 + quarter * 32 + lane;
   const uint32_t key = quarter * 32 + lane;              // this thread's key of a tile
   const uint32_t lane_at = static_cast<uint32_t>(quarter * 32) << 16;
@@ -692,9 +687,9 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
       // ---- scores
       softmax_wait(smem_u32(&s.s_full[tile & 1]), (tile >> 1) & 1u, abort);
       if constexpr (FP4) {
-        const Place<NR, FP4> at(tile, 0);                     // (complete long ago: orders this thread after its exponent)
-        softmax_wait(smem_u32(&s.full[at.slot]), at.phase, abort);
-        const uint32_t e = s.key_e[tile & 1][key];
+        const Place<NR, FP4> at(tile, 0);                // (complete long ago: orders this thread after its exponent)
+        softmax_wait(smem_u32(&s.full[at.slot / 2]), at.phase, abort);
+        const uint32_t e = s.key_e[tile % DecodeSmem4<NR>::kExponents][key];
         ok = e != kNoKey;
         // The codes are in units of 2^(E - 133).
         sc = e == kFp4NanE ? __uint_as_float(0x7FC00000u) : __uint_as_float((max(e, 13u) - 6u) << 23);
@@ -814,7 +809,10 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
       {
         const uint32_t swz = (key >> 1) & 3;
         uint8_t* row = s.p + key * 64;
-        if constexpr (NR == 32) {
+        if constexpr (NR == 32 && N == 16) {
+          *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(row + (((2 + group) ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        } else if constexpr (NR == 32) {
           uint8_t* at = row + 8 * (group & 1);
           *reinterpret_cast<uint2*>(at + (((group >> 1) ^ swz) << 4)) = make_uint2(t1[0], t1[1]);
           *reinterpret_cast<uint2*>(at + (((2 + (group >> 1)) ^ swz) << 4)) = make_uint2(t2[0], t2[1]);
@@ -950,80 +948,81 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
 }
 
 // ------------------------------------------------------------ 4-bit rows to codes
-// Warp w takes keys 16 w .. 16 w + 15 of a tile, chunk by chunk (128 dims, four
-// blocks): lane l block l % 4 of keys 16 w + l / 4 and 8 further, so that eight lanes'
-// 16-byte loads and stores fall into different banks.  A block's 32 codes are 16 bytes and
-// become 32.  The fence between these warps' stores and the tensor cores' reads is the
-// issuers', behind their wait.
+// Warp w takes keys 16 w .. 16 w + 15 of a tile.  Of a chunk (128 dims, four blocks of
+// 16 bytes, which become 32) lane l takes block l % 4 of two keys 8 apart.  Four lanes' key is
+// k of the warp's, the next four's k ^ 5: in 128-byte swizzled rows eight lanes' loads of 16
+// bytes (columns 0 .. 3 or 4 .. 7) then fall into different banks, and so do their stores (even
+// columns, then odd ones).  The fence between these warps' stores and the tensor cores'
+// reads is the issuers', behind their wait.
 template <int NR>
 __device__ void dequantise(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, uint32_t w, uint32_t lane, volatile uint32_t* abort) {
   using R = Rows<NR, true>;
-  const uint32_t j = lane & 3u, near = w * 16 + (lane >> 2);   // keys near, near + 8
+  const uint32_t j = lane & 3u, k7 = (lane >> 3) ^ (lane & 4u ? 5u : 0u), near = w * 16 + k7;   // keys near, near + 8
+  const uint32_t from = near * 128 + ((j ^ k7) << 4);                        // of a half's first chunk; the other's is ^ 64
+  const uint32_t to = near * 128 + (((2 * j) ^ k7) << 4);                    // the block's first half; the second's is ^ 16
+  const uint32_t rope_key = near + 8 * (j >> 1);                             // its block j % 2
+  const uint32_t rope_to = rope_key * 64 + (((2 * (j & 1u)) ^ ((rope_key >> 1) & 3u)) << 4);
   auto wait = [&](uint64_t& bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1u, abort)); };
   auto arrive = [&](uint64_t& bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
-  auto convert = [&](const uint4& v, uint32_t shift, uint8_t* row, uint32_t col, uint32_t swz) {
+  auto convert = [&](const uint4& v, uint32_t shift, uint8_t* base, uint32_t at) {
     const uint2 t = s.table[shift];
     const Fp4Table tab = {t.x, t.y};
     const uint2 a = fp4_to_e4m3(v.x, tab), b = fp4_to_e4m3(v.y, tab), d = fp4_to_e4m3(v.z, tab), f = fp4_to_e4m3(v.w, tab);
-    *reinterpret_cast<uint4*>(row + ((col ^ swz) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4*>(row + (((col + 1) ^ swz) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+    *reinterpret_cast<uint4*>(base + at) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(base + (at ^ 16u)) = make_uint4(d.x, d.y, f.x, f.y);
   };
   uint32_t tile = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
-    // Bit e: key near + 8 e is looked up; what lies on bad pages or past the context is no key.
-    KeyWalk walk(p, g.kt0 * kKeys + near + 8 * (j & 1u));
+    KeyWalk walk(p, g.kt0 * kKeys + near + 8 * (j & 1u));   // lanes 0 and 1 of four: whether there is such a key
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
       const uint32_t page = j < 2 ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
       walk.next(p);
-      const uint32_t tail = tile % R::kRawTails, tail_phase = tile / R::kRawTails;
-      if (!wait(s.tail_full[tail], tail_phase)) return;
-      const uint8_t* from = s.raw_tail[tail] + near * kTailRow;
-      const uint4 meta[2] = {*reinterpret_cast<const uint4*>(from + kRope / 2), *reinterpret_cast<const uint4*>(from + 8 * kTailRow + kRope / 2)};
-      const uint4 rope = *reinterpret_cast<const uint4*>(from + (j >> 1) * 8 * kTailRow + (j & 1u) * 16);
-      arrive(s.tail_empty[tail]);
+      const uint32_t rs = tile % R::kRopeSlots;
+      if (!wait(s.tail_full[rs], tile / R::kRopeSlots)) return;
+      const uint8_t* tail = s.rope[rs] + near * 64;
+      const uint4 meta[2] = {*reinterpret_cast<const uint4*>(tail + kRope / 2), *reinterpret_cast<const uint4*>(tail + 8 * 64 + kRope / 2)};
+      const uint4 rope = *reinterpret_cast<const uint4*>(tail + (j >> 1) * 8 * 64 + (j & 1u) * 16);
       // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
       const uint32_t by = 8 + 4 * j;
       const uint32_t lo[2] = {__funnelshift_r(meta[0].x, meta[0].y, by), __funnelshift_r(meta[1].x, meta[1].y, by)};
       const uint32_t hi[2] = {__funnelshift_r(meta[0].y, meta[0].z, by), __funnelshift_r(meta[1].y, meta[1].z, by)};
       const uint32_t e = (j & 1u ? meta[1].x : meta[0].x) & 255u;
-      {
-        const uint32_t key = near + 8 * (j >> 1), shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
-        const uint32_t rs = tile % R::kRopeSlots;
-        if (!wait(s.rope_empty[rs], tile / R::kRopeSlots ^ 1u)) return;
-        convert(rope, shift, s.rope[rs] + key * 64, 2 * (j & 1u), (key >> 1) & 3u);
-        arrive(s.rope_full[rs]);
-      }
+      const uint32_t rope_shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
+      __syncwarp();                                         // read by all lanes, then written
+      convert(rope, rope_shift, s.rope[rs], rope_to);
+      arrive(s.rope_full[rs]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t pos = tile * 4 + c, rs = pos % R::kRawSlots;
-        if (!wait(s.raw_full[rs], pos / R::kRawSlots)) return;
-        const uint8_t* src = s.raw[rs] + near * 64 + j * 16;
-        const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 8 * 64)};
-        arrive(s.raw_empty[rs]);
-        const Place<NR, true> at(tile, c);
-        if (!wait(s.empty[at.slot], at.phase ^ 1u)) return;
-        // (The chunk ring has room for this tile: two tiles ago all exponents were read.)
-        if (c == 0 && j < 2) s.key_e[tile & 1][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t pos = tile * 2 + h, hs = pos % R::kHalves;
+        if (!wait(s.raw_full[hs], pos / R::kHalves)) return;
+        uint8_t* base = s.chunk[2 * hs];
+        uint4 v[2][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t key = near + 8 * k, shift = (c < 2 ? lo[k] : hi[k]) >> (16 * (c & 1)) & 15u;
-          convert(v[k], shift, s.chunk[at.slot] + key * 128, 2 * j, key & 7u);
-        }
-        arrive(s.full[at.slot]);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) v[c][k] = *reinterpret_cast<const uint4*>(base + kChunk + (from ^ (c ? 64u : 0u)) + k * 8 * 128);
+        __syncwarp();
+        // (The ring has room for this tile: whoever read the exponent's slot before is done.)
+        if (h == 0 && j < 2) s.key_e[tile % DecodeSmem4<NR>::kExponents][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) convert(v[c][k], (h ? hi[k] : lo[k]) >> (16 * c) & 15u, base + c * kChunk, to + k * 8 * 128);
+        arrive(s.full[hs]);
       }
     }
   }
 }
 
 template <int NR, bool FP4>
-__global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
   using R = Rows<NR, FP4>;
   using Smem = DecodeSmem<NR, FP4>;
-  constexpr int kThreads = FP4 ? kDec4Threads : kDecThreads;
+  constexpr int kThreads = R::kThreads, kSoftmaxWarps = R::kSoftmaxWarps, kRings = FP4 ? R::kHalves : R::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (FP4 && (smem_u32(smem_raw) & 1023u)) {  // (no room is left to round up)
@@ -1040,7 +1039,7 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
   Prologue& pro = *reinterpret_cast<Prologue*>(s.q[0]);
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (uint32_t i = 0; i < R::kSlots; ++i) {
+    for (uint32_t i = 0; i < kRings; ++i) {
       mbar_init(smem_u32(&s.full[i]), FP4 ? kDequantWarps : 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
@@ -1062,14 +1061,8 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
   }
   if constexpr (FP4) {
     if (threadIdx.x == 0) {
-      for (uint32_t i = 0; i < R::kRawSlots; ++i) {
-        mbar_init(smem_u32(&s.raw_full[i]), 1);
-        mbar_init(smem_u32(&s.raw_empty[i]), kDequantWarps);
-      }
-      for (uint32_t i = 0; i < R::kRawTails; ++i) {
-        mbar_init(smem_u32(&s.tail_full[i]), 1);
-        mbar_init(smem_u32(&s.tail_empty[i]), kDequantWarps);
-      }
+      for (uint32_t i = 0; i < R::kHalves; ++i) mbar_init(smem_u32(&s.raw_full[i]), 1);
+      for (uint32_t i = 0; i < R::kRopeSlots; ++i) mbar_init(smem_u32(&s.tail_full[i]), 1);
       fence_barrier_init();
     }
     if (threadIdx.x >= 32 && threadIdx.x < 48) {
@@ -1148,9 +1141,11 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
     }
     __syncwarp();
   };
+  // Registers, of what the block was launched with: 640 x 96 = 128 x 64 + 512 x 104 (8-bit) = 128 x 64 + 256 x 128 + 256 x 80,
+  // 896 x 72 = 128 x 40 + 512 x 88 + 256 x 56.
   if (warp < 4) {
-    if constexpr (FP4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (kThreads == 640) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) decode_producer<NR, FP4>(s, p, sh, lane, abort);
     if (warp > 0 && elect_one()) {
       if (warp == 1) issue_scores<NR, FP4>(s, p, sh, tmem, abort);
@@ -1159,11 +1154,13 @@ __global__ void __launch_bounds__(FP4 ? kDec4Threads : kDecThreads, 1) decode_ke
     }
     __syncwarp();
   } else if (!FP4 || warp < 4 + kSoftmaxWarps) {
-    if constexpr (FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");  // 128 x 40 + 512 x 88 + 256 x 56 = 896 x 72
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");               // 128 x 64 + 512 x 104 = 640 x 96
+    if constexpr (!FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else if constexpr (kThreads == 640) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     decode_softmax<NR, FP4>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   } else if constexpr (FP4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kThreads == 640) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     dequantise<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
   }
   tc_fence_before();
@@ -1282,11 +1279,11 @@ mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStre
   const void* kernel = reinterpret_cast<const void*>(decode_kernel<NR, FP4>);
   const int smem = static_cast<int>(FP4 ? sizeof(DecodeSmem4<NR>) : sizeof(DecodeSmem8<NR>) + 1024);
   mla_status_t st;
-  if ((st = check_registers(kernel, FP4 ? kDec4Regs : kDecRegs, dev, slot)) != MLA_OK) return st;
+  if ((st = check_registers(kernel, Rows<NR, FP4>::kRegs, dev, slot)) != MLA_OK) return st;
   if ((st = set_max_dynamic_smem(kernel, smem, dev, slot)) != MLA_OK) return st;
   const uint32_t ctas = std::min<uint32_t>(static_cast<uint32_t>(sms), kMaxCtas);
   p.ctas = ctas;
-  decode_kernel<NR, FP4><<<ctas, FP4 ? kDec4Threads : kDecThreads, smem, stream>>>(p);
+  decode_kernel<NR, FP4><<<ctas, Rows<NR, FP4>::kThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
   // Row tiles: each sequence's last one may be partial.  (us with a block / a warp per
@@ -1476,9 +1473,9 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   {
     const uint64_t dims[2] = {kRow4Bytes, static_cast<uint64_t>(NP * P)};
     const uint64_t str[1] = {static_cast<uint64_t>(cache->stride[1])};
-    const uint32_t r = static_cast<uint32_t>(box_rows), box[2] = {64, r}, tail_box[2] = {kTailRow, r};
+    const uint32_t r = static_cast<uint32_t>(box_rows), box[2] = {128, r}, tail_box[2] = {64, r};
     if ((st = encode_tiled(&p.tm_latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, box,
-                           CU_TENSOR_MAP_SWIZZLE_NONE, "cache")) != MLA_OK)
+                           CU_TENSOR_MAP_SWIZZLE_128B, "cache")) != MLA_OK)
       return st;
     if ((st = encode_tiled(&p.tm_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, tail_box,
                            CU_TENSOR_MAP_SWIZZLE_NONE, "cache")) != MLA_OK)
