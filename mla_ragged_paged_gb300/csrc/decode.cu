@@ -75,7 +75,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kKeys = 128;               // keys per tile
 constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent dims
 constexpr uint32_t kRopeBytes = kKeys * 64;
-constexpr int kDequantWarps = 8;              // 4-bit cache: they turn its rows into e4m3 codes
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
@@ -131,8 +130,9 @@ template <int NR, bool FP4>
 struct Rows {
   static constexpr int kGroups = FP4 && NR <= 32 ? 2 : 4;  // softmax warpgroups
   static constexpr int kSoftmaxWarps = 4 * kGroups;
-  // Producer and three UMMA issuers, the softmax warps, the warps that make codes.
-  static constexpr int kThreads = 128 + 128 * kGroups + (FP4 ? 32 * kDequantWarps : 0);
+  // Producer and three UMMA issuers, the softmax warps, the warps that turn 4-bit rows into e4m3 codes.
+  static constexpr int kCodeWarps = FP4 ? 8 : 0;
+  static constexpr int kThreads = 128 + 128 * kGroups + 32 * kCodeWarps;
   static constexpr int kRegs = kThreads == 640 ? 96 : 72;
   static constexpr int kCols = NR / kGroups;      // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
@@ -455,7 +455,8 @@ __device__ void issue_scores(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Shar
   }
 }
 
-// Chunks [c0, c0 + 2) of the output: A = codes^T (dims contiguous: MN-major), B =
+// Chunks [c0, c0 + 2) of the output (4-bit cache: c0 / 2 and the one two further, so that both threads
+// work on a half tile at a time): A = codes^T (dims contiguous: MN-major), B =
 // P^T (rows contiguous: MN-major); the weights' second term is e5m2 (format 1 of B).
 template <int NR, bool FP4>
 __device__ void issue_output(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Share sh, uint32_t tmem, uint32_t c0,
@@ -473,17 +474,17 @@ __device__ void issue_output(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Shar
       const uint32_t more = kt != g.kt0;
 #pragma unroll 1
       for (uint32_t c = 0; c < 2; ++c) {
-        const Place<NR, FP4> at(tile, c0 + c);
+        const uint32_t chunk = FP4 ? c0 / 2 + 2 * c : c0 + c;
+        const Place<NR, FP4> at(tile, chunk);
         const uint64_t vd = chunk_desc + at.slot * (kChunk >> 4);
-        const uint32_t d = tmem + (c0 + c) * NR;
+        const uint32_t d = tmem + chunk * NR;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int term = 0; term < 2; ++term)
             umma_f8_ss(d, vd + k * (32 * 128 >> 4), p_desc + term * (R::kPTerm >> 4) + k * (32 * 64 >> 4),
                        term ? id_o | 1u << 10 : id_o, term || k ? 1u : more);
-        if (!FP4) umma_commit(smem_u32(&s.empty[at.slot]));
-        else if (c) umma_commit(smem_u32(&s.empty[at.slot / 2]));
+        umma_commit(smem_u32(&s.empty[FP4 ? at.slot / 2 : at.slot]));
       }
       umma_commit(smem_u32(&s.pv_done));
     }
@@ -948,70 +949,91 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
 }
 
 // ------------------------------------------------------------ 4-bit rows to codes
-// Warp w takes keys 16 w .. 16 w + 15 of a tile.  Of a chunk (128 dims, four blocks of
-// 16 bytes, which become 32) lane l takes block l % 4 of two keys 8 apart.  Four lanes' key is
-// k of the warp's, the next four's k ^ 5: in 128-byte swizzled rows eight lanes' loads of 16
-// bytes (columns 0 .. 3 or 4 .. 7) then fall into different banks, and so do their stores (even
-// columns, then odd ones).  The fence between these warps' stores and the tensor cores'
-// reads is the issuers', behind their wait.
+// A warp takes 8 or 16 keys of a tile.  Of a chunk (128 dims, four blocks of 16 bytes,
+// which become 32) lane l takes block l % 4 of a key, and of another 8 further.  Four lanes'
+// key is k of the warp's, the next four's k ^ 5: in 128-byte swizzled rows eight lanes'
+// loads of 16 bytes (columns 0 .. 3 or 4 .. 7) then fall into different banks, and so do
+// their stores (even columns, then odd ones).  The fence between these warps' stores and the
+// tensor cores' reads is the issuers', behind their wait.
 template <int NR>
-__device__ void dequantise(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, uint32_t w, uint32_t lane, volatile uint32_t* abort) {
+__device__ void make_codes(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, uint32_t w, uint32_t lane, volatile uint32_t* abort) {
   using R = Rows<NR, true>;
-  const uint32_t j = lane & 3u, k7 = (lane >> 3) ^ (lane & 4u ? 5u : 0u), near = w * 16 + k7;   // keys near, near + 8
+  constexpr int kEach = kKeys / 8 / R::kCodeWarps;                           // keys of a lane
+  const uint32_t j = lane & 3u, k7 = (lane >> 3) ^ (lane & 4u ? 5u : 0u), near = w * 8 * kEach + k7;   // and 8 further
   const uint32_t from = near * 128 + ((j ^ k7) << 4);                        // of a half's first chunk; the other's is ^ 64
   const uint32_t to = near * 128 + (((2 * j) ^ k7) << 4);                    // the block's first half; the second's is ^ 16
-  const uint32_t rope_key = near + 8 * (j >> 1);                             // its block j % 2
-  const uint32_t rope_to = rope_key * 64 + (((2 * (j & 1u)) ^ ((rope_key >> 1) & 3u)) << 4);
+  // Rope dims: a block of one of two keys, or half a block of the one.
+  const uint32_t rope_key = near + (kEach == 2 ? 8 * (j >> 1) : 0), rope_col = kEach == 2 ? 2 * (j & 1u) : j;
+  const uint32_t rope_to = rope_key * 64 + ((rope_col ^ ((rope_key >> 1) & 3u)) << 4);
   auto wait = [&](uint64_t& bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1u, abort)); };
   auto arrive = [&](uint64_t& bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
-  auto convert = [&](const uint4& v, uint32_t shift, uint8_t* base, uint32_t at) {
-    const uint2 t = s.table[shift];
+  auto convert = [&](uint32_t x, uint32_t y, const uint2& t, uint8_t* to16) {
     const Fp4Table tab = {t.x, t.y};
-    const uint2 a = fp4_to_e4m3(v.x, tab), b = fp4_to_e4m3(v.y, tab), d = fp4_to_e4m3(v.z, tab), f = fp4_to_e4m3(v.w, tab);
-    *reinterpret_cast<uint4*>(base + at) = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4*>(base + (at ^ 16u)) = make_uint4(d.x, d.y, f.x, f.y);
+    const uint2 a = fp4_to_e4m3(x, tab), b = fp4_to_e4m3(y, tab);
+    *reinterpret_cast<uint4*>(to16) = make_uint4(a.x, a.y, b.x, b.y);
   };
   uint32_t tile = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
-    KeyWalk walk(p, g.kt0 * kKeys + near + 8 * (j & 1u));   // lanes 0 and 1 of four: whether there is such a key
+    KeyWalk walk(p, g.kt0 * kKeys + near + (kEach == 2 ? 8 * (j & 1u) : 0));   // the first lanes of four: whether there is such a key
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
-      const uint32_t page = j < 2 ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
+      const uint32_t page = j < kEach ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
       walk.next(p);
       const uint32_t rs = tile % R::kRopeSlots;
       if (!wait(s.tail_full[rs], tile / R::kRopeSlots)) return;
       const uint8_t* tail = s.rope[rs] + near * 64;
-      const uint4 meta[2] = {*reinterpret_cast<const uint4*>(tail + kRope / 2), *reinterpret_cast<const uint4*>(tail + 8 * 64 + kRope / 2)};
-      const uint4 rope = *reinterpret_cast<const uint4*>(tail + (j >> 1) * 8 * 64 + (j & 1u) * 16);
+      uint4 meta[kEach], rope;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) meta[k] = *reinterpret_cast<const uint4*>(tail + k * 8 * 64 + kRope / 2);
+      if constexpr (kEach == 2) {
+        rope = *reinterpret_cast<const uint4*>(tail + (j >> 1) * 8 * 64 + (j & 1u) * 16);
+      } else {
+        const uint2 half = *reinterpret_cast<const uint2*>(tail + j * 8);
+        rope = make_uint4(half.x, half.y, 0u, 0u);
+      }
       // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
       const uint32_t by = 8 + 4 * j;
-      const uint32_t lo[2] = {__funnelshift_r(meta[0].x, meta[0].y, by), __funnelshift_r(meta[1].x, meta[1].y, by)};
-      const uint32_t hi[2] = {__funnelshift_r(meta[0].y, meta[0].z, by), __funnelshift_r(meta[1].y, meta[1].z, by)};
-      const uint32_t e = (j & 1u ? meta[1].x : meta[0].x) & 255u;
-      const uint32_t rope_shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
+      uint32_t lo[kEach], hi[kEach];
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        lo[k] = __funnelshift_r(meta[k].x, meta[k].y, by);
+        hi[k] = __funnelshift_r(meta[k].y, meta[k].z, by);
+      }
+      const uint32_t e = (kEach == 2 && (j & 1u) ? meta[kEach - 1].x : meta[0].x) & 255u;
+      const uint32_t rope_shift = kEach == 2 ? (j >> 1 ? meta[kEach - 1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u
+                                             : meta[0].z >> (8 + 4 * (j >> 1)) & 15u;
       __syncwarp();                                         // read by all lanes, then written
-      convert(rope, rope_shift, s.rope[rs], rope_to);
+      {
+        const uint2 t = s.table[rope_shift];
+        convert(rope.x, rope.y, t, s.rope[rs] + rope_to);
+        if constexpr (kEach == 2) convert(rope.z, rope.w, t, s.rope[rs] + (rope_to ^ 16u));
+      }
       arrive(s.rope_full[rs]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t pos = tile * 2 + h, hs = pos % R::kHalves;
         if (!wait(s.raw_full[hs], pos / R::kHalves)) return;
         uint8_t* base = s.chunk[2 * hs];
-        uint4 v[2][2];
+        uint4 v[2][kEach];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) v[c][k] = *reinterpret_cast<const uint4*>(base + kChunk + (from ^ (c ? 64u : 0u)) + k * 8 * 128);
+          for (int k = 0; k < kEach; ++k) v[c][k] = *reinterpret_cast<const uint4*>(base + kChunk + (from ^ (c ? 64u : 0u)) + k * 8 * 128);
         __syncwarp();
         // (The ring has room for this tile: whoever read the exponent's slot before is done.)
-        if (h == 0 && j < 2) s.key_e[tile % DecodeSmem4<NR>::kExponents][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
+        if (h == 0 && j < kEach)
+          s.key_e[tile % DecodeSmem4<NR>::kExponents][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) convert(v[c][k], (h ? hi[k] : lo[k]) >> (16 * c) & 15u, base + c * kChunk, to + k * 8 * 128);
+          for (int k = 0; k < kEach; ++k) {
+            const uint2 t = s.table[(h ? hi[k] : lo[k]) >> (16 * c) & 15u];
+            convert(v[c][k].x, v[c][k].y, t, base + c * kChunk + to + k * 8 * 128);
+            convert(v[c][k].z, v[c][k].w, t, base + c * kChunk + (to ^ 16u) + k * 8 * 128);
+          }
         arrive(s.full[hs]);
       }
     }
@@ -1040,11 +1062,11 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (uint32_t i = 0; i < kRings; ++i) {
-      mbar_init(smem_u32(&s.full[i]), FP4 ? kDequantWarps : 1);
-      mbar_init(smem_u32(&s.empty[i]), 1);
+      mbar_init(smem_u32(&s.full[i]), FP4 ? R::kCodeWarps : 1);
+      mbar_init(smem_u32(&s.empty[i]), FP4 ? 2 : 1);   // (4-bit: a chunk each of both output issuers)
     }
     for (uint32_t i = 0; i < R::kRopeSlots; ++i) {
-      mbar_init(smem_u32(&s.rope_full[i]), FP4 ? kDequantWarps : 1);
+      mbar_init(smem_u32(&s.rope_full[i]), FP4 ? R::kCodeWarps : 1);
       mbar_init(smem_u32(&s.rope_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1141,11 +1163,11 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
     }
     __syncwarp();
   };
-  // Registers, of what the block was launched with: 640 x 96 = 128 x 64 + 512 x 104 (8-bit) = 128 x 64 + 256 x 128 + 256 x 80,
-  // 896 x 72 = 128 x 40 + 512 x 88 + 256 x 56.
+  // Registers, of what the block was launched with: 640 x 96 = 128 x 64 + 512 x 104; 4-bit: 896 x 72 = 128 x 40 + 512 x 88 +
+  // 256 x 56 (64-row tiles) = 128 x 40 + 256 x 104 + 512 x 64 (32-row tiles).
   if (warp < 4) {
-    if constexpr (kThreads == 640) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (kThreads == 896) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) decode_producer<NR, FP4>(s, p, sh, lane, abort);
     if (warp > 0 && elect_one()) {
       if (warp == 1) issue_scores<NR, FP4>(s, p, sh, tmem, abort);
@@ -1156,12 +1178,13 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   } else if (!FP4 || warp < 4 + kSoftmaxWarps) {
     if constexpr (!FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     else if constexpr (kThreads == 640) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    else if constexpr (NR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     decode_softmax<NR, FP4>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   } else if constexpr (FP4) {
     if constexpr (kThreads == 640) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    dequantise<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
+    else if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    make_codes<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
   }
   tc_fence_before();
   __syncthreads();
