@@ -33,6 +33,7 @@ struct RopeSide {
   long long x_tok, x_head, y_tok, y_head;
   uint32_t heads, dim, norm_dim, w_f32;
   uint32_t blocks, rows_per_block;
+  uint32_t form;             // 0: element by element; else lanes of a row * 16 + items of a lane * 4 + log2 of rows of a lane
 };
 struct RopeParams {
   RopeSide side[2];          // queries, keys
@@ -66,23 +67,15 @@ __device__ __forceinline__ float2 rope_angle(uint32_t position, float f, float s
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
 __device__ __forceinline__ uint16_t to_bf16(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f)); }
 
-// A warp per row, element by element: any strides, widths and alignments.
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParams p) {
-  extern __shared__ float2 turn[];  // [tokens of the block][pairs]
-  const bool keys = blockIdx.x >= p.side[0].blocks;
-  const RopeSide& sd = p.side[keys];
-  const uint32_t block = blockIdx.x - (keys ? p.side[0].blocks : 0u);
+struct RopeBlock {
+  uint32_t row0, row1, tok0;
+};
+
+// Rows element by element, a warp each: any strides, widths and alignments.
+__device__ __forceinline__ void rope_rows_by_elements(const RopeParams& p, const RopeSide& sd, const RopeBlock& bl, const float2* turn) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const uint32_t total = p.tokens * sd.heads, row0 = block * sd.rows_per_block;
-  const uint32_t row1 = min(total, row0 + sd.rows_per_block);
-  const uint32_t tok0 = row0 / sd.heads, toks = (row1 - 1) / sd.heads - tok0 + 1;
-  for (uint32_t i = threadIdx.x; i < toks * p.pairs; i += kRopeThreads) {
-    const uint32_t t = i / p.pairs;
-    turn[i] = rope_angle(__ldg(p.positions + tok0 + t), __ldg(p.inv_freq + (i - t * p.pairs)), p.scale);
-  }
-  __syncthreads();
   const uint32_t dim = sd.dim, plain = dim - 2 * p.pairs;
-  for (uint32_t row = row0 + warp; row < row1; row += kRopeThreads / 32) {
+  for (uint32_t row = bl.row0 + warp; row < bl.row1; row += kRopeThreads / 32) {
     const uint32_t tok = row / sd.heads, head = row - tok * sd.heads;
     const uint16_t* x = sd.x + tok * sd.x_tok + head * sd.x_head;
     uint16_t* y = sd.y + tok * sd.y_tok + head * sd.y_head;
@@ -106,12 +99,171 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeParam
     for (uint32_t c = lane; c < plain; c += 32) y[c] = to_bf16(value(c));
     for (uint32_t i = lane; i < p.pairs; i += 32) {
       const uint32_t a = plain + (p.halves ? i : 2 * i), b = p.halves ? a + p.pairs : a + 1;
-      const float2 cs = turn[(tok - tok0) * p.pairs + i];
+      const float2 cs = turn[(tok - bl.tok0) * p.pairs + i];
       const float u = value(a), v = value(b);
       y[a] = to_bf16(u * cs.x - v * cs.y);
       y[b] = to_bf16(u * cs.y + v * cs.x);
     }
   }
+}
+
+// Rows in items of 16 bytes (8 columns), or, of halves that turn together, twice 16:
+// `lanes` lanes have a row, K items each, U rows at a time, all loaded before the angles are
+// formed and waited for.
+template <bool HALVES, int K, int U>
+struct RopeItems {
+  uint4 v[U][K][HALVES ? 2 : 1];
+  uint32_t lanes, lane, row_step, row;   // lane within the row; first row of this lane
+  uint32_t items, plain;                 // of a row; its items that are not turned
+
+  __device__ __forceinline__ void load(const RopeParams& p, const RopeSide& sd, const RopeBlock& bl, uint32_t lanes_) {
+    lanes = lanes_;
+    lane = threadIdx.x & (lanes - 1);
+    row_step = kRopeThreads / lanes;
+    row = bl.row0 + threadIdx.x / lanes;
+    plain = (sd.dim - 2 * p.pairs) / 8;
+    items = plain + (HALVES ? p.pairs / 8 : p.pairs / 4);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t r = row + u * row_step, tok = r / sd.heads;
+      const uint16_t* x = sd.x + tok * sd.x_tok + (r - tok * sd.heads) * sd.x_head;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t i = lane + k * lanes;
+        const bool live = r < bl.row1 && i < items;
+        v[u][k][0] = live ? *reinterpret_cast<const uint4*>(x + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (HALVES)
+          v[u][k][1] = live && i >= plain ? *reinterpret_cast<const uint4*>(x + 8 * i + p.pairs) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  static __device__ __forceinline__ void widen(const uint4& q, float (&f)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(w[e] << 16);
+      f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+  // Columns c .. c + 7 of the weight times rs.
+  static __device__ __forceinline__ void scale(const RopeSide& sd, uint32_t c, float rs, float (&f)[8]) {
+    if (c >= sd.norm_dim) return;
+    float w[8];
+    if (sd.w_f32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(sd.w) + c));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(sd.w) + c) + 1);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      widen(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(sd.w) + c)), w);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= rs * w[e];
+  }
+  __device__ __forceinline__ void finish(const RopeParams& p, const RopeSide& sd, const RopeBlock& bl, const float2* turn) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t r = row + u * row_step, tok = r / sd.heads;
+      float rs = 1.f;
+      if (sd.norm_dim) {
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int h = 0; h < (HALVES ? 2 : 1); ++h) {
+            float f[8];
+            widen(v[u][k][h], f);
+            const uint32_t c = 8 * (lane + k * lanes) + h * p.pairs;
+            if (c < sd.norm_dim)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+          }
+        for (uint32_t o = lanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        rs = rsqrtf(ss / sd.norm_dim + p.eps);
+      }
+      if (r >= bl.row1) continue;
+      uint16_t* y = sd.y + tok * sd.y_tok + (r - tok * sd.heads) * sd.y_head;
+      const float2* cs = turn + (tok - bl.tok0) * p.pairs;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t i = lane + k * lanes;
+        if (i >= items) continue;
+        float a[8];
+        widen(v[u][k][0], a);
+        scale(sd, 8 * i, rs, a);
+        if (i >= plain) {
+          if constexpr (HALVES) {
+            float b[8];
+            widen(v[u][k][1], b);
+            scale(sd, 8 * i + p.pairs, rs, b);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float4 t = *reinterpret_cast<const float4*>(cs + 8 * (i - plain) + e);
+              const float u0 = a[e], v0 = b[e], u1 = a[e + 1], v1 = b[e + 1];
+              a[e] = u0 * t.x - v0 * t.y;
+              b[e] = u0 * t.y + v0 * t.x;
+              a[e + 1] = u1 * t.z - v1 * t.w;
+              b[e + 1] = u1 * t.w + v1 * t.z;
+            }
+            *reinterpret_cast<uint4*>(y + 8 * i + p.pairs) = narrow(b);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float4 t = *reinterpret_cast<const float4*>(cs + 4 * (i - plain) + e);
+              const float u0 = a[2 * e], v0 = a[2 * e + 1], u1 = a[2 * e + 2], v1 = a[2 * e + 3];
+              a[2 * e] = u0 * t.x - v0 * t.y;
+              a[2 * e + 1] = u0 * t.y + v0 * t.x;
+              a[2 * e + 2] = u1 * t.z - v1 * t.w;
+              a[2 * e + 3] = u1 * t.w + v1 * t.z;
+            }
+          }
+        }
+        *reinterpret_cast<uint4*>(y + 8 * i) = narrow(a);
+      }
+    }
+  }
+};
+
+template <bool HALVES>
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 turn[];  // [tokens of the block][pairs]
+  const bool keys = blockIdx.x >= p.side[0].blocks;
+  const RopeSide& sd = p.side[keys];
+  const uint32_t block = blockIdx.x - (keys ? p.side[0].blocks : 0u);
+  RopeBlock bl;
+  bl.row0 = block * sd.rows_per_block;
+  bl.row1 = min(p.tokens * sd.heads, bl.row0 + sd.rows_per_block);
+  bl.tok0 = bl.row0 / sd.heads;
+  const uint32_t angles = ((bl.row1 - 1) / sd.heads - bl.tok0 + 1) * p.pairs;
+  auto form_angles = [&] {
+    for (uint32_t i = threadIdx.x; i < angles; i += kRopeThreads) {
+      const uint32_t t = i / p.pairs;
+      turn[i] = rope_angle(__ldg(p.positions + bl.tok0 + t), __ldg(p.inv_freq + (i - t * p.pairs)), p.scale);
+    }
+    __syncthreads();
+  };
+  const uint32_t lanes = sd.form >> 4;
+  auto by_items = [&](auto items) {
+    items.load(p, sd, bl, lanes);
+    form_angles();
+    items.finish(p, sd, bl, turn);
+  };
+  switch (sd.form & 15u) {
+    case 4: return by_items(RopeItems<HALVES, 1, 1>());
+    case 4 + 2: return by_items(RopeItems<HALVES, 1, 4>());
+    case 8 + 1: return by_items(RopeItems<HALVES, 2, 2>());
+    case 12: return by_items(RopeItems<HALVES, 4, 1>());
+    default: form_angles(); rope_rows_by_elements(p, sd, bl, turn);
+  }
+}
+
+// Whether rows can be moved in items: 16-byte aligned, and every boundary between two items.
+bool rope_items_ok(const RopeSide& sd, const RopeParams& p) {
+  const long long strides = sd.x_tok | sd.x_head | sd.y_tok | sd.y_head;
+  return aligned16(sd.x) && aligned16(sd.y) && (!sd.w || aligned16(sd.w)) && strides % 8 == 0 && sd.dim % 8 == 0 &&
+         sd.norm_dim % 8 == 0 && p.pairs % (p.halves ? 8 : 4) == 0;
 }
 
 // One of q and k: its descriptors, and whether it is there.
@@ -195,16 +347,31 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
   size_t smem = 0;
   for (RopeSide& sd : p.side) {
     if (!sd.x) continue;
-    sd.rows_per_block = 32;
+    // Items of a lane: 1, 2 or up to 4.  Four rows a lane where there are more rows than fill the SMs at once.
+    const uint32_t items = (sd.dim - 2 * p.pairs) / 8 + p.pairs / (p.halves ? 8 : 4);
+    if (rope_items_ok(sd, p)) {
+      uint32_t lanes = 4;
+      while (lanes < 32 && lanes < items) lanes *= 2;
+      const uint32_t each = (items + lanes - 1) / lanes, groups = kRopeThreads / lanes;
+      // (The angles of a block's tokens lie in shared memory.)
+      const bool many = T * sd.heads > static_cast<int64_t>(groups) * 8 * sms && 4 * groups / sd.heads * p.pairs <= 2048;
+      const uint32_t rows = each == 1 ? (many ? 4 : 1) : each == 2 ? 2 : 1;
+      sd.form = lanes << 4 | (each > 2 ? 3u : each) << 2 | (rows == 4 ? 2u : rows - 1);
+      sd.rows_per_block = groups * rows;
+    } else {
+      sd.form = 0;
+      sd.rows_per_block = 32;
+    }
     sd.blocks = static_cast<uint32_t>((T * sd.heads + sd.rows_per_block - 1) / sd.rows_per_block);
     // The rows of a block begin in any head of a token.
     const uint32_t toks = std::min<uint32_t>(sd.rows_per_block, (sd.rows_per_block + 2 * sd.heads - 2) / sd.heads);
     smem = std::max(smem, sizeof(float2) * toks * p.pairs);
   }
-  if (smem > 48 * 1024 && (st = set_max_dynamic_smem(reinterpret_cast<const void*>(norm_rope_kernel),
-                                                     static_cast<int>(smem), dev, 15)) != MLA_OK)
+  const auto kernel = p.halves ? norm_rope_kernel<true> : norm_rope_kernel<false>;
+  if (smem > 48 * 1024 && (st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem), dev,
+                                                     p.halves ? 15 : 18)) != MLA_OK)
     return st;
-  norm_rope_kernel<<<p.side[0].blocks + p.side[1].blocks, kRopeThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  kernel<<<p.side[0].blocks + p.side[1].blocks, kRopeThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
   return MLA_OK;
