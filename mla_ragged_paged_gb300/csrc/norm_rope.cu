@@ -32,8 +32,9 @@ struct RopeSide {
   const void* w;
   long long x_tok, x_head, y_tok, y_head;
   uint32_t heads, dim, norm_dim, w_f32;
+  float per_heads;           // 1 / heads
   uint32_t blocks, rows_per_block;
-  uint32_t form;             // 0: element by element; else lanes of a row * 16 + items of a lane * 4 + log2 of rows of a lane
+  uint32_t form;             // 0: element by element; else lanes of a row * 16 + which RopeItems
 };
 struct RopeParams {
   RopeSide side[2];          // queries, keys
@@ -68,15 +69,25 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 __device__ __forceinline__ uint16_t to_bf16(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f)); }
 
 struct RopeBlock {
-  uint32_t row0, row1, tok0;
+  uint32_t row0, row1, tok0, head0;  // rows [row0, row1), the first of them head head0 of token tok0
 };
+// Token and head of row r of the block.  The rows are at most 256, so the quotient of a small
+// number of heads is exact in fp32, and of a larger number 0 or 1.
+struct RopeRow {
+  uint32_t tok, head;
+};
+__device__ __forceinline__ RopeRow rope_row(const RopeSide& sd, const RopeBlock& bl, uint32_t r) {
+  const uint32_t at = r - bl.row0 + bl.head0;
+  const uint32_t toks = sd.heads < 256 ? __float2uint_rz((at + 0.5f) * sd.per_heads) : at >= sd.heads ? 1u : 0u;
+  return {bl.tok0 + toks, at - toks * sd.heads};
+}
 
 // Rows element by element, a warp each: any strides, widths and alignments.
 __device__ __forceinline__ void rope_rows_by_elements(const RopeParams& p, const RopeSide& sd, const RopeBlock& bl, const float2* turn) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t dim = sd.dim, plain = dim - 2 * p.pairs;
   for (uint32_t row = bl.row0 + warp; row < bl.row1; row += kRopeThreads / 32) {
-    const uint32_t tok = row / sd.heads, head = row - tok * sd.heads;
+    const auto [tok, head] = rope_row(sd, bl, row);
     const uint16_t* x = sd.x + tok * sd.x_tok + head * sd.x_head;
     uint16_t* y = sd.y + tok * sd.y_tok + head * sd.y_head;
     float rs = 1.f;
@@ -125,8 +136,9 @@ struct RopeItems {
     items = plain + (HALVES ? p.pairs / 8 : p.pairs / 4);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t r = row + u * row_step, tok = r / sd.heads;
-      const uint16_t* x = sd.x + tok * sd.x_tok + (r - tok * sd.heads) * sd.x_head;
+      const uint32_t r = row + u * row_step;
+      const auto [tok, head] = rope_row(sd, bl, r);
+      const uint16_t* x = sd.x + tok * sd.x_tok + head * sd.x_head;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const uint32_t i = lane + k * lanes;
@@ -165,7 +177,8 @@ struct RopeItems {
   __device__ __forceinline__ void finish(const RopeParams& p, const RopeSide& sd, const RopeBlock& bl, const float2* turn) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t r = row + u * row_step, tok = r / sd.heads;
+      const uint32_t r = row + u * row_step;
+      const auto [tok, head] = rope_row(sd, bl, r);
       float rs = 1.f;
       if (sd.norm_dim) {
         float ss = 0.f;
@@ -184,7 +197,7 @@ struct RopeItems {
         rs = rsqrtf(ss / sd.norm_dim + p.eps);
       }
       if (r >= bl.row1) continue;
-      uint16_t* y = sd.y + tok * sd.y_tok + (r - tok * sd.heads) * sd.y_head;
+      uint16_t* y = sd.y + tok * sd.y_tok + head * sd.y_head;
       const float2* cs = turn + (tok - bl.tok0) * p.pairs;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -227,7 +240,7 @@ struct RopeItems {
 };
 
 template <bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, HALVES ? 4 : 5) norm_rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) float2 turn[];  // [tokens of the block][pairs]
   const bool keys = blockIdx.x >= p.side[0].blocks;
   const RopeSide& sd = p.side[keys];
@@ -236,6 +249,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
   bl.row0 = block * sd.rows_per_block;
   bl.row1 = min(p.tokens * sd.heads, bl.row0 + sd.rows_per_block);
   bl.tok0 = bl.row0 / sd.heads;
+  bl.head0 = bl.row0 - bl.tok0 * sd.heads;
   const uint32_t angles = ((bl.row1 - 1) / sd.heads - bl.tok0 + 1) * p.pairs;
   auto form_angles = [&] {
     for (uint32_t i = threadIdx.x; i < angles; i += kRopeThreads) {
@@ -252,7 +266,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
   };
   switch (sd.form & 15u) {
     case 4: return by_items(RopeItems<HALVES, 1, 1>());
-    case 4 + 2: return by_items(RopeItems<HALVES, 1, 4>());
+    case 4 + 2: return by_items(RopeItems<HALVES, 1, HALVES ? 2 : 4>());
     case 8 + 1: return by_items(RopeItems<HALVES, 2, 2>());
     case 12: return by_items(RopeItems<HALVES, 4, 1>());
     default: form_angles(); rope_rows_by_elements(p, sd, bl, turn);
@@ -303,6 +317,7 @@ mla_status_t rope_side(RopeSide& sd, const char* name, const mla_tensor_t* out, 
   sd.y_tok = out->stride[0];
   sd.y_head = out->stride[1];
   sd.heads = static_cast<uint32_t>(H);
+  sd.per_heads = 1.f / static_cast<float>(H);
   sd.dim = static_cast<uint32_t>(D);
   return MLA_OK;
 }
@@ -347,7 +362,7 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
   size_t smem = 0;
   for (RopeSide& sd : p.side) {
     if (!sd.x) continue;
-    // Items of a lane: 1, 2 or up to 4.  Four rows a lane where there are more rows than fill the SMs at once.
+    // Items of a lane: 1, 2 or up to 4.  Four loads a lane where there are more rows than fill the SMs at once.
     const uint32_t items = (sd.dim - 2 * p.pairs) / 8 + p.pairs / (p.halves ? 8 : 4);
     if (rope_items_ok(sd, p)) {
       uint32_t lanes = 4;
@@ -355,8 +370,8 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
       const uint32_t each = (items + lanes - 1) / lanes, groups = kRopeThreads / lanes;
       // (The angles of a block's tokens lie in shared memory.)
       const bool many = T * sd.heads > static_cast<int64_t>(groups) * 8 * sms && 4 * groups / sd.heads * p.pairs <= 2048;
-      const uint32_t rows = each == 1 ? (many ? 4 : 1) : each == 2 ? 2 : 1;
-      sd.form = lanes << 4 | (each > 2 ? 3u : each) << 2 | (rows == 4 ? 2u : rows - 1);
+      const uint32_t rows = each == 1 ? (many ? (p.halves ? 2 : 4) : 1) : each == 2 ? 2 : 1;
+      sd.form = lanes << 4 | (each > 2 ? 3u : each) << 2 | (each == 1 && many ? 2u : rows - 1);
       sd.rows_per_block = groups * rows;
     } else {
       sd.form = 0;
