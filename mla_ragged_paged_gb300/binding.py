@@ -541,17 +541,28 @@ _BYTES = (torch.uint8,)
 _INDEX = (torch.int32, torch.uint32)
 
 
+_PACK1, _PACK2, _PACK3 = _LAYOUT[1], _LAYOUT[2], _LAYOUT[3]
+
+
 def _operand(t, what, dtypes, dtype):
-    """_typed, then _pack, in one call."""
+    """_typed, then _pack, in one call (its usual ranks without argument unpacking, which
+    would be a third of it)."""
     if t is None:
         return None
     if t.dtype not in dtypes:
         _typed(t, what, *dtypes)
-    shape = t.shape
-    n = len(shape)
-    if not 1 <= n <= 4:
-        return _pack(t, dtype)
-    return _LAYOUT[n](t.data_ptr(), dtype, n, *shape, *t.stride(), 0, MLA_SCALE_NONE)
+    n = t.ndim
+    if n == 3:
+        a, b, c = t.shape
+        x, y, z = t.stride()
+        return _PACK3(t.data_ptr(), dtype, 3, a, b, c, x, y, z, 0, 0)
+    if n == 2:
+        a, b = t.shape
+        x, y = t.stride()
+        return _PACK2(t.data_ptr(), dtype, 2, a, b, x, y, 0, 0)
+    if n == 1:
+        return _PACK1(t.data_ptr(), dtype, 1, t.shape[0], t.stride(0), 0, 0)
+    return _pack(t, dtype)
 
 
 def _bf16_or_f32(t):
@@ -581,13 +592,15 @@ def _device_of(*tensors):
         if t is None:
             continue
         at = t.get_device()
-        if at < 0:
-            _on_device(t)
-        if dev < 0:
+        if at == dev:
+            if at < 0:
+                _on_device(t)
+        elif dev < 0:
             dev = at
             if dev != torch._C._cuda_getDevice():   # (a CUDA tensor exists: no lazy start)
                 raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on the current device (got {t.device})")
-        elif at != dev:
+        else:
+            _on_device(t)
             raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must be on one device (got cuda:{dev} and {t.device})")
     return dev
 

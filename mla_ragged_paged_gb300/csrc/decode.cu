@@ -1479,10 +1479,11 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
                                   workspace_bytes)) != MLA_OK)
     return st;
   const int64_t NP = cache->shape[0], P = cache->shape[1];
-  if (cache->stride[0] != P * cache->stride[1] && NP > 1)
+  if (cache->stride[0] != P * cache->stride[1] && NP > 1 && P > 1)
     return fail(MLA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = P x token stride)");
-  if (cache->stride[1] < kRow4Bytes || cache->stride[1] >= (1ll << 40))
-    return fail(MLA_ERR_INVALID_ARG, "cache needs a token stride >= %u bytes", kRow4Bytes);
+  // From row to row: strides of dimensions of one element say nothing.
+  const int64_t pitch = P > 1 ? cache->stride[1] : NP > 1 ? cache->stride[0] : kRow4Bytes;
+  if (pitch >= (1ll << 40)) return fail(MLA_ERR_INVALID_ARG, "cache rows are too far apart");
   int dev = 0, sms = 0;
   if ((st = check_device(&dev, &sms)) != MLA_OK) return st;
   const int64_t Tq = q->shape[0], H = q->shape[1], B = page_table->shape[0];
@@ -1495,7 +1496,7 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   if (box_rows < 8) box_rows = 1;   // row gathers take a one-row box
   {
     const uint64_t dims[2] = {kRow4Bytes, static_cast<uint64_t>(NP * P)};
-    const uint64_t str[1] = {static_cast<uint64_t>(cache->stride[1])};
+    const uint64_t str[1] = {static_cast<uint64_t>(pitch)};
     const uint32_t r = static_cast<uint32_t>(box_rows), box[2] = {128, r}, tail_box[2] = {64, r};
     if ((st = encode_tiled(&p.tm_latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache->data, dims, str, box,
                            CU_TENSOR_MAP_SWIZZLE_128B, "cache")) != MLA_OK)
