@@ -671,9 +671,10 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
     named_bar_sync(1 + kGroups, 128 * kGroups);          // col_factor is written by all warpgroups
     float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
     uint32_t look = g.kt0 + 2;                           // form the maxima in all tiles before this one
-    float l[N], lq[N];
+    // Pairs of neighbouring rows go through packed arithmetic (the same roundings, half the instructions).
+    uint64_t l[N / 2], lq[N / 2];
 #pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = lq[i] = 0.f;
+    for (int i = 0; i < N / 2; ++i) l[i] = lq[i] = 0;
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
       float sc = sc_next, ls;
       bool ok = ok_next;
@@ -698,7 +699,7 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
       }
       const float to_sum = ex2_approx(-kShift - kSumShift - ls);
       tc_fence_after();
-      float y[N];
+      uint64_t y[N / 2];
       {
         uint32_t a[N], b[N];
         const uint32_t col = tmem + lane_at + kColS + (tile & 1) * (2 * NR) + r0;
@@ -708,40 +709,53 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.s_empty[tile & 1]));
+        const uint64_t sc2 = f2_pack(sc, sc), ls2 = f2_pack(ls, ls);
+        auto pair = [](const uint32_t* r) { return f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])); };
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&s.col_factor[r0 + i]);
-          y[i] = fmaf((__uint_as_float(a[i]) + __uint_as_float(b[i])) * f.x, sc, ls);
-          y[i + 1] = fmaf((__uint_as_float(a[i + 1]) + __uint_as_float(b[i + 1])) * f.y, sc, ls);
-          y[i + 2] = fmaf((__uint_as_float(a[i + 2]) + __uint_as_float(b[i + 2])) * f.z, sc, ls);
-          y[i + 3] = fmaf((__uint_as_float(a[i + 3]) + __uint_as_float(b[i + 3])) * f.w, sc, ls);
+          y[i / 2] = f2_fma(f2_mul(f2_add(pair(a + i), pair(b + i)), f2_pack(f.x, f.y)), sc2, ls2);
+          y[i / 2 + 1] = f2_fma(f2_mul(f2_add(pair(a + i + 2), pair(b + i + 2)), f2_pack(f.z, f.w)), sc2, ls2);
         }
       }
       const bool partial = ok && j >= shared;            // some rows see this key, some do not
-      if (!ok) {
+      if (__any_sync(0xffffffffu, !ok || partial)) {     // (else nothing to mask in the whole warp)
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = -INFINITY;
-      } else if (partial) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (j > g.s.prior + (first_row + r0 + i) / p.H) y[i] = -INFINITY;
+        for (int i = 0; i < N; i += 2) {
+          float y0, y1;
+          f2_unpack(y[i / 2], y0, y1);
+          if (!ok || (partial && j > g.s.prior + (first_row + r0 + i) / p.H)) y0 = -INFINITY;
+          if (!ok || (partial && j > g.s.prior + (first_row + r0 + i + 1) / p.H)) y1 = -INFINITY;
+          y[i / 2] = f2_pack(y0, y1);
+        }
       }
+      // Rows i .. i + 3: the scores above their references.
+      const uint64_t minus1 = f2_pack(-1.f, -1.f);
+      auto above = [&](int i, float (&d)[4]) {
+        const float4 m4 = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
+        f2_unpack(f2_fma(f2_pack(m4.x, m4.y), minus1, y[i / 2]), d[0], d[1]);
+        f2_unpack(f2_fma(f2_pack(m4.z, m4.w), minus1, y[i / 2 + 1]), d[2], d[3]);
+      };
       // ---- the rows' references: formed anew, or still good for every key?
       bool form = kt < look || (kt - g.kt0) % kLook == 0;
       if (!form) {
         float over = -INFINITY;
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
-          over = max3(over, y[i] - m4.x, y[i + 1] - m4.y);
-          over = max3(over, y[i + 2] - m4.z, y[i + 3] - m4.w);
+          float d[4];
+          above(i, d);
+          over = max3(over, d[0], d[1]);
+          over = max3(over, d[2], d[3]);
         }
         form = bar_any(bar, 128, over > kShift + kRaise);
       }
       uint32_t moved = 0;
       float factor = 1.f;
       if (form) {
-        const float wm = warp_transpose_reduce<N>(y, lane, fmax2);
+        float each[N];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) f2_unpack(y[i / 2], each[i], each[i + 1]);
+        const float wm = warp_transpose_reduce<N>(each, lane, fmax2);
         if (lane < N) s.warp_red[group][quarter][lane] = wm;
         named_bar_sync(bar, 128);
         const float tm = fmaxf(fmaxf(s.warp_red[group][0][my_row], s.warp_red[group][1][my_row]),
@@ -761,31 +775,32 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
         if (moved) {
           look = kt + 2;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float f = __shfl_sync(0xffffffffu, factor, i);
-            if (moved >> i & 1) l[i] *= f, lq[i] *= f;
+          for (int i = 0; i < N; i += 2) {
+            const float f0 = __shfl_sync(0xffffffffu, factor, i), f1 = __shfl_sync(0xffffffffu, factor, i + 1);
+            const uint64_t f = f2_pack(moved >> i & 1 ? f0 : 1.f, moved >> (i + 1) & 1 ? f1 : 1.f);
+            l[i / 2] = f2_mul(l[i / 2], f);
+            lq[i / 2] = f2_mul(lq[i / 2], f);
           }
         }
       }
       // ---- weights: two terms per row
       uint32_t t1[N / 4], t2[N / 4];
+      const uint64_t to_sum2 = f2_pack(to_sum, to_sum);
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
-        const float4 m4 = *reinterpret_cast<const float4*>(&s.row_val[group][i]);
-        const float w0 = ex2_approx(y[i] - m4.x), w1 = ex2_approx(y[i + 1] - m4.y), w2 = ex2_approx(y[i + 2] - m4.z),
-                    w3 = ex2_approx(y[i + 3] - m4.w);
-        l[i] = fmaf(w0, to_sum, l[i]);
-        l[i + 1] = fmaf(w1, to_sum, l[i + 1]);
-        l[i + 2] = fmaf(w2, to_sum, l[i + 2]);
-        l[i + 3] = fmaf(w3, to_sum, l[i + 3]);
+        float w[4], q[4];
+        above(i, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = ex2_approx(w[e]);
+        l[i / 2] = f2_fma(f2_pack(w[0], w[1]), to_sum2, l[i / 2]);
+        l[i / 2 + 1] = f2_fma(f2_pack(w[2], w[3]), to_sum2, l[i / 2 + 1]);
         uint32_t a0, b0, a1, b1;
-        float q0, q1, q2, q3;
-        weight_terms(w0, w1, a0, b0, q0, q1);
-        weight_terms(w2, w3, a1, b1, q2, q3);
-        lq[i] = fmaf(w0 >= kSmall ? q0 : w0, to_sum, lq[i]);
-        lq[i + 1] = fmaf(w1 >= kSmall ? q1 : w1, to_sum, lq[i + 1]);
-        lq[i + 2] = fmaf(w2 >= kSmall ? q2 : w2, to_sum, lq[i + 2]);
-        lq[i + 3] = fmaf(w3 >= kSmall ? q3 : w3, to_sum, lq[i + 3]);
+        weight_terms(w[0], w[1], a0, b0, q[0], q[1]);
+        weight_terms(w[2], w[3], a1, b1, q[2], q[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = w[e] >= kSmall ? q[e] : w[e];
+        lq[i / 2] = f2_fma(f2_pack(q[0], q[1]), to_sum2, lq[i / 2]);
+        lq[i / 2 + 1] = f2_fma(f2_pack(q[2], q[3]), to_sum2, lq[i / 2 + 1]);
         t1[i / 4] = a0 | a1 << 16;
         t2[i / 4] = b0 | b1 << 16;
       }
@@ -858,7 +873,16 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
     tc_fence_after();
     // The rows' sums over the warps meet in P's place, which is free now.
     float(*sums)[4][2][N] = reinterpret_cast<float(*)[4][2][N]>(s.p);
-    const float mine = warp_transpose_reduce<N>(l, lane, add2), mine_q = warp_transpose_reduce<N>(lq, lane, add2);
+    float mine, mine_q;
+    {
+      float each[N];
+#pragma unroll
+      for (int i = 0; i < N; i += 2) f2_unpack(l[i / 2], each[i], each[i + 1]);
+      mine = warp_transpose_reduce<N>(each, lane, add2);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) f2_unpack(lq[i / 2], each[i], each[i + 1]);
+      mine_q = warp_transpose_reduce<N>(each, lane, add2);
+    }
     if (lane < N) {
       sums[group][quarter][0][lane] = mine;
       sums[group][quarter][1][lane] = mine_q;
