@@ -93,6 +93,11 @@ constexpr float kSumShift = 30.f;
 constexpr uint32_t kStartSteps = 4;
 constexpr float kUnit = 0x1p-37f;             // 2^-(kShift + kSumShift): out = O / l in these units
 
+// a / b; a short division where it does.
+__device__ __forceinline__ unsigned long long divide(unsigned long long a, uint32_t b) {
+  return a >> 32 ? a / b : static_cast<uint32_t>(a) / b;
+}
+
 // Part of a row tile's result: slot 2 c of CTA c for one that continues an
 // earlier CTA's, 2 c + 1 for one that begins and does not end.
 struct PartHeader {
@@ -272,6 +277,10 @@ constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 struct KeyWalk {
   uint32_t col, off;
   __device__ __forceinline__ KeyWalk(const DecodeParams& p, uint32_t key) : col(key / p.P) { off = key - col * p.P; }
+  // The key behind another's.
+  __device__ __forceinline__ KeyWalk(const DecodeParams& p, const KeyWalk& before) : col(before.col), off(before.off + 1) {
+    if (off == p.P) off = 0, ++col;
+  }
   __device__ __forceinline__ uint32_t page(const DecodeParams& p, uint32_t b, bool wanted) const {
     return wanted && col < p.max_pages ? __ldg(p.page_table + static_cast<long long>(b) * p.pt_stride + col) : kNoPage;
   }
@@ -313,7 +322,8 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
     // gathers: rows 4 lane .. 4 lane + 3.  What lies past the context or on a
     // bad page is read from slot 0 on, whatever it holds (the softmax zeroes it).
     const uint32_t at = boxed ? lane * p.box_rows : 4 * lane, first = g.kt0 * kKeys + at;
-    KeyWalk walk[4] = {KeyWalk(p, first), KeyWalk(p, first + 1), KeyWalk(p, first + 2), KeyWalk(p, first + 3)};
+    const KeyWalk w0(p, first), w1(p, w0), w2(p, w1), w3(p, w2);
+    KeyWalk walk[4] = {w0, w1, w2, w3};
     uint32_t page[4];
     auto look_up = [&](uint32_t kt) {
 #pragma unroll
@@ -323,14 +333,6 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
       }
     };
     look_up(g.kt0);
-    // The segment's queries into L2: the softmax warps come to them up to two
-    // tiles later, and would wait for HBM.
-    for (uint32_t r = lane; r < NR && g.rt * NR + r < g.s.rows; r += 32) {
-      const uint32_t row = g.rt * NR + r, tok = row / p.H;
-      const uint16_t* q = p.q + (g.s.q0 + static_cast<long long>(tok)) * p.q_tok + (row - tok * p.H) * p.q_head;
-#pragma unroll
-      for (int i = 0; i < kWidth; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
-    }
     for (uint32_t kt = g.kt0; kt < g.kt1 && alive; ++kt, ++tile) {
       int32_t rows[4];
 #pragma unroll
@@ -381,6 +383,15 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
           tma_gather4_2d(dst + lane * 4 * row_bytes, map, bar, c * 128, rows[0], rows[1], rows[2], rows[3]);
         else if (lane < boxes)
           tma_load_2d(dst + lane * p.box_rows * row_bytes, map, bar, c * 128, rows[0]);
+      }
+      if (kt != g.kt0) continue;
+      // Behind the first copies the segment's queries into L2: the softmax warps come to them up to
+      // two tiles later, and would wait for HBM.
+      for (uint32_t r = lane; r < NR && g.rt * NR + r < g.s.rows; r += 32) {
+        const uint32_t row = g.rt * NR + r, tok = row / p.H;
+        const uint16_t* q = p.q + (g.s.q0 + static_cast<long long>(tok)) * p.q_tok + (row - tok * p.H) * p.q_head;
+#pragma unroll
+        for (int i = 0; i < kWidth; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
       }
     }
   }
@@ -1147,17 +1158,25 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  unsigned long long before = 0, steps = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += pro.warp_sum[w];
-    steps += pro.warp_sum[w];
+  // (Every launch waits for its instructions here: as few of them as will do.)
+  unsigned long long before, steps;
+  {
+    unsigned long long sum = lane < kThreads / 32 ? pro.warp_sum[lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    before = __shfl_sync(0xffffffffu, sum, max(warp - 1, 0));
+    if (warp == 0) before = 0;
+    steps = __shfl_sync(0xffffffffu, sum, 31);
   }
   // CTAs with a share: all, or the first of them when there are fewer steps.  A
   // share of nothing but start steps stays idle: no row tile's key tiles lie on both
   // sides of it.
   const uint32_t ctas = static_cast<uint32_t>(min(static_cast<unsigned long long>(gridDim.x), steps));
-  const unsigned long long u0 = blockIdx.x < ctas ? steps * blockIdx.x / ctas : 0;
-  const unsigned long long u1 = blockIdx.x < ctas ? steps * (blockIdx.x + 1) / ctas : 0;
+  const unsigned long long u0 = blockIdx.x < ctas ? divide(steps * blockIdx.x, ctas) : 0;
+  const unsigned long long u1 = blockIdx.x < ctas ? divide(steps * (blockIdx.x + 1), ctas) : 0;
   unsigned long long start = before + incl - mine;
   if (u0 < u1 && start <= u0 && u0 < start + mine) {
     for (uint32_t b = b0; b < b1; ++b) {
@@ -1168,8 +1187,9 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
       if (u0 < start + here) {
         pro.start.left = u1 - u0;
         pro.start.b = b;
-        pro.start.rt = static_cast<uint32_t>((u0 - start) / each);
-        pro.start.at = static_cast<uint32_t>((u0 - start) % each);
+        const unsigned long long rt = divide(u0 - start, each);
+        pro.start.rt = static_cast<uint32_t>(rt);
+        pro.start.at = static_cast<uint32_t>(u0 - start - rt * each);
         break;
       }
       start += here;
