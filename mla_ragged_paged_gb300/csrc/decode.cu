@@ -141,9 +141,9 @@ struct Rows {
   static constexpr int kRegs = kThreads == 640 ? 96 : 72;
   static constexpr int kCols = NR / kGroups;      // rows of one softmax warpgroup
   static constexpr uint32_t kQChunk = 2 * NR * 128;
-  // P: a row of codes per key.  64 rows: an array of 64-byte rows per term; 32
-  // rows: both terms side by side in one.
-  static constexpr uint32_t kPBytes = kKeys * 2 * NR;
+  // P: a row of codes per key.  64 rows: an array of 64-byte rows per term; fewer: both terms
+  // side by side in one, 32 bytes apart.
+  static constexpr uint32_t kPBytes = kKeys * (NR == 64 ? 128 : 64);
   static constexpr uint32_t kPTerm = NR == 64 ? kKeys * 64 : 32;  // bytes from the first term to the second
   // What fits: 8 latent chunks are two tiles.
   static constexpr uint32_t kSlots = NR <= 32 ? 10 : 8, kRopeSlots = NR <= 32 ? 2 : 1;
@@ -196,6 +196,7 @@ template <int NR, bool FP4>
 using DecodeSmem = std::conditional_t<FP4, DecodeSmem4<NR>, DecodeSmem8<NR>>;
 static_assert(sizeof(DecodeSmem4<64>) <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem4<32>) <= 232448, "decode shared memory");
+static_assert(sizeof(DecodeSmem4<16>) <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem8<64>) + 1024 <= 232448, "decode shared memory");
 static_assert(sizeof(DecodeSmem8<32>) + 1024 <= 232448, "decode shared memory");
 
@@ -839,7 +840,7 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
         if constexpr (NR == 32 && N == 16) {
           *reinterpret_cast<uint4*>(row + ((group ^ swz) << 4)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
           *reinterpret_cast<uint4*>(row + (((2 + group) ^ swz) << 4)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-        } else if constexpr (NR == 32) {
+        } else if constexpr (NR <= 32) {
           uint8_t* at = row + 8 * (group & 1);
           *reinterpret_cast<uint2*>(at + (((group >> 1) ^ swz) << 4)) = make_uint2(t1[0], t1[1]);
           *reinterpret_cast<uint2*>(at + (((2 + (group >> 1)) ^ swz) << 4)) = make_uint2(t2[0], t2[1]);
@@ -1263,6 +1264,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   __shared__ JoinSum sums[WARP ? 1 : kJoinWarps][32];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   uint32_t c = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the whole decode kernel and what it wrote
   if constexpr (!WARP) {
     uint32_t nth = blockIdx.x;
     c = p.ctas;
@@ -1357,9 +1359,17 @@ mla_status_t launch_decode(DecodeParams& p, int dev, int sms, int slot, cudaStre
   // row to join: 1 x 131072 x 16 heads 38 / 116, 4 x 32768 x 128 heads 54 / 63, 16 x 8000 x
   // 40 heads 42 / 45, 30 x 4000 x 64 heads 45 / 41, 64 x 4500 x 128 heads 137 / 108.)
   const uint64_t tiles = static_cast<uint64_t>(p.Tq) * p.H / NR + std::min(p.B, p.Tq);
-  if (tiles > kFewTiles) decode_join_kernel<true><<<dim3(ctas, NR / kJoinWarps), 32 * kJoinWarps, 0, stream>>>(p, NR);
-  else decode_join_kernel<false><<<dim3(static_cast<uint32_t>(tiles), NR), 32 * kJoinWarps, 0, stream>>>(p, NR);
-  e = cudaGetLastError();
+  // Launched while the decode kernel ends, whose end it waits for itself: 2 us less a call.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t join = {};
+  join.gridDim = tiles > kFewTiles ? dim3(ctas, NR / kJoinWarps) : dim3(static_cast<uint32_t>(tiles), NR);
+  join.blockDim = dim3(32 * kJoinWarps);
+  join.stream = stream;
+  join.attrs = &early;
+  join.numAttrs = 1;
+  e = cudaLaunchKernelEx(&join, tiles > kFewTiles ? decode_join_kernel<true> : decode_join_kernel<false>, p, static_cast<uint32_t>(NR));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode join launch: %s", cudaGetErrorString(e));
   return MLA_OK;
 }
@@ -1552,5 +1562,7 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   p.box_rows = static_cast<uint32_t>(box_rows);
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return rows <= 32 ? launch_decode<32, true>(p, dev, sms, 16, s) : launch_decode<64, true>(p, dev, sms, 17, s);
+  return rows <= 16   ? launch_decode<16, true>(p, dev, sms, 19, s)
+         : rows <= 32 ? launch_decode<32, true>(p, dev, sms, 16, s)
+                      : launch_decode<64, true>(p, dev, sms, 17, s);
 }
