@@ -345,10 +345,11 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
         walk[e].next(p);
       }
       look_up(kt + 1);
-      if (boxed && lane < boxes) {
+      if (!FP4 && boxed && lane < boxes) {
         // The tile's shared memory comes free chunk by chunk, most of a tile's time
         // from now; into L2 the rows can come at once (measured: 118 -> 108 us
-        // for 152 sequences x 4500 x 64 heads).
+        // for 152 sequences x 4500 x 64 heads; 4-bit rows gain nothing by it, and in boxes of
+        // 8 rows it cost 64 sequences of 4500 with 16 heads 72 us in the place of 58).
 #pragma unroll
         for (int c = 0; c < kBodies; ++c) tma_prefetch_2d(&p.tm_latent, c * 128, rows[0]);
         tma_prefetch_2d(&p.tm_rope, kBodies * 128, rows[0]);
@@ -1200,16 +1201,8 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   Share sh = {};
   if (u0 < u1) sh = pro.start;
   __syncthreads();     // the scratch becomes query space
-  auto issue = [&] {
-    if (warp > 0 && elect_one()) {
-      if (warp == 1) issue_scores<NR, FP4>(s, p, sh, tmem, abort);
-      else issue_output<NR, FP4>(s, p, sh, tmem, 2 * (warp - 2), abort);
-      drain_umma(&s.drain[warp - 1]);
-    }
-    __syncwarp();
-  };
-  // Registers, of what the block was launched with: 640 x 96 = 128 x 64 + 512 x 104; 4-bit: 896 x 72 = 128 x 40 + 512 x 88 +
-  // 256 x 56 (64-row tiles) = 128 x 40 + 256 x 104 + 512 x 64 (32-row tiles).
+  // Registers, of what the block was launched with: 640 x 96 = 128 x 64 + 512 x 104; 4-bit: = 128 x 64 + 256 x 128 + 256 x 80,
+  // 64-row tiles 896 x 72 = 128 x 40 + 512 x 88 + 256 x 56.
   if (warp < 4) {
     if constexpr (kThreads == 896) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -1547,7 +1540,7 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
   fill_params(p, out, lse, q, cache, page_table, row_offsets, cache_lens, scale, mask, status, workspace);
   int64_t box_rows = 1;
   while (box_rows < kKeys && P % (2 * box_rows) == 0) box_rows *= 2;
-  if (box_rows < 8) box_rows = 1;   // row gathers take a one-row box
+  if (box_rows < 4) box_rows = 1;   // row gathers, of four rows each, take a one-row box
   {
     const uint64_t dims[2] = {kRow4Bytes, static_cast<uint64_t>(NP * P)};
     const uint64_t str[1] = {static_cast<uint64_t>(pitch)};
