@@ -357,8 +357,11 @@ __device__ void decode_producer(DecodeSmem<NR, FP4>& s, const DecodeParams& p, S
       for (int i = 0; i <= kBodies && alive; ++i) {
         const int c = FP4 ? (i + kBodies) % (kBodies + 1) : i;   // kBodies: the tail
         const bool body = c < kBodies;
-        const uint32_t pos = body ? tile * kBodies + c : tile, ring = body ? kBodySlots : R::kRopeSlots;
-        const uint32_t slot = pos % ring, phase = (pos / ring) & 1u;
+        // (Each ring's length is a constant here: dividing by a selected one cost the 8-bit kernel 76 -> 91 us for
+        // 4 sequences of 131072 with 32 queries.)
+        const uint32_t pos = body ? tile * kBodies + c : tile;
+        const uint32_t slot = body ? pos % kBodySlots : pos % R::kRopeSlots;
+        const uint32_t phase = (body ? pos / kBodySlots : pos / R::kRopeSlots) & 1u;
         uint64_t *full, *empty = body ? &s.empty[slot] : &s.rope_empty[slot];
         uint32_t dst = smem_u32(s.rope[body ? 0 : slot]);
         if constexpr (FP4) {
