@@ -239,8 +239,9 @@ struct RopeItems {
   }
 };
 
-template <bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads, HALVES ? 4 : 5) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+// WIDE: a side has rows of more than one item a lane, which take more registers.
+template <bool HALVES, bool WIDE>
+__global__ void __launch_bounds__(kRopeThreads, HALVES && WIDE ? 4 : 5) norm_rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) float2 turn[];  // [tokens of the block][pairs]
   const bool keys = blockIdx.x >= p.side[0].blocks;
   const RopeSide& sd = p.side[keys];
@@ -267,8 +268,12 @@ __global__ void __launch_bounds__(kRopeThreads, HALVES ? 4 : 5) norm_rope_kernel
   switch (sd.form & 15u) {
     case 4: return by_items(RopeItems<HALVES, 1, 1>());
     case 4 + 2: return by_items(RopeItems<HALVES, 1, HALVES ? 2 : 4>());
-    case 8 + 1: return by_items(RopeItems<HALVES, 2, 2>());
-    case 12: return by_items(RopeItems<HALVES, 4, 1>());
+    case 8 + 1:
+      if constexpr (WIDE) by_items(RopeItems<HALVES, 2, 2>());
+      return;
+    case 12:
+      if constexpr (WIDE) by_items(RopeItems<HALVES, 4, 1>());
+      return;
     default: form_angles(); rope_rows_by_elements(p, sd, bl, turn);
   }
 }
@@ -369,6 +374,8 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
       while (lanes < 32 && lanes < items) lanes *= 2;
       const uint32_t each = (items + lanes - 1) / lanes, groups = kRopeThreads / lanes;
       // (The angles of a block's tokens lie in shared memory.)
+      // (The angles of a block's tokens lie in shared memory.  Halves have two loads a row; 5003 tokens x 40 heads of 128 took
+      // 28 us with one row a lane, 26 with two.)
       const bool many = T * sd.heads > static_cast<int64_t>(groups) * 8 * sms && 4 * groups / sd.heads * p.pairs <= 2048;
       const uint32_t rows = each == 1 ? (many ? (p.halves ? 2 : 4) : 1) : each == 2 ? 2 : 1;
       sd.form = lanes << 4 | (each > 2 ? 3u : each) << 2 | (each == 1 && many ? 2u : rows - 1);
@@ -382,9 +389,11 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
     const uint32_t toks = std::min<uint32_t>(sd.rows_per_block, (sd.rows_per_block + 2 * sd.heads - 2) / sd.heads);
     smem = std::max(smem, sizeof(float2) * toks * p.pairs);
   }
-  const auto kernel = p.halves ? norm_rope_kernel<true> : norm_rope_kernel<false>;
+  const bool wide = ((p.side[0].form | p.side[1].form) & 8u) != 0;
+  const auto kernel = p.halves ? (wide ? norm_rope_kernel<true, true> : norm_rope_kernel<true, false>)
+                               : (wide ? norm_rope_kernel<false, true> : norm_rope_kernel<false, false>);
   if (smem > 48 * 1024 && (st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem), dev,
-                                                     p.halves ? 15 : 18)) != MLA_OK)
+                                                     p.halves ? (wide ? 15 : 20) : wide ? 18 : 21)) != MLA_OK)
     return st;
   kernel<<<p.side[0].blocks + p.side[1].blocks, kRopeThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   cudaError_t e = cudaGetLastError();
