@@ -1,4 +1,4 @@
-// Attention of new tokens over a paged 8-bit latent cache (the absorbed form
+// Attention of new tokens over a paged 8-bit or 4-bit latent cache (the absorbed form
 // of MLA: every head's query is already in the latent space):
 //   c_j = s_j * code_j          cached row j of the sequence, s_j its scale
 //   x_j = scale * q . c_j       q [576] = [latent 512 | rope 64]
@@ -9,11 +9,26 @@
 // is up to 64 (token, head) queries.  A cached row costs 576 bytes and 2 * 1088
 // flops per query: up to about 60 queries a sequence the kernel is bound by
 // HBM, above that by the tensor cores and their shared-memory operands.  Measured:
-// 4 sequences of 131072 with 32 queries each 72 us (4.2 TB/s; 6.3 in the steady
-// state, 17 us of start, segment ends and joining); 64 of 4500 with 128 queries 107 us
-// (4.1 k cycles a tile of 64 queries, 2.7 k of them tensor-core work: shared memory has
+// 4 sequences of 131072 with 32 queries each 73 us (4.2 TB/s; 6.3 in the steady
+// state, 17 us of start, segment ends and joining); 64 of 4500 with 128 queries 106 us
+// (4 k cycles a tile of 64 queries, 2.7 k of them tensor-core work: shared memory has
 // room for two key tiles and one tile of weights, so load, scores, softmax and output
 // wait for one another).
+//
+// 4-bit rows (latent_fp4.cuh).  An element is e2m1 times a power of two, and e2m1 * 2^(6 - shift)
+// is an e4m3 code exactly, in units of 2^(E - 133) for the row: warps of their own make the
+// codes in shared memory, where they lie as an 8-bit row's would, the exponent takes the
+// scale's place, and all that follows is the same.  Half the bytes and no fewer UMMAs, and
+// a tile's 73 728 codes on top: a table in two words per shift and byte permutations, 9
+// instructions for 8 codes, 2.6 k of the 10.9 k (32-row tiles) or 17.6 k (64-row) that a
+// tile takes.  Measured: 64 sequences of 4500 with 16 heads 50 us (8-bit 52), with 128
+// heads 129 us (106), 4 of 131072 with 32 queries 83 us (73).  A tile takes 4.7 k cycles
+// (32 rows) or 6.5 k (64): codes 3 to 4 k, softmax 3.3 or 5 k, UMMAs 2.1 or 2.7 k, one
+// behind the other for a tile and beside one another for neighbours, as far as a ring of
+// 2 to 2.5 tiles lets them; without any one of them the time falls by 4 to 11 %.  Kept out:
+// rows by plain loads into registers (158 us for 4 x 131072; a spilt register waits for its
+// load), a ring of raw chunks beside the codes' (108), 16 code warps (95 against 88), four
+// softmax warpgroups for 32 rows (95 against 88).
 //
 // Tensor cores.  The cached codes go from HBM to the tensor cores as they are:
 // keys are the 128-row operand of both products, so few queries waste no
@@ -1556,6 +1571,9 @@ extern "C" mla_status_t mla_decode_latent_fp4(const mla_tensor_t* out, const mla
       return st;
   }
   p.box_rows = static_cast<uint32_t>(box_rows);
+  // The smallest row tile that holds an average sequence's queries (us in tiles of 16 / 32 / 64 rows, 64 sequences of
+  // 4500 with 16 heads 50 / 58 / 78, 32 heads - / 58 / 81, 64 heads - / 101 / 79, 72 heads - / 140 / 134, 128 heads
+  // - / 183 / 132).
   const uint64_t rows = (static_cast<uint64_t>(Tq) + B - 1) / B * H;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return rows <= 16   ? launch_decode<16, true>(p, dev, sms, 19, s)

