@@ -380,7 +380,6 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
       uint32_t lanes = 4;
       while (lanes < 32 && lanes < items) lanes *= 2;
       const uint32_t each = (items + lanes - 1) / lanes, groups = kRopeThreads / lanes;
-      // (The angles of a block's tokens lie in shared memory.)
       // (The angles of a block's tokens lie in shared memory.  Halves have two loads a row; 5003 tokens x 40 heads of 128 took
       // 28 us with one row a lane, 26 with two.)
       const bool many = T * sd.heads > static_cast<int64_t>(groups) * 8 * sms && 4 * groups / sd.heads * p.pairs <= 2048;

@@ -76,7 +76,8 @@ def _u32(pos):
     (1, 1, 2, 0, 1), (1, 1, 1, 1, 0), (3, 2, 7, 7, 3), (1, 128, 64, 0, 32), (5, 1, 576, 512, 32), (70, 3, 128, 128, 64),
     (33, 128, 64, 0, 32), (257, 1, 576, 512, 32), (19, 5, 80, 80, 20), (4, 7, 50, 50, 12), (9, 2, 192, 0, 32),
     (2, 3, 1024, 1024, 512), (6, 4, 1024, 1000, 8), (40, 2, 48, 0, 24), (11, 1, 1023, 1000, 500), (300, 12, 96, 96, 0),
-    (3, 200, 256, 256, 16), (130, 1, 64, 64, 32), (64, 9, 8, 8, 4), (1000, 2, 136, 136, 68), (5, 3, 576, 40, 32)])
+    (3, 200, 256, 256, 16), (130, 1, 64, 64, 32), (64, 9, 8, 8, 4), (1000, 2, 136, 136, 68), (5, 3, 576, 40, 32),
+    (40, 1, 1024, 1024, 512), (350, 300, 64, 64, 32)])
 @pytest.mark.parametrize("halves", [False, True])
 def test_norm_rope(lib, T, H, D, norm, pairs, halves):
     from mla_ragged_paged_gb300 import binding
@@ -92,7 +93,7 @@ def test_norm_rope(lib, T, H, D, norm, pairs, halves):
 
 
 @pytest.mark.parametrize("T,Hq,Dq,Hk,Dk", [(1, 128, 64, 1, 576), (300, 128, 64, 1, 576), (77, 12, 128, 3, 128),
-                                           (5003, 1, 64, 1, 64), (10, 3, 70, 2, 66)])
+                                           (5003, 1, 64, 1, 64), (10, 3, 70, 2, 66), (50, 257, 64, 2, 70), (30, 1, 70, 1, 576)])
 @pytest.mark.parametrize("halves", [False, True])
 def test_norm_rope_queries_and_keys(lib, T, Hq, Dq, Hk, Dk, halves):
     from mla_ragged_paged_gb300 import binding
