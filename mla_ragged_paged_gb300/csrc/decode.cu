@@ -92,6 +92,7 @@ constexpr uint32_t kChunk = kKeys * 128;      // 16 KB: 128 keys x 128 latent di
 constexpr uint32_t kRopeBytes = kKeys * 64;
 constexpr uint32_t kMaxCtas = 160;            // what the workspace has room for
 constexpr uint32_t kMaxRows = 64;
+constexpr uint32_t kPartValues = 4;           // of a row of a part
 constexpr uint32_t kColS = 256;               // tensor memory: O [0, 256), two S tiles from here
 constexpr float kShift = 7.f;                 // w = 2^(y - mu + kShift)
 constexpr float kSmall = 0x1p-6f;             // weights below it (e4m3's normal numbers end there) are summed unrounded
@@ -100,13 +101,24 @@ constexpr float kDrop = 12.f;                 // and falls when a tile's maximum
 constexpr float kMargin = 2.f;                // in both cases to that far above the maximum
 constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
-// The sum is kept as sum 2^(x - mu - kSumShift): with scales from 1e-33 to
-// 1e27 neither end leaves fp32.
+// The sum is kept as sum 2^(x - mu - kSumShift + up): each weight, at most 2^8.5, times 2^(up - 37) / s_j.
+// With M the largest scale's exponent in a segment's first key tile, up = M + 21 (0 below), so that for
+// scales within 2^110 of each other the factor lies between 2^-126 and 2^94, and neither end leaves
+// fp32.  (Always 2^-37 / s_j, it vanished for scales from 2^89 on, and with it the output.)
 constexpr float kSumShift = 30.f;
+constexpr float kSumRoom = 21.f;
 // Steps that beginning a row tile counts for: its queries, pipeline fill and result take as
 // long as about four key tiles.
 constexpr uint32_t kStartSteps = 4;
-constexpr float kUnit = 0x1p-37f;             // 2^-(kShift + kSumShift): out = O / l in these units
+
+// 2^k for a whole k from -126 to 127.
+__device__ __forceinline__ float whole_power(float k) { return __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(k)) << 23); }
+// log2 of a sum of weights in units of 2^(mu + kSumShift - up).
+__device__ __forceinline__ float log2_sum(float mu, float up, float sum) {
+  const float shift = kSumShift - up;
+  const bool large = sum > 0x1p90f;
+  return mu + log2f(large ? sum : sum * whole_power(shift)) + (large ? shift : 0.f);
+}
 
 // a / b; a short division where it does.
 __device__ __forceinline__ unsigned long long divide(unsigned long long a, uint32_t b) {
@@ -136,7 +148,7 @@ struct DecodeParams {
   const uint32_t* lens;
   uint32_t* status;
   PartHeader* headers;             // [2 * kMaxCtas]
-  float* part_ml;                  // [slots][3][kMaxRows]: mu, the sum of the weights, and the sum that divides O
+  float* part_ml;                  // [slots][kPartValues][kMaxRows]: mu, the sum of the weights, the sum that divides O, up
   float* part_o;                   // [slots][kMaxRows][512]
   float sl2;                       // scale * log2(e)
   uint32_t step_col, step_off;     // kKeys = step_col * P + step_off
@@ -175,6 +187,7 @@ struct __align__(1024) DecodeSmem8 {
   uint8_t p[R::kPBytes];
   float warp_red[R::kGroups][4][R::kCols];
   float row_val[R::kGroups][R::kCols];
+  uint32_t warp_scale[R::kGroups][4];         // largest scale's exponent + 128, 0: none
   float col_factor[NR];
   uint64_t full[R::kSlots], empty[R::kSlots];
   uint64_t rope_full[R::kRopeSlots], rope_empty[R::kRopeSlots];
@@ -197,6 +210,7 @@ struct __align__(1024) DecodeSmem4 {
   uint8_t p[R::kPBytes];
   float warp_red[R::kGroups][4][R::kCols];
   float row_val[R::kGroups][R::kCols];
+  uint32_t warp_scale[R::kGroups][4];         // largest scale's exponent + 128, 0: none
   float col_factor[NR];
   uint2 table[16];                            // the e4m3 forms of a block's codes, by its shift
   static constexpr uint32_t kExponents = (R::kHalves + 1) / 2;
@@ -699,7 +713,27 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+    {
+      uint32_t e = 0;
+      if constexpr (FP4) {
+        const Place<NR, FP4> at(tile, 0);
+        softmax_wait(smem_u32(&s.full[at.slot / 2]), at.phase, abort);
+        e = s.key_e[tile % DecodeSmem4<NR>::kExponents][key];
+        e = e <= kFp4MostE ? max(e, 13u) - 5u : 0u;
+      } else if (ok_next && sc_next < INFINITY) {
+        e = __float2uint_ru(__log2f(fmaxf(sc_next, 0x1p-120f)) + 128.f);
+      }
+      e = __reduce_max_sync(0xffffffffu, e);
+      if (lane == 0) s.warp_scale[group][quarter] = e;
+    }
     named_bar_sync(1 + kGroups, 128 * kGroups);          // col_factor is written by all warpgroups
+    float up;
+    {
+      uint32_t e = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e = max(e, s.warp_scale[group][i]);
+      up = fmaxf(static_cast<float>(min(e, 255u)) - (128.f - kSumRoom), 0.f);
+    }
     float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
     uint32_t look = g.kt0 + 2;                           // form the maxima in all tiles before this one
     // Pairs of neighbouring rows go through packed arithmetic (the same roundings, half the instructions).
@@ -728,7 +762,7 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
         sc = e == kFp4NanE ? __uint_as_float(0x7FC00000u) : __uint_as_float((max(e, 13u) - 6u) << 23);
         ls = static_cast<float>(static_cast<int>(max(e, 13u)) - 133);
       }
-      const float to_sum = ex2_approx(-kShift - kSumShift - ls);
+      const float to_sum = ex2_approx((-kShift - kSumShift - ls) + up);
       tc_fence_after();
       uint64_t y[N / 2];
       {
@@ -928,17 +962,18 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
     const uint32_t slot = 2 * blockIdx.x + (begins ? 1 : 0);
     const uint32_t row = first_row + r0 + my_row;
     if (quarter == 0 && lane < N) {
-      // 2^(mu - kShift) and 2^(mu + kSumShift) are the units of O and l.
-      s.row_val[group][lane] = seen != 0.f ? kUnit / seen : 0.f;
+      // 2^(mu - kShift) and 2^(mu + kSumShift - up) are the units of O and l: out = O / l times the quotient.
+      s.row_val[group][lane] = seen != 0.f ? whole_power(up - kShift - kSumShift) / seen : 0.f;
       if (!whole) {
-        float* ml = p.part_ml + static_cast<size_t>(slot) * 3 * kMaxRows + r0 + lane;
+        float* ml = p.part_ml + static_cast<size_t>(slot) * kPartValues * kMaxRows + r0 + lane;
         ml[0] = mu;
         ml[kMaxRows] = total;
         ml[2 * kMaxRows] = seen;
+        ml[3 * kMaxRows] = up;
       } else if (p.lse && row < g.s.rows) {
         const uint32_t tok = row / p.H;
         p.lse[(g.s.q0 + static_cast<long long>(tok)) * p.l_tok + (row - tok * p.H) * p.l_head] =
-            total != 0.f ? (mu + log2f(total * 0x1p30f)) * kLn2 : -INFINITY;
+            total != 0.f ? log2_sum(mu, up, total) * kLn2 : -INFINITY;
       }
     }
     named_bar_sync(bar, 128);
@@ -1294,22 +1329,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   const uint32_t lo = p.ro[h.b], row = h.rt * nr + r;
   if (row >= (p.ro[h.b + 1] - lo) * p.H) return;
   const uint32_t tok = row / p.H, head = row - tok * p.H;
-  float m = -INFINITY;
-  for (uint32_t i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[static_cast<size_t>(part_slot(c, i)) * 3 * kMaxRows + r]);
+  float m = -INFINITY, up = 0.f;
+  for (uint32_t i = lane; i < parts; i += 32) {
+    const float* ml = p.part_ml + static_cast<size_t>(part_slot(c, i)) * kPartValues * kMaxRows + r;
+    m = fmaxf(m, ml[0]);
+    up = fmaxf(up, ml[3 * kMaxRows]);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  up = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(up)));   // (not negative: its bits order as it does)
   JoinSum a = {};
 #pragma unroll 2
   for (uint32_t i = WARP ? 0 : warp; i < parts; i += WARP ? 1 : kJoinWarps) {
     const size_t s = part_slot(c, i);
-    const float* ml = p.part_ml + s * 3 * kMaxRows + r;
+    const float* ml = p.part_ml + s * kPartValues * kMaxRows + r;
     const float* src = p.part_o + (s * kMaxRows + r) * kLatent + 4 * lane;
-    const float mi = ml[0], li = ml[kMaxRows], qi = ml[2 * kMaxRows];
+    const float mi = ml[0], ui = ml[3 * kMaxRows];
+    float li = ml[kMaxRows], qi = ml[2 * kMaxRows];
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4*>(src + 128 * k);
     if (li != 0.f) {
       const float f = exp2f(mi - m);
+      if (ui != up) {
+        const float to_up = whole_power(fminf(up - ui, 127.f));
+        li *= to_up;
+        qi *= to_up;
+      }
       a.l = fmaf(li, f, a.l);
       a.lq = fmaf(qi, f, a.lq);
 #pragma unroll
@@ -1339,7 +1385,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
     }
   }
   uint16_t* out = p.out + (lo + static_cast<long long>(tok)) * p.o_tok + head * p.o_head + 4 * lane;
-  const float f = a.lq != 0.f ? kUnit / a.lq : 0.f;
+  const float f = a.lq != 0.f ? whole_power(up - kShift - kSumShift) / a.lq : 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     *reinterpret_cast<uint2*>(out + 128 * k) =
@@ -1347,11 +1393,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
                     : make_uint2(0u, 0u);
   if (lane == 0 && p.lse)
     p.lse[(lo + static_cast<long long>(tok)) * p.l_tok + head * p.l_head] =
-        a.l != 0.f ? (m + log2f(a.l * 0x1p30f)) * kLn2 : -INFINITY;
+        a.l != 0.f ? log2_sum(m, up, a.l) * kLn2 : -INFINITY;
 }
 
 constexpr size_t kHeaderBytes = (sizeof(PartHeader) * kMaxCtas + 255) / 256 * 256;
-constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * 3 * kMaxRows;
+constexpr size_t kMlBytes = sizeof(float) * 2 * kMaxCtas * kPartValues * kMaxRows;
 constexpr size_t kWorkspace = kHeaderBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * kLatent;
 
 template <int NR, bool FP4>

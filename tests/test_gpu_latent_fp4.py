@@ -853,3 +853,45 @@ def test_decode_wait_timeout_sets_status_and_context_survives(lib, heads, P):
     out, lse = _run_decode(d2, status=status)
     assert int(status) == 0
     _check_decode(d2, out, lse)
+
+
+# ------------------------------------------------------------------ the ends of the exponents
+
+def _set_exponents(d, lo, hi, seed):
+    """Every cached row an exponent E of its own in lo .. hi."""
+    g = torch.Generator().manual_seed(seed)
+    e = d.raw[..., WIDTH // 2]
+    kept = e != 255
+    e[kept] = torch.randint(lo, hi + 1, (int(kept.sum()),), generator=g).to(torch.uint8)
+
+
+@pytest.mark.parametrize("lo,hi,q_std", [(223, 232, 2.0 ** -106), (200, 232, 2.0 ** -106), (122, 232, 2.0 ** -106),
+                                         (245, 252, 0.0), (142, 252, 0.0), (27, 36, 1.0), (27, 137, 0.0)])
+@pytest.mark.parametrize("n,prior,heads", [([1, 2], [1500, 300], 20), ([1], [9000], 16), ([1] * 170, [100] * 170, 40)])
+def test_decode_rows_of_every_exponent(lib, n, prior, heads, lo, hi, q_std):
+    """Rows near 2^125 and near 2^-100, within 110 of each other: the sums of the weights stay in range, in
+    row tiles that one CTA takes whole and in joined ones."""
+    d = DecodeFp4(n, prior, heads, 64, seed=hi, q_std=q_std)
+    _set_exponents(d, lo, hi, lo)
+    out, lse = _run_decode(d)
+    if hi < 64:
+        # The absolute part of the tolerance, made for rows near one, is above these: checked as the same
+        # rows times 2^60 (exactly: a power of two).
+        d.raw[..., WIDTH // 2][d.raw[..., WIDTH // 2] != 255] += 60
+        out, d.q = out.float() * 2.0 ** 60, (d.q.float() * 2.0 ** -60).to(torch.bfloat16)
+    _check_decode(d, out, lse)
+
+
+def test_decode_exponents_that_rise_and_fall(lib):
+    """The largest rows first, last and in the middle of a sequence, for one token alone and beside
+    keys that no row sees."""
+    d = DecodeFp4([1, 1, 1, 3], [3000, 3000, 3000, 257], 16, 16, seed=5, q_std=2.0 ** -106)
+    for b in range(4):
+        L = d.prior[b] + d.n[b]
+        pos = torch.arange(L)
+        e = {0: 232 - pos * 100 // L, 1: 132 + pos * 100 // L, 2: 232 - (pos - L // 2).abs() * 100 // L,
+             3: torch.where(pos >= L - 2, 252, 150)}[b]
+        d.raw[d.table[b, pos // d.P].long(), pos % d.P, WIDTH // 2] = e.to(torch.uint8)
+    d.q[3:] = 0
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)

@@ -500,6 +500,24 @@ def test_decode_scales_far_apart(lib, n, prior, spread):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("lo,hi,q_std", [(86, 110, 2.0 ** -106), (8, 117, 0.0), (105, 117, 0.0), (0, 110, 2.0 ** -106),
+                                         (-120, -119.9, 0.0), (-119, -112, 1.0), (-108, -100, 0.0)])
+@pytest.mark.parametrize("n,prior", [([1, 2], [1500, 300]), ([1], [9000]), ([1] * 170, [100] * 170)])
+def test_decode_scales_of_every_size(lib, n, prior, lo, hi, q_std):
+    """Scales 2^lo .. 2^hi: neither the sums of the weights nor their logarithm leave fp32."""
+    d = Decode(n, prior, 20, 64, seed=46, q_std=q_std)
+    g = torch.Generator().manual_seed(int(hi) + 200)
+    kept = ~torch.isnan(d.scales)
+    d.scales[kept] = torch.exp2(torch.empty(int(kept.sum())).uniform_(lo, hi, generator=g))
+    out, lse = _run_decode(d)
+    # The absolute part of the tolerance, made for scales near one, is far above these rows: checked as
+    # the same rows times 2^60 (exactly: a power of two).
+    if hi < 0:
+        d.scales, out = d.scales * 2.0 ** 60, (out.float() * 2.0 ** 60)
+        d.q = (d.q.float() * 2.0 ** -60).to(torch.bfloat16)
+    _check_decode(d, out, lse)
+
+
 @pytest.mark.parametrize("q_std", [0.0, 1.0])
 @pytest.mark.parametrize("lengths,zeros", [
     ([2], "late"), ([2], "early"), ([300], "early"), ([300], "late"), ([300], "odd"), ([5000], "odd"), ([5000], "early"),
