@@ -392,7 +392,7 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
     }
     sd.blocks = static_cast<uint32_t>((T * sd.heads + sd.rows_per_block - 1) / sd.rows_per_block);
     // The rows of a block begin in any head of a token.
-    const uint32_t toks = std::min<uint32_t>(sd.rows_per_block, (sd.rows_per_block + 2 * sd.heads - 2) / sd.heads);
+    const uint32_t toks = std::min<uint32_t>(sd.rows_per_block, (sd.rows_per_block + 2ull * sd.heads - 2) / sd.heads);
     smem = std::max(smem, sizeof(float2) * toks * p.pairs);
   }
   const bool wide = ((p.side[0].form | p.side[1].form) & 8u) != 0;

@@ -221,6 +221,24 @@ def test_norm_rope_no_tokens_and_other_stream(lib):
         binding.norm_rope(p[:-1], f_d, q=dev, q_out=a)
 
 
+@pytest.mark.parametrize("heads", [2 ** 31 - 1, 2 ** 31 - 15])
+def test_norm_rope_most_heads(lib, heads):
+    """As many heads as a call takes: the angles' place is counted in 64 bits."""
+    from mla_ragged_paged_gb300 import binding
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough memory")
+    part = 1 << 20
+    base, w, f, pos = _rope_inputs(1, part, 2, 2, 1, 13)
+    buf = torch.empty(2048, part * 2, dtype=torch.bfloat16, device="cuda")
+    buf[:] = base.cuda().view(1, -1)
+    q = buf.view(-1)[:2 * heads].view(1, heads, 2)
+    binding.norm_rope(_u32(pos), f.cuda(), q=q, q_out=q, q_weight=w.cuda())
+    _check_rope(q[:, :part], base, w, f, pos)
+    left = 2 ** 31 - heads
+    assert (buf[:-1] == buf[0]).all()
+    assert torch.equal(buf[-1, :-2 * left], buf[0, :-2 * left]) and torch.equal(buf[-1, -2 * left:].cpu(), base.view(-1)[-2 * left:])
+
+
 # ------------------------------------------------------------------ append and gather
 
 def _bf16_rows(n, W, seed, spread=2.0):
