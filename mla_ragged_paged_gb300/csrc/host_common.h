@@ -35,7 +35,8 @@ mla_status_t check_tensor(const mla_tensor_t* t, const char* name, int ndim, mla
                           bool empty_ok = false);
 
 // Allow `bytes` of dynamic shared memory for `func` on `device`, cached per
-// (device, slot): each kernel needs a slot of its own (0 plan, 1 scheduler,
+// (device, slot), the same `bytes` in every call of a slot (calls of several threads are
+// not ordered): each kernel needs a slot of its own (0 plan, 1 scheduler,
 // 2 / 3 / 4 attention bf16 / fp8 / fp8 with per-token K scales, 6 / 7 the last
 // two with two-term precision, 5 up-projection, 8 / 12 fp8 product, 9 .. 11 its
 // form for few tokens, 13 / 14 latent decode, 15 / 18 / 20 / 21

@@ -32,6 +32,10 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr uint32_t kRopeMaxDim = 1024;
+constexpr uint32_t kRopeElementRows = 32;  // of a block, element by element
+// The most that a block's angles take: those of one token for every row by elements (rows in items are
+// fewer, the wider they are: 64 KB at most).
+constexpr int kRopeMaxSmem = kRopeElementRows * (kRopeMaxDim / 2) * static_cast<int>(sizeof(float2));
 
 struct RopeSide {
   const uint16_t* x;
@@ -388,7 +392,7 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
       sd.rows_per_block = groups * rows;
     } else {
       sd.form = 0;
-      sd.rows_per_block = 32;
+      sd.rows_per_block = kRopeElementRows;
     }
     sd.blocks = static_cast<uint32_t>((T * sd.heads + sd.rows_per_block - 1) / sd.rows_per_block);
     // The rows of a block begin in any head of a token.
@@ -398,7 +402,8 @@ extern "C" mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tenso
   const bool wide = ((p.side[0].form | p.side[1].form) & 8u) != 0;
   const auto kernel = p.halves ? (wide ? norm_rope_kernel<true, true> : norm_rope_kernel<true, false>)
                                : (wide ? norm_rope_kernel<false, true> : norm_rope_kernel<false, false>);
-  if (smem > 48 * 1024 && (st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem), dev,
+  // (One limit for all sizes: threads that set different ones could leave the smaller.)
+  if (smem > 48 * 1024 && (st = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kRopeMaxSmem, dev,
                                                      p.halves ? (wide ? 15 : 20) : wide ? 18 : 21)) != MLA_OK)
     return st;
   kernel<<<p.side[0].blocks + p.side[1].blocks, kRopeThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);

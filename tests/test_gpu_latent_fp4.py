@@ -239,6 +239,46 @@ def test_norm_rope_most_heads(lib, heads):
     assert torch.equal(buf[-1, :-2 * left], buf[0, :-2 * left]) and torch.equal(buf[-1, -2 * left:].cpu(), base.view(-1)[-2 * left:])
 
 
+_THREADS = """
+import threading, torch
+from mla_ragged_paged_gb300 import binding
+# 64 KB of angles (1024 columns in items) and 128 KB (1024 columns two bytes past 16), halves and pairs.
+T = 64
+x = torch.randn(T, 1, 1024, device="cuda").to(torch.bfloat16)
+odd = torch.empty(T, 1, 1032, dtype=torch.bfloat16, device="cuda")[:, :, 1:1025]
+odd.copy_(x)
+f = torch.rand(512, device="cuda")
+pos = torch.arange(T, dtype=torch.int32, device="cuda")
+outs, errors = [torch.zeros(T, 1, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(16)], []
+torch.cuda.synchronize()
+start = threading.Barrier(16)
+def work(i):
+    try:
+        start.wait()
+        for _ in range(50):
+            binding.norm_rope(pos, f, q=odd if i & 1 else x, q_out=outs[i], interleaved=i & 2 == 0)
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=work, args=(i,)) for i in range(16)]
+[t.start() for t in threads], [t.join() for t in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+assert all(torch.equal(outs[i], outs[i & 2]) for i in range(16))
+"""
+
+
+def test_norm_rope_sizes_from_several_threads(lib):
+    """Calls of different shared-memory sizes, the first ones of their process, in 16 threads at once: all are
+    launched."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", _THREADS], cwd=root, capture_output=True, text=True, timeout=200)
+        assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ------------------------------------------------------------------ append and gather
 
 def _bf16_rows(n, W, seed, spread=2.0):
