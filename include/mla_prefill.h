@@ -748,9 +748,11 @@ mla_status_t mla_norm_rope(const mla_tensor_t* q_out, const mla_tensor_t* q, con
  *   E - 127 = max over j of e_j, held to -100 .. 125
  *   shift_j = E - 127 - e_j, held to 0 .. 14
  *   code_k  = e2m1(row_k / 2^(E - 127 - shift)), to nearest, ties to even, at most 6
- * (a negative value that rounds to 0 keeps its sign).  So a block holds its values to
- * within a sixth of the largest or better, unless the block is 2^14 below the
- * row's largest.  A row with a NaN or an infinity becomes E = 255 and zeros.
+ * (a negative value that rounds to 0 keeps its sign).  So a value is held to within
+ * a fifth of its block's largest (5 becomes 4) or, where that is more, in a block 2^14 below
+ * the row's largest or below 2^-100, to within a quarter of 2^(E - 127 - 14); in a block
+ * that goes past 7 * 2^125, to within a quarter of its largest.  A row of zeros has E = 27.
+ * A row with a NaN or an infinity becomes E = 255 and zeros.
  *   cache        device bytes [num_pages, P, mla_latent_fp4_row_bytes(W)] (written)
  *   rows         device bf16 [Tq, W], 16-byte aligned rows
  *   page_table   device uint32 [B, max_pages]

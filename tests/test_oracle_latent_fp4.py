@@ -37,6 +37,37 @@ def test_rows_are_near_and_exact_in_e4m3(spread):
     assert np.array_equal(decode_e4m3(codes) * scales[:, None].astype(np.float64), v)
 
 
+def test_how_far_values_are_held():
+    """Every mantissa of a block's largest value, with values of every mantissa and smaller exponents beside it, in
+    blocks up to 2^20 below the row's largest and in rows at both ends of the exponents."""
+    least = np.inf
+    for row_exp in (0, -90, -105, -115, 125, 127):
+        worst = 0.0
+        for block_exp in (0, 3, 13, 14, 15, 20):
+            x = np.zeros((128, 64))
+            m = 1 + np.arange(128) / 128
+            x[:, 0] = 1.75 * 2.0 ** row_exp                            # the row's largest, exact
+            x[:, 32] = m * 2.0 ** (row_exp - block_exp) if block_exp else np.minimum(m, 1.9921875) * 2.0 ** row_exp
+            for j in range(31):
+                x[:, 33 + j] = -m[(np.arange(128) * 5 + 37 * j) % 128] * 2.0 ** (row_exp - block_exp - j // 8)
+            x[:, 33:] = np.clip(x[:, 33:], -x[:, 32:33], 0)
+            x = np.clip(x, -3.3895e38, 3.3895e38)
+            if row_exp - block_exp < -126:
+                continue
+            x = _bf16(x).astype(np.float64)
+            raw = ora.encode(x)
+            v, top = ora.decode(raw, 64), 2.0 ** (raw[:, 32].astype(np.float64) - 127)
+            amax = np.abs(x[:, 32:]).max(axis=1)
+            past = amax > 7 * 2.0 ** 125
+            share = np.where(past, 0.25, 0.2)
+            err = np.abs(v - x)[:, 32:].max(axis=1)
+            assert (err <= np.maximum(share * amax, top * 2.0 ** -14 / 4)).all(), (row_exp, block_exp)
+            worst = max(worst, float((err / amax)[~past].max()) if (~past).any() else 0.0)
+        least = min(least, worst) if row_exp == 0 else least
+    assert least >= 0.2                                                  # a largest value of 5 becomes 4
+    assert ora.encode(np.zeros((1, 64)))[0, 32] == 27
+
+
 def test_special_rows():
     x = np.zeros((5, 64), dtype=np.float32)
     x[1, 3], x[2, 40] = np.nan, -np.inf
