@@ -682,10 +682,11 @@ mla_status_t mla_decode_latent(const mla_tensor_t* out, const mla_tensor_t* lse,
  * ---- The 4-bit latent cache, and what comes before it ----
  * (No counterpart on the reference pages.)  As the 8-bit serving step with half
  * the cache: mla_norm_rope of the queries' rope dims and of the new latent rows,
- * mla_append_latent_fp4, then mla_decode_latent_fp4 for new tokens or, for a
- * prompt over cached contexts, mla_gather_latent_fp4 to e4m3 rows with a scale
- * each, mla_matmul_fp8 with the up-projection weights and the prefill calls
- * with a contiguous K_rope.
+ * mla_append_latent_fp4, then mla_decode_latent_fp4 for new tokens.  For a prompt
+ * over cached contexts mla_gather_latent_fp4 to bf16 rows, mla_up_project of their
+ * first columns and a bf16 prefill call whose contiguous K_rope is their last 64; with
+ * 8-bit up-projection weights a second gather to e4m3 rows with a scale each, for
+ * mla_matmul_fp8 in mla_up_project's place (which writes bf16 too: K_rope stays bf16).
  *
  * A cached row of W elements (W a multiple of 64, up to 1024) is
  * mla_latent_fp4_row_bytes(W) bytes:
@@ -773,9 +774,9 @@ mla_status_t mla_append_latent_fp4(const mla_tensor_t* cache, const mla_tensor_t
  *          device e4m3 [rows, W] with one scale a row (scale_gran
  *          MLA_SCALE_PER_TOKEN, [rows] floats, written although the
  *          descriptor's pointer is const): codes e2m1 * 2^(6 - shift) and the scale
- *          2^(E - 133), exact; what mla_matmul_fp8 (column stride 0 of x_scales)
- *          and the fp8 prefill calls' contiguous K_rope take.  A row with E = 255
- *          gets NaN codes and a NaN scale.
+ *          2^(E - 133), exact; what mla_matmul_fp8 takes (column stride 0 of x_scales),
+ *          and the prefill calls as contiguous K_rope where q, k_nope and v are
+ *          fp8 as well.  A row with E = 255 gets NaN codes and a NaN scale.
  *          16-byte aligned rows; written for positions < min(rows,
  *          buffer_row_offsets[B]) only, from buffer_row_offsets[0] on
  *   cache  device bytes [num_pages, P, mla_latent_fp4_row_bytes(W)]

@@ -953,3 +953,82 @@ def test_decode_exponents_that_rise_and_fall(lib):
     d.q[3:] = 0
     out, lse = _run_decode(d)
     _check_decode(d, out, lse)
+
+
+# ------------------------------------------------------------------ prompts over cached rows
+
+def test_prefill_from_bf16_rows(lib):
+    """A prompt's chunk over rows kept in 4 bits, read back once in bf16: the 16-bit up-projection of their first 512
+    columns, K_rope as the tail of the same rows.  Each stage is checked on its own inputs."""
+    from mla_ragged_paged_gb300 import binding
+    B, H, P = 2, 4, 16
+    n, prior = [40, 25], [30, 100]
+    d = DecodeFp4(n, prior, H, P, seed=70)
+    L = [a + b for a, b in zip(n, prior)]
+    S = sum(L)
+    g = torch.Generator().manual_seed(71)
+    wk, wv = ((torch.randn(H * 128, LATENT, generator=g) / 16).to(torch.bfloat16).cuda() for _ in range(2))
+    ro, cl = (t.cuda() for t in d.offsets())
+    bro, co, _, _ = binding.plan(ro, cl, S, 1)
+    rows = torch.empty(S, WIDTH, dtype=torch.bfloat16, device="cuda")
+    binding.gather_latent_fp4(rows, d.raw.cuda(), d.table.cuda(), bro[0], co[0])
+    slots = torch.cat([d.table[b, torch.arange(L[b]) // P].long() * P + torch.arange(L[b]) % P for b in range(B)])
+    assert np.array_equal(_f64(rows), ora.decode(d.raw.view(-1, 304)[slots].numpy(), WIDTH))
+    k_nope = torch.empty(S, H, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k_nope)
+    for out, w in ((k_nope, wk), (v, wv)):
+        binding.up_project(out.view(S, -1), rows[:, :LATENT], w)
+        ref, mag = _f64(rows[:, :LATENT]) @ _f64(w).T, np.abs(_f64(rows[:, :LATENT])) @ np.abs(_f64(w)).T
+        _within(_f64(out.view(S, -1)), ref, 2.0 ** -8 * np.abs(ref) + 600 * 2.0 ** -23 * mag, "projection")
+    q = (torch.randn(sum(n), H, 192, generator=g) * 0.3).to(torch.bfloat16)
+    out = torch.empty(sum(n), H, 128, dtype=torch.bfloat16, device="cuda")
+    rope = rows[:, LATENT:]
+    binding.prefill_ragged_contiguous(out, q.cuda(), k_nope, v, rope, ro, cl, d.scale)
+    for b in range(B):
+        rows_b = slice(sum(L[:b]), sum(L[:b + 1]))
+        k = torch.cat([k_nope[rows_b].cpu(), rope[rows_b, None, :].cpu().expand(-1, H, -1)], 2).double()
+        qb = q[d.ro[b]:d.ro[b + 1]].double().transpose(0, 1)
+        allowed = torch.arange(L[b])[None] <= prior[b] + torch.arange(n[b])[:, None]
+        k, vb = k.transpose(0, 1), v[rows_b].cpu().double().transpose(0, 1)
+        p = torch.softmax((qb @ k.transpose(1, 2) * d.scale).masked_fill(~allowed, float("-inf")), dim=2)
+        # (The prefill's roundings: as above.)
+        move = 4 * 192 * 2.0 ** -23 * d.scale * (qb.abs() @ k.abs().transpose(1, 2)).amax(dim=2, keepdim=True)
+        ref = p @ vb
+        tol = (2.0 ** -7 + move) * (p @ vb.abs()) + 2.0 ** -8 * ref.abs()
+        got = out[d.ro[b]:d.ro[b + 1]].cpu().double().transpose(0, 1)
+        _within(got.numpy(), ref.numpy(), tol.numpy(), f"sequence {b}")
+
+
+def test_fp8_prefill_over_gathered_rows(lib):
+    """K_rope of an 8-bit prefill as rows kept in 4 bits and read back in e4m3 with a scale each: the rope columns of the
+    gathered rows, contiguous, beside 8-bit queries, K_nope and V.  (The 8-bit prefill's tolerance.)"""
+    import workloads
+    from mla_ragged_paged_gb300 import binding
+    from oracle import attention as oatt
+    from oracle.numerics import decode_e4m3
+    w = workloads.custom([140, 60], [10, 130], heads=2, page_size=16, seed=810, row_width=WIDTH, rope_col=LATENT, dtype="fp8")
+    shape = w.k_rope_pool.shape
+    rows = decode_e4m3(w.k_rope_pool.view(torch.uint8).numpy()) * w.k_rope_scales.numpy().astype(np.float64)[..., None]
+    rows[..., :LATENT] = np.random.default_rng(811).standard_normal(shape[:2] + (LATENT,))   # (NaN in the workload: not K_rope)
+    rows = torch.from_numpy(rows).to(torch.bfloat16).float().numpy().reshape(-1, WIDTH)
+    raw = torch.from_numpy(ora.encode(rows)).view(shape[0], shape[1], 304)
+    codes, scales = ora.to_e4m3(raw.numpy(), WIDTH)
+    w.k_rope_pool = torch.from_numpy(codes).view(w.k_rope_pool.dtype)
+    w.k_rope_scales = torch.from_numpy(scales)
+    d = workloads.device_inputs(w)
+    Sk = w.total_k
+    dst = torch.empty(Sk, WIDTH, dtype=torch.uint8, device="cuda")
+    dst_scales = torch.empty(Sk, device="cuda")
+    bro, co, _, _ = binding.plan(d["row_offsets"], d["cache_lens"], Sk, 1)
+    binding.gather_latent_fp4(dst, raw.cuda(), d["page_table"], bro[0], co[0], dst_scales=dst_scales)
+    want, want_scales = workloads.contiguous_rope(w)
+    assert torch.equal(dst.cpu(), want.view(torch.uint8)) and torch.equal(dst_scales.cpu(), want_scales)
+    out = torch.full((w.total_q, w.heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = binding.alloc_workspace(w.batch, fp8_pool_slots=Sk)
+    rope = dst.view(d["q"].dtype)[:, LATENT:]
+    binding.prefill_ragged_contiguous(out, d["q"], d["k_nope"], d["v"], rope, d["row_offsets"], d["cache_lens"], w.scale,
+                                      binding.MLA_MASK_CAUSAL, ws, q_scale=d["q_scale"], k_scale=d["k_scale"],
+                                      v_scale=d["v_scale"], k_rope_scales=dst_scales)
+    assert binding.device_status(ws) == 0
+    ref = oatt.reference(w)
+    _within(_f64(out), ref, 6e-2 + 6e-2 * np.abs(ref), "out")
