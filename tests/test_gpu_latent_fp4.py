@@ -955,6 +955,133 @@ def test_decode_exponents_that_rise_and_fall(lib):
     _check_decode(d, out, lse)
 
 
+# ------------------------------------------------------------------ layouts and sizes that take other paths
+
+@pytest.mark.parametrize("n,prior,heads,P,pad", [
+    *[([1] * 60, [1100] * 60, heads, P, pad) for heads, P, pad in ((16, 1, 0), (16, 7, 48), (32, 3, 16), (32, 5, 0), (40, 1, 32),
+                                                                   (40, 6, 0))],
+    *[([1, 3, 0, 2], [127, 128, 9, 1], 8, P, 16) for P in (2, 3, 9)]])
+def test_decode_row_gathers(lib, n, prior, heads, P, pad):
+    """Pages of no multiple of four tokens, which are read row by row: 16-, 32- and 64-row tiles, about four tiles
+    a CTA, so that the rings wrap; padded rows."""
+    d = DecodeFp4(n, prior, heads, P, seed=P)
+    cache = torch.full((d.raw.shape[0], P, 304 + pad), 0xFF, dtype=torch.uint8, device="cuda")[:, :, :304]
+    cache.copy_(d.raw.cuda())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = _run_decode(d, cache=cache, status=status)
+    assert int(status) == 0
+    _check_decode(d, out, lse)
+
+
+@pytest.mark.parametrize("pages,P,strides", [(1, 900, (16, 320, 1)), (1, 896, (0, 304, 1)), (900, 1, (352, 16, 1)),
+                                             (900, 1, (304, 0, 1)), (1, 1, (16, 0, 1))])
+def test_caches_of_one_page_or_one_slot_a_page(lib, pages, P, strides):
+    """The stride of a dimension of one element says nothing."""
+    from mla_ragged_paged_gb300 import binding
+    store = torch.full((900 * 352,), 0xFF, dtype=torch.uint8, device="cuda")
+    cache = store.as_strided((pages, P, 304), strides)
+    slots = pages * P
+    d = DecodeFp4([1], [slots - 1], 16, P, seed=P)
+    d.table = torch.randperm(pages, generator=torch.Generator().manual_seed(1))[None].to(torch.int32)
+    rows = _bf16_rows(slots, WIDTH, 3)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ro = torch.tensor([0, slots], dtype=torch.int32, device="cuda")
+    binding.append_latent_fp4(cache, rows.cuda(), d.table.cuda(), ro, zero)
+    raw = torch.from_numpy(ora.encode(rows.float().numpy()))
+    pos = torch.arange(slots)
+    d.raw = torch.zeros(pages, P, 304, dtype=torch.uint8)
+    d.raw[d.table[0, pos // P].long(), pos % P] = raw
+    assert torch.equal(cache.cpu(), d.raw)
+    assert int((store == 0xFF).sum()) >= store.numel() - slots * 304   # nothing but the rows is written
+    back = torch.empty(slots, WIDTH, dtype=torch.bfloat16, device="cuda")
+    binding.gather_latent_fp4(back, cache, d.table.cuda(), ro, zero)
+    assert np.array_equal(_f64(back), ora.decode(raw.numpy(), WIDTH))
+    out, lse = _run_decode(d, cache=cache)
+    _check_decode(d, out, lse)
+
+
+def _lengths(kind, rows, g):
+    """Sequence lengths that sum to `rows`: `long` ones, or `tiny` ones of 0 .. 3 with runs of 40 and 90 empty ones
+    among them (for 12 000 rows, then long ones)."""
+    out, left = [], rows
+    while left and kind == "tiny" and rows - left < 12000:
+        few = torch.randint(0, 4, (50,), generator=g).tolist() + [0] * (40 if len(out) % 3 else 90)
+        for n in few:
+            out.append(min(n, left))
+            left -= out[-1]
+    while left:
+        out.append(min(left, int(torch.randint(1, 1700, (1,), generator=g))))
+        left -= out[-1]
+    return out
+
+
+# A warp takes ceil(rows / (32 warps x SMs)) rows, 32 at most: 4864 and 155 648 rows on 152 SMs.
+@pytest.mark.parametrize("rows,W", [(5000, 576), (9800, 1024), (12000, 768), (14700, 512), (20000, 64), (100001, 64),
+                                    (200000, 64), (170003, 128)])
+@pytest.mark.parametrize("kind", ["long", "tiny"])
+def test_append_and_gather_many_rows(lib, rows, W, kind):
+    """Several rows a warp: two, an odd number, the most; sequences that end anywhere in a warp's rows, more
+    empty ones in a row than a warp has lanes, bad pages in their midst, rows outside the batch."""
+    from mla_ragged_paged_gb300 import binding
+    g = torch.Generator().manual_seed(rows + W)
+    P, first, behind = 16, 5, 3
+    new = _lengths(kind, rows - first - behind, g)
+    prior = torch.randint(0, 40, (len(new),), generator=g)
+    n = torch.tensor(new)
+    table, pages = page_table((n + prior).tolist(), P, g)
+    ro = first + torch.cat([torch.zeros(1, dtype=torch.int64), n.cumsum(0)])
+    b = torch.repeat_interleave(torch.arange(len(new)), n)
+    pos = prior[b] + torch.arange(len(b)) - (ro[b] - first)
+    good = table.clone()
+    for at in torch.randint(0, len(b), (40,), generator=g).tolist():
+        table[b[at], pos[at] // P] = pages + 7
+    ok = table[b, pos // P] < pages
+    slots = (good[b, pos // P].long() * P + pos % P)[ok]
+    x = _bf16_rows(rows, W, rows)
+    raw = torch.from_numpy(fast_encode(x[first:rows - behind].float().numpy()))[ok]
+    cache = torch.full((pages, P, ora.row_bytes(W)), 0xA5, dtype=torch.uint8, device="cuda")
+    want = torch.full((pages * P, ora.row_bytes(W)), 0xA5, dtype=torch.uint8)
+    want[slots] = raw
+    args = [t.to(torch.int32).cuda() for t in (table, ro, prior)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.append_latent_fp4(cache, x.cuda(), *args, status)
+    assert int(status) == 0x1
+    assert torch.equal(cache.cpu().view(-1, ora.row_bytes(W)), want)
+    mine = torch.zeros(rows, dtype=torch.bool)
+    mine[first:rows - behind] = ok
+    codes, scales = ora.to_e4m3(raw.numpy(), W)
+    back = torch.full((rows, W), 3.0, dtype=torch.bfloat16, device="cuda")
+    status.zero_()
+    binding.gather_latent_fp4(back, cache, *args, status=status)
+    assert int(status) == 0x1
+    assert np.array_equal(_f64(back[mine.cuda()]), ora.decode(raw.numpy(), W)) and (back[~mine.cuda()] == 3).all()
+    back8 = torch.full((rows, W), 9, dtype=torch.uint8, device="cuda")
+    back_s = torch.full((rows,), 5.0, device="cuda")
+    binding.gather_latent_fp4(back8, cache, *args, dst_scales=back_s, status=status)
+    assert np.array_equal(back8[mine.cuda()].cpu().numpy(), codes) and (back8[~mine.cuda()] == 9).all()
+    assert np.array_equal(back_s[mine.cuda()].cpu().numpy(), scales) and (back_s[~mine.cuda()] == 5).all()
+
+
+@pytest.mark.parametrize("heads,P", [(16, 64), (32, 64), (40, 7)])
+def test_decode_wait_timeout_in_every_row_tile(lib, heads, P):
+    """Copies that never come, in 16-, 32- and 64-row tiles, in boxes and row by row: the call ends, says so, and the
+    next one is right."""
+    from mla_ragged_paged_gb300 import binding
+    d = DecodeFp4([1] * 60, [1500] * 60, heads, P, seed=68)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    binding.test_inject_stall(True)
+    try:
+        _run_decode(d, status=status)
+        assert int(status) == 0x8
+    finally:
+        binding.test_inject_stall(False)
+    status.zero_()
+    d2 = DecodeFp4([1, 1], [700, 40], heads, P, seed=69)
+    out, lse = _run_decode(d2, status=status)
+    assert int(status) == 0
+    _check_decode(d2, out, lse)
+
+
 # ------------------------------------------------------------------ prompts over cached rows
 
 def test_prefill_from_bf16_rows(lib):
