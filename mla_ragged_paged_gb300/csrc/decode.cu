@@ -1138,7 +1138,10 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (FP4 && (smem_u32(smem_raw) & 1023u)) {  // (no room is left to round up)
-    if (threadIdx.x == 0 && p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+    if (threadIdx.x == 0) {
+      p.headers[blockIdx.x] = {0u, 0u, 0u, 0u};   // nothing to join
+      if (p.status) atomicOr(p.status, MLA_DEVICE_STATUS_TIMEOUT);
+    }
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
