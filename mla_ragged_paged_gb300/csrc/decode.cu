@@ -1039,7 +1039,7 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
 }
 
 // ------------------------------------------------------------ 4-bit rows to codes
-// A warp takes 8 or 16 keys of a tile.  Of a chunk (128 dims, four blocks of 16 bytes,
+// A warp takes 16 keys of a tile.  Of a chunk (128 dims, four blocks of 16 bytes,
 // which become 32) lane l takes block l % 4 of a key, and of another 8 further.  Four lanes'
 // key is k of the warp's, the next four's k ^ 5: in 128-byte swizzled rows eight lanes'
 // loads of 16 bytes (columns 0 .. 3 or 4 .. 7) then fall into different banks, and so do
@@ -1048,13 +1048,12 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
 template <int NR>
 __device__ void make_codes(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, uint32_t w, uint32_t lane, volatile uint32_t* abort) {
   using R = Rows<NR, true>;
-  constexpr int kEach = kKeys / 8 / R::kCodeWarps;                           // keys of a lane
-  const uint32_t j = lane & 3u, k7 = (lane >> 3) ^ (lane & 4u ? 5u : 0u), near = w * 8 * kEach + k7;   // and 8 further
+  static_assert(kKeys == 16 * R::kCodeWarps, "two keys of a lane");
+  const uint32_t j = lane & 3u, k7 = (lane >> 3) ^ (lane & 4u ? 5u : 0u), near = w * 16 + k7;   // and 8 further
   const uint32_t from = near * 128 + ((j ^ k7) << 4);                        // of a half's first chunk; the other's is ^ 64
   const uint32_t to = near * 128 + (((2 * j) ^ k7) << 4);                    // the block's first half; the second's is ^ 16
-  // Rope dims: a block of one of two keys, or half a block of the one.
-  const uint32_t rope_key = near + (kEach == 2 ? 8 * (j >> 1) : 0), rope_col = kEach == 2 ? 2 * (j & 1u) : j;
-  const uint32_t rope_to = rope_key * 64 + ((rope_col ^ ((rope_key >> 1) & 3u)) << 4);
+  // Rope dims: a block of one of the two keys.
+  const uint32_t rope_key = near + 8 * (j >> 1), rope_to = rope_key * 64 + (((2 * (j & 1u)) ^ ((rope_key >> 1) & 3u)) << 4);
   auto wait = [&](uint64_t& bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1u, abort)); };
   auto arrive = [&](uint64_t& bar) {
     __syncwarp();
@@ -1068,38 +1067,32 @@ __device__ void make_codes(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, 
   uint32_t tile = 0;
   Segment g;
   while (next_segment<NR>(p, sh, g)) {
-    KeyWalk walk(p, g.kt0 * kKeys + near + (kEach == 2 ? 8 * (j & 1u) : 0));   // the first lanes of four: whether there is such a key
+    KeyWalk walk(p, g.kt0 * kKeys + near + 8 * (j & 1u));   // the first two lanes of four: whether there is such a key
     for (uint32_t kt = g.kt0; kt < g.kt1; ++kt, ++tile) {
-      const uint32_t page = j < kEach ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
+      const uint32_t page = j < 2 ? walk.page(p, g.b, kt * kKeys + near + 8 * j < g.s.keys) : 0u;
       walk.next(p);
       const uint32_t rs = tile % R::kRopeSlots;
       if (!wait(s.tail_full[rs], tile / R::kRopeSlots)) return;
       const uint8_t* tail = s.rope[rs] + near * 64;
-      uint4 meta[kEach], rope;
+      uint4 meta[2];
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) meta[k] = *reinterpret_cast<const uint4*>(tail + k * 8 * 64 + kRope / 2);
-      if constexpr (kEach == 2) {
-        rope = *reinterpret_cast<const uint4*>(tail + (j >> 1) * 8 * 64 + (j & 1u) * 16);
-      } else {
-        const uint2 half = *reinterpret_cast<const uint2*>(tail + j * 8);
-        rope = make_uint4(half.x, half.y, 0u, 0u);
-      }
+      for (int k = 0; k < 2; ++k) meta[k] = *reinterpret_cast<const uint4*>(tail + k * 8 * 64 + kRope / 2);
+      const uint4 rope = *reinterpret_cast<const uint4*>(tail + (j >> 1) * 8 * 64 + (j & 1u) * 16);
       // Block l % 4's shifts in all chunks: bytes 1 .. 8 behind the exponent, two blocks each.
       const uint32_t by = 8 + 4 * j;
-      uint32_t lo[kEach], hi[kEach];
+      uint32_t lo[2], hi[2];
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {
+      for (int k = 0; k < 2; ++k) {
         lo[k] = __funnelshift_r(meta[k].x, meta[k].y, by);
         hi[k] = __funnelshift_r(meta[k].y, meta[k].z, by);
       }
-      const uint32_t e = (kEach == 2 && (j & 1u) ? meta[kEach - 1].x : meta[0].x) & 255u;
-      const uint32_t rope_shift = kEach == 2 ? (j >> 1 ? meta[kEach - 1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u
-                                             : meta[0].z >> (8 + 4 * (j >> 1)) & 15u;
+      const uint32_t e = (j & 1u ? meta[1].x : meta[0].x) & 255u;
+      const uint32_t rope_shift = (j >> 1 ? meta[1].z : meta[0].z) >> (8 + 4 * (j & 1u)) & 15u;
       __syncwarp();                                         // read by all lanes, then written
       {
         const uint2 t = s.table[rope_shift];
         convert(rope.x, rope.y, t, s.rope[rs] + rope_to);
-        if constexpr (kEach == 2) convert(rope.z, rope.w, t, s.rope[rs] + (rope_to ^ 16u));
+        convert(rope.z, rope.w, t, s.rope[rs] + (rope_to ^ 16u));
       }
       arrive(s.rope_full[rs]);
 #pragma unroll
@@ -1107,19 +1100,19 @@ __device__ void make_codes(DecodeSmem4<NR>& s, const DecodeParams& p, Share sh, 
         const uint32_t pos = tile * 2 + h, hs = pos % R::kHalves;
         if (!wait(s.raw_full[hs], pos / R::kHalves)) return;
         uint8_t* base = s.chunk[2 * hs];
-        uint4 v[2][kEach];
+        uint4 v[2][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int k = 0; k < kEach; ++k) v[c][k] = *reinterpret_cast<const uint4*>(base + kChunk + (from ^ (c ? 64u : 0u)) + k * 8 * 128);
+          for (int k = 0; k < 2; ++k) v[c][k] = *reinterpret_cast<const uint4*>(base + kChunk + (from ^ (c ? 64u : 0u)) + k * 8 * 128);
         __syncwarp();
         // (The ring has room for this tile: whoever read the exponent's slot before is done.)
-        if (h == 0 && j < kEach)
+        if (h == 0 && j < 2)
           s.key_e[tile % DecodeSmem4<NR>::kExponents][near + 8 * j] = static_cast<uint8_t>(page < p.num_pages ? e : kNoKey);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int k = 0; k < kEach; ++k) {
+          for (int k = 0; k < 2; ++k) {
             const uint2 t = s.table[(h ? hi[k] : lo[k]) >> (16 * c) & 15u];
             convert(v[c][k].x, v[c][k].y, t, base + c * kChunk + to + k * 8 * 128);
             convert(v[c][k].z, v[c][k].w, t, base + c * kChunk + (to ^ 16u) + k * 8 * 128);
@@ -1272,12 +1265,11 @@ __global__ void __launch_bounds__(Rows<NR, FP4>::kThreads, 1) decode_kernel(cons
   } else if (!FP4 || warp < 4 + kSoftmaxWarps) {
     if constexpr (!FP4) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     else if constexpr (kThreads == 640) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    else if constexpr (NR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     decode_softmax<NR, FP4>(s, p, sh, steps, ctas, tmem, (warp - 4) >> 2, warp & 3, lane, abort);
   } else if constexpr (FP4) {
     if constexpr (kThreads == 640) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    else if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     make_codes<NR>(s, p, sh, warp - 4 - kSoftmaxWarps, lane, abort);
   }
   tc_fence_before();
