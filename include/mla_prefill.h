@@ -665,9 +665,9 @@ size_t mla_decode_latent_workspace_size(void);
  * same small weight can together be off by n * 2^-18 of the largest key's part, and
  * those below 2^-21 of it may drop out of the output.  The sum that normalises
  * the output counts every key; lse is of unrounded weights.  A
- * query's elements are taken exactly down to 2^-9 of its largest one, smaller
- * ones to 2^-17 of that: next to an element 2^10 times larger they keep seven
- * bits, next to one 2^14 times larger three.
+ * query's elements are taken exactly down to 2^-9 of its largest one (or of 2^-113,
+ * if that is larger), smaller ones to 2^-17 of that: next to an element 2^10 times
+ * larger they keep seven bits, next to one 2^14 times larger three.
  * Slots past a sequence's context may hold anything.  A query all of whose
  * keys are masked gets 0 and lse -inf.  Rows outside [row_offsets[0],
  * row_offsets[B]) are not written.
@@ -730,8 +730,9 @@ size_t mla_latent_fp4_row_bytes(uint32_t width);
  * angle's part beyond whole turns is exact to 2^-24 of a turn at any position, for
  * inv_freq as given and up to 256 in magnitude (an infinity or NaN gives NaNs).  A row
  * whose sum of squares exceeds float32 gives zeros in [0, Dn).
- * Inputs may have any strides, outputs any under which no two of their elements share memory; rows
- * that all start 16-byte aligned, with D, Dn and R multiples of 8 (16 for R with
+ * Columns lie next to each other (stride 1); tokens and heads of inputs may have any
+ * strides >= 0, those of outputs any under which no two rows share memory; rows that
+ * all start 16-byte aligned, with D, Dn and R multiples of 8 (16 for R with
  * MLA_ROPE_HALVES), take wide accesses.  An output may be the same view as its
  * input (in place).  One launch.
  */
