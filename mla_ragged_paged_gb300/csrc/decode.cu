@@ -10,7 +10,7 @@
 // flops per query: up to about 60 queries a sequence the kernel is bound by
 // HBM, above that by the tensor cores and their shared-memory operands.  Measured:
 // 4 sequences of 131072 with 32 queries each 73 us (4.2 TB/s; 6.3 in the steady
-// state, 17 us of start, segment ends and joining); 64 of 4500 with 128 queries 104 us
+// state, 17 us of start, segment ends and joining); 64 of 4500 with 128 queries 107 us
 // (4 k cycles a tile of 64 queries, 2.7 k of them tensor-core work: shared memory has
 // room for two key tiles and one tile of weights, so load, scores, softmax and output
 // wait for one another).
@@ -21,8 +21,8 @@
 // scale's place, and all that follows is the same.  Half the bytes and no fewer UMMAs, and
 // a tile's 73 728 codes on top: a table in two words per shift and byte permutations, 9
 // instructions for 8 codes, 2.6 k of the 10.9 k (32-row tiles) or 17.6 k (64-row) that a
-// tile takes.  Measured: 64 sequences of 4500 with 16 heads 50 us (8-bit 52), with 128
-// heads 129 us (104), 4 of 131072 with 32 queries 83 us (73).  A tile takes 4.7 k cycles
+// tile takes.  Measured (in graphs): 64 sequences of 4500 with 16 heads 50 us (8-bit 51), with 128
+// heads 130 us (107), 4 of 131072 with 32 queries 85 us (73).  A tile takes 4.7 k cycles
 // (32 rows) or 6.5 k (64): codes 3 to 4 k, softmax 3.3 or 5 k, UMMAs 2.1 or 2.7 k, one
 // behind the other for a tile and beside one another for neighbours, as far as a ring of
 // 2 to 2.5 tiles lets them; without any one of them the time falls by 4 to 11 %.  Kept out:
@@ -102,7 +102,7 @@ constexpr float kMargin = 2.f;                // in both cases to that far above
 constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
 // The sum is kept as sum 2^(x - mu - kSumShift + up): each weight, at most 2^8.5, times 2^(up - 37) / s_j.
-// With M the largest scale's exponent in a segment's first key tile, up = M + 21 (0 below), so that for
+// With M the largest scale's exponent in a segment's first key tile, up = M + 21 (0 below, or if no key there has one), so that for
 // scales within 2^110 of each other the factor lies between 2^-126 and 2^94, and neither end leaves
 // fp32.  (Always 2^-37 / s_j, it vanished for scales from 2^89 on, and with it the output.)
 constexpr float kSumShift = 30.f;
