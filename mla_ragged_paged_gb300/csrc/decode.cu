@@ -102,11 +102,13 @@ constexpr float kMargin = 2.f;                // in both cases to that far above
 constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
 constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
 // The sum is kept as sum 2^(x - mu - kSumShift + up): each weight, at most 2^8.5, times 2^(up - 37) / s_j.
-// With M the largest scale's exponent in a segment's first key tile, up = M + 21 (0 below, or if no key there has one), so that for
-// scales within 2^110 of each other the factor lies between 2^-126 and 2^94, and neither end leaves
-// fp32.  (Always 2^-37 / s_j, it vanished for scales from 2^89 on, and with it the output.)
+// With M the largest scale's exponent in a segment's first key tile, up = M + 21, from 0 (also
+// where no key has one) to 40: for scales within 2^110 of each other the factor lies between 2^-126
+// and 2^94, and neither end leaves fp32.  (Always 2^-37 / s_j, it vanished for scales from 2^89 on,
+// and with it the output.)  At 40 it suits every scale up to 2^128, and stays finite for rows of
+// zeros, whose scales lie further below.
 constexpr float kSumShift = 30.f;
-constexpr float kSumRoom = 21.f;
+constexpr float kSumRoom = 21.f, kMostUp = 40.f;
 // Steps that beginning a row tile counts for: its queries, pipeline fill and result take as
 // long as about four key tiles.
 constexpr uint32_t kStartSteps = 4;
@@ -732,7 +734,7 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
       uint32_t e = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) e = max(e, s.warp_scale[group][i]);
-      up = fmaxf(static_cast<float>(min(e, 255u)) - (128.f - kSumRoom), 0.f);
+      up = fminf(fmaxf(static_cast<float>(e) - (128.f - kSumRoom), 0.f), kMostUp);
     }
     float mu = -INFINITY, peak = -INFINITY;              // of row r0 + my_row
     uint32_t look = g.kt0 + 2;                           // form the maxima in all tiles before this one
@@ -1347,7 +1349,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
     if (li != 0.f) {
       const float f = exp2f(mi - m);
       if (ui != up) {
-        const float to_up = whole_power(fminf(up - ui, 127.f));
+        const float to_up = whole_power(up - ui);
         li *= to_up;
         qi *= to_up;
       }

@@ -940,6 +940,20 @@ def test_decode_rows_of_every_exponent(lib, n, prior, heads, lo, hi, q_std):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("lo,hi,q_std", [(150, 154, 2.0 ** -20), (178, 182, 2.0 ** -48), (230, 232, 2.0 ** -98)])
+@pytest.mark.parametrize("n,prior", [([1, 2], [1500, 300]), ([1], [9000])])
+def test_decode_rows_of_zeros_beside_large_ones(lib, n, prior, lo, hi, q_std):
+    """Rows of zeros (E = 27) more than 110 below the others, which have all the weight: no weight of theirs becomes an
+    infinity or a NaN."""
+    d = DecodeFp4(n, prior, 16, 64, seed=lo, q_std=q_std)
+    _set_exponents(d, lo, hi, hi)
+    pick = torch.rand(d.raw.shape[:2], generator=torch.Generator().manual_seed(lo)) < 0.5
+    zero = torch.from_numpy(ora.encode(np.zeros((1, WIDTH))))[0]
+    d.raw[pick & (d.raw[..., WIDTH // 2] != 255)] = zero
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
 def test_decode_exponents_that_rise_and_fall(lib):
     """The largest rows first, last and in the middle of a sequence, for one token alone and beside
     keys that no row sees."""
