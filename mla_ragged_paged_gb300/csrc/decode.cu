@@ -100,7 +100,8 @@ constexpr float kRaise = 1.5f;                // mu rises when a key is that far
 constexpr float kDrop = 12.f;                 // and falls when a tile's maximum is that far below it,
 constexpr float kMargin = 2.f;                // in both cases to that far above the maximum
 constexpr uint32_t kLook = 8;                 // the maxima are formed in every kLook-th tile
-constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far
+constexpr float kDepth = 60.f;                // mu stays within 2^60 of the largest maximum so far,
+constexpr float kFloor = -126.f;              // and does not fall below this + up
 // The sum is kept as sum 2^(x - mu - kSumShift + up): each weight, at most 2^8.5, times 2^(up - 37) / s_j.
 // With M the largest scale's exponent in a segment's first key tile, up = M + 21, from 0 (also
 // where no key has one) to 40: for scales within 2^110 of each other the factor lies between 2^-126
@@ -829,7 +830,9 @@ __device__ void decode_softmax(DecodeSmem<NR, FP4>& s, const DecodeParams& p, Sh
                                fmaxf(s.warp_red[group][2][my_row], s.warp_red[group][3][my_row]));
         // Whole numbers, so that rescaling multiplies by powers of two and rounds nothing.
         float next = mu;
-        if (tm > mu + kRaise || (tm < mu - kDrop && tm > -INFINITY)) next = fmaxf(rintf(tm) + kMargin, peak - kDepth);
+        // (Where it falls the sum rises; a row of zeros, x = 0, has 2^96 in it at the floor.)
+        if (tm > mu + kRaise || (tm < mu - kDrop && tm > -INFINITY))
+          next = fmaxf(rintf(tm) + kMargin, fmaxf(peak - kDepth, tm < mu ? fminf(mu, up + kFloor) : -INFINITY));
         peak = fmaxf(peak, next);
         factor =
             mu == next ? 1.f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(fmaxf(mu - next, -127.f))) << 23);

@@ -954,6 +954,22 @@ def test_decode_rows_of_zeros_beside_large_ones(lib, n, prior, lo, hi, q_std):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("nats", [40.0, 80.0, 95.0, 105.0, 140.0, 1000.0])
+@pytest.mark.parametrize("zeros,others", [(100, 500), (3, 300)])
+def test_decode_rows_of_zeros_far_above_the_others(lib, zeros, others, nats):
+    """Rows of zeros first, then rows whose scores are far below theirs, 200 sequences of the same pages, so that CTAs
+    take whole ones: the sum of the weights stays in fp32 when the others' maxima are followed downwards."""
+    n = zeros + others
+    d = DecodeFp4([1], [n - 1], 4, 64, seed=zeros)
+    x = -torch.ones(n, WIDTH)
+    x[:zeros] = 0
+    d.put(0, x)
+    d.n, d.prior, d.ro = [1] * 200, [n - 1] * 200, np.arange(201)
+    d.table, d.q = d.table.repeat(200, 1), torch.full((200, 4, WIDTH), nats / (WIDTH * d.scale)).to(torch.bfloat16)
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
 def test_decode_exponents_that_rise_and_fall(lib):
     """The largest rows first, last and in the middle of a sequence, for one token alone and beside
     keys that no row sees."""

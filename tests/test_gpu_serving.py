@@ -518,6 +518,25 @@ def test_decode_scales_of_every_size(lib, n, prior, lo, hi, q_std):
     _check_decode(d, out, lse)
 
 
+@pytest.mark.parametrize("nats", [40.0, 80.0, 95.0, 105.0, 140.0, 1000.0])
+@pytest.mark.parametrize("zeros,others", [(100, 500), (3, 300)])
+def test_decode_rows_of_zeros_far_above_the_others(lib, zeros, others, nats):
+    """Rows of zeros first, then rows whose scores are far below theirs, 200 sequences of the same pages, so that CTAs
+    take whole ones: the sum of the weights stays in fp32 when the others' maxima are followed downwards."""
+    n = zeros + others
+    d = Decode([1], [n - 1], 4, 64, seed=zeros)
+    x = -torch.ones(n, WIDTH)
+    x[:zeros] = 0
+    c, s = quantise_rows(x)
+    pos = torch.arange(n)
+    d.codes[d.table[0, pos // 64].long(), pos % 64] = c
+    d.scales[d.table[0, pos // 64].long(), pos % 64] = s
+    d.n, d.prior, d.ro = [1] * 200, [n - 1] * 200, np.arange(201)
+    d.table, d.q = d.table.repeat(200, 1), torch.full((200, 4, WIDTH), nats / (WIDTH * d.scale)).to(torch.bfloat16)
+    out, lse = _run_decode(d)
+    _check_decode(d, out, lse)
+
+
 @pytest.mark.parametrize("q_std", [0.0, 1.0])
 @pytest.mark.parametrize("lengths,zeros", [
     ([2], "late"), ([2], "early"), ([300], "early"), ([300], "late"), ([300], "odd"), ([5000], "odd"), ([5000], "early"),
